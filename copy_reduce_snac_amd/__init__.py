@@ -1,5 +1,6 @@
 """Python binding of libsnac.so, the C-ABI copy / N-to-1 reduce collective
-library for MI355X (declared in include/snac.h).
+library for MI355X (declared in include/snac.h), and of the operators beside
+the collectives (include/snac_ops.h).
 
 Argument marshalling only: every function here has the name of the C entry
 point it calls and does nothing but convert Python arguments (ints, torch
@@ -113,10 +114,25 @@ class snac_coll_desc(ctypes.Structure):
     ]
 
 
+class snac_router(ctypes.Structure):
+    _fields_ = [
+        ("experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renorm", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
+_I64 = ctypes.c_int64
+_F = ctypes.c_float
 
 # name -> (restype, argtypes)
 _SIGS = {
@@ -150,6 +166,21 @@ _SIGS = {
     "snac_tuning_lookup": (_I, [ctypes.c_int32, _I, _I, _SZ, ctypes.POINTER(snac_tuning)]),
     "snac_get_tuning": (_I, [ctypes.POINTER(snac_tuning)]),
     "snac_set_tuning": (_I, [ctypes.POINTER(snac_tuning)]),
+    "snac_route": (_I, [ctypes.POINTER(snac_router), _VP, _SZ, _VP, _SZ, _I, _VP, _VP, _VP]),
+    "snac_route_backward": (_I, [ctypes.POINTER(snac_router), _VP, _SZ, _VP, _VP, _SZ, _I, _VP, _SZ, _VP]),
+    "snac_dispatch_plan": (_I, [_VP, _VP, _I, _SZ, _I, _VP, _VP, _VP, _VP]),
+    "snac_dispatch": (_I, [_VP, _SZ, _VP, _SZ, _I, _SZ, _I, _VP, _SZ, _SZ, _VP]),
+    "snac_combine": (_I, [_VP, _SZ, _SZ, _VP, _VP, _SZ, _I, _SZ, _I, _VP, _SZ, _VP]),
+    "snac_combine_backward": (_I, [_VP, _SZ, _VP, _SZ, _SZ, _VP, _VP, _SZ, _I, _SZ, _I, _VP, _SZ, _VP, _VP]),
+    "snac_embedding": (_I, [_VP, _SZ, _SZ, _I64, _VP, _I, _SZ, _SZ, _F, _I, _VP, _SZ, _VP]),
+    "snac_embedding_scratch": (_SZ, [_SZ, _SZ, _SZ]),
+    "snac_embedding_backward": (_I, [_VP, _VP, _SZ, _I, _VP, _I, _SZ, _I64, _SZ, _I64, _SZ, _F, _VP, _SZ, _I, _I, _VP]),
+    "snac_grads_init": (_I, [ctypes.POINTER(_VP), ctypes.POINTER(_VP), ctypes.POINTER(_SZ),
+                             ctypes.POINTER(ctypes.c_int32), _SZ, _VP, ctypes.POINTER(_VP)]),
+    "snac_grads_finalize": (_I, [_VP, _VP]),
+    "snac_grad_norm": (_I, [_VP, _VP, _VP]),
+    "snac_clip_grads": (_I, [_VP, _VP, _F, _VP]),
+    "snac_clip_grad_norm": (_I, [_VP, _F, _VP, _VP]),
 }
 
 
@@ -453,3 +484,99 @@ def snac_tuning_lookup(coll: int, nranks: int, esize: int, nbytes: int) -> dict:
     t = snac_tuning()
     _check(lib().snac_tuning_lookup(coll, nranks, esize, nbytes, ctypes.byref(t)), "snac_tuning_lookup")
     return {name: getattr(t, name) for name, _ in snac_tuning._fields_}
+
+
+# ------------------------------------------- operators beside the collectives
+SNAC_SCORE_SOFTMAX, SNAC_SCORE_SIGMOID = 0, 1
+_SCORES = {"softmax": SNAC_SCORE_SOFTMAX, "sigmoid": SNAC_SCORE_SIGMOID}
+SNAC_MAX_EXPERTS, SNAC_MAX_TOPK, SNAC_MAX_IDS = 1024, 32, 1 << 24
+
+
+def router(experts: int, topk: int, score="softmax", groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+           renorm: bool = True, scale: float = 1.0) -> snac_router:
+    """A snac_router; ``score`` is "softmax", "sigmoid" or a SNAC_SCORE_* value."""
+    sc = _SCORES[score] if isinstance(score, str) else int(score)
+    return snac_router(experts, topk, groups, topk_groups, group_top, sc, int(renorm), scale)
+
+
+def snac_route(r: snac_router, logits, ld: int, bias, tokens: int, dtype, weights, ids, stream=None) -> None:
+    _check(lib().snac_route(r, _ptr(logits), ld, _ptr(bias), tokens, _dtype(dtype), _ptr(weights), _ptr(ids),
+                            _stream(stream)), "snac_route")
+
+
+def snac_route_backward(r: snac_router, logits, ld: int, ids, dweights, tokens: int, dtype, dlogits, ld_d: int,
+                        stream=None) -> None:
+    _check(lib().snac_route_backward(r, _ptr(logits), ld, _ptr(ids), _ptr(dweights), tokens, _dtype(dtype),
+                                     _ptr(dlogits), ld_d, _stream(stream)), "snac_route_backward")
+
+
+def snac_dispatch_plan(ctx, ids, id_bytes: int, slots: int, experts: int, counts, row_of_slot, slot_of_row,
+                       stream=None) -> None:
+    _check(lib().snac_dispatch_plan(ctx, _ptr(ids), id_bytes, slots, experts, _ptr(counts), _ptr(row_of_slot),
+                                    _ptr(slot_of_row), _stream(stream)), "snac_dispatch_plan")
+
+
+def snac_dispatch(x, ld_x: int, row_of_slot, tokens: int, topk: int, width: int, dtype, out, ld_out: int, rows: int,
+                  stream=None) -> None:
+    _check(lib().snac_dispatch(_ptr(x), ld_x, _ptr(row_of_slot), tokens, topk, width, _dtype(dtype), _ptr(out), ld_out,
+                               rows, _stream(stream)), "snac_dispatch")
+
+
+def snac_combine(y, ld_y: int, rows: int, row_of_slot, weights, tokens: int, topk: int, width: int, dtype, out,
+                 ld_out: int, stream=None) -> None:
+    _check(lib().snac_combine(_ptr(y), ld_y, rows, _ptr(row_of_slot), _ptr(weights), tokens, topk, width, _dtype(dtype),
+                              _ptr(out), ld_out, _stream(stream)), "snac_combine")
+
+
+def snac_combine_backward(dout, ld_dout: int, y, ld_y: int, rows: int, row_of_slot, weights, tokens: int, topk: int,
+                          width: int, dtype, dy, ld_dy: int, dweights, stream=None) -> None:
+    _check(lib().snac_combine_backward(_ptr(dout), ld_dout, _ptr(y), ld_y, rows, _ptr(row_of_slot), _ptr(weights), tokens,
+                                       topk, width, _dtype(dtype), _ptr(dy), ld_dy, _ptr(dweights), _stream(stream)),
+           "snac_combine_backward")
+
+
+def snac_embedding(table, ld_table: int, vocab: int, first: int, ids, id_bytes: int, tokens: int, width: int,
+                   scale: float, dtype, out, ld_out: int, stream=None) -> None:
+    _check(lib().snac_embedding(_ptr(table), ld_table, vocab, first, _ptr(ids), id_bytes, tokens, width, scale,
+                                _dtype(dtype), _ptr(out), ld_out, _stream(stream)), "snac_embedding")
+
+
+def snac_embedding_scratch(tokens: int, vocab: int, width: int) -> int:
+    return lib().snac_embedding_scratch(tokens, vocab, width)
+
+
+def snac_embedding_backward(ctx, dout, ld_dout: int, dtype, ids, id_bytes: int, tokens: int, first: int, vocab: int,
+                            pad_id: int, width: int, scale: float, dtable, ld_dtable: int, grad_dtype,
+                            accumulate: int = 0, stream=None) -> None:
+    _check(lib().snac_embedding_backward(ctx, _ptr(dout), ld_dout, _dtype(dtype), _ptr(ids), id_bytes, tokens, first,
+                                         vocab, pad_id, width, scale, _ptr(dtable), ld_dtable, _dtype(grad_dtype),
+                                         accumulate, _stream(stream)), "snac_embedding_backward")
+
+
+def snac_grads_init(srcs: Sequence, dsts: Sequence | None, counts: Sequence[int], dtypes: Sequence, stream=None) -> int:
+    srcs, counts = list(srcs), [int(c) for c in counts]
+    types = [_dtype(t) for t in dtypes]
+    dsts = None if dsts is None else list(dsts)
+    if len(counts) != len(srcs) or len(types) != len(srcs) or (dsts is not None and len(dsts) != len(srcs)):
+        raise ValueError("snac_grads_init: lists of different lengths")
+    out = _VP()
+    _check(lib().snac_grads_init(_ptrs(srcs), None if dsts is None else _ptrs(dsts), _sizes(counts),
+                                 (ctypes.c_int32 * max(1, len(types)))(*types), len(srcs), _stream(stream),
+                                 ctypes.byref(out)), "snac_grads_init")
+    return out.value
+
+
+def snac_grads_finalize(grads, stream=None) -> None:
+    _check(lib().snac_grads_finalize(grads, _stream(stream)), "snac_grads_finalize")
+
+
+def snac_grad_norm(grads, norm, stream=None) -> None:
+    _check(lib().snac_grad_norm(grads, _ptr(norm), _stream(stream)), "snac_grad_norm")
+
+
+def snac_clip_grads(grads, norm, max_norm: float, stream=None) -> None:
+    _check(lib().snac_clip_grads(grads, _ptr(norm), max_norm, _stream(stream)), "snac_clip_grads")
+
+
+def snac_clip_grad_norm(grads, max_norm: float, norm, stream=None) -> None:
+    _check(lib().snac_clip_grad_norm(grads, max_norm, _ptr(norm), _stream(stream)), "snac_clip_grad_norm")

@@ -16,6 +16,7 @@
 #include <string>
 
 #include "internal.hpp"
+#include "ops.hpp"
 #include "snac.h"
 #include "snac_layout.hpp"
 
@@ -42,8 +43,10 @@ struct snac_ctx {
 };
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace snac {
 
 snac_status fail(snac_status s, const char* fmt, ...) {
   char buf[512];
@@ -63,6 +66,10 @@ snac_status ok() {
 snac_status hip_fail(hipError_t e, const char* what) {
   return fail(SNAC_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace snac
+
+namespace {
 
 // Process-wide tuning, initialised from the environment when the library
 // loads: SNAC_WGS_PER_CU, SNAC_CACHE_POLICY, SNAC_PIPELINE_TILE_BYTES,
@@ -492,6 +499,21 @@ snac_status v_collective(int32_t coll, snac_ctx* ctx, const void* const* src, vo
 }
 
 }  // namespace
+
+namespace snac {
+
+snac_status ctx_scratch(snac_ctx* ctx, uint64_t bytes, const char* what, char** out) {
+  const snac_status st = check_ctx(ctx);
+  if (st != SNAC_OK) return st;
+  const uint64_t have = (uint64_t)ctx->nranks * ctx->staging_bytes;
+  if (bytes > have)
+    return fail(SNAC_E_ARG, "%s needs %llu bytes of scratch, the context's staging rings hold %llu", what,
+                (unsigned long long)bytes, (unsigned long long)have);
+  *out = ctx->staging;
+  return SNAC_OK;
+}
+
+}  // namespace snac
 
 extern "C" {
 

@@ -1,0 +1,160 @@
+// rows.hpp -- device helpers of the operators' kernels: rows of bf16 or
+// binary32 elements in 16-byte units at any element alignment, and
+// reductions over a 64-lane wave in a fixed order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "snac_device.hpp"
+
+namespace snac {
+
+// 16 bytes at any element alignment: one dwordx4 access (global accesses of
+// gfx950 need no alignment; aligned ones touch fewer lines)
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+// Elements of a 16-byte unit
+template <typename T>
+constexpr uint32_t kUnit = 16 / T::kSize;
+
+template <typename T>
+__device__ __forceinline__ void unpack(const u32x4& w, float (&f)[kUnit<T>]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if constexpr (T::kSize == 4) {
+      f[c] = __uint_as_float(w[c]);
+    } else {
+      f[2 * c] = bf16_lo(w[c]);
+      f[2 * c + 1] = bf16_hi(w[c]);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 pack(const float (&f)[kUnit<T>]) {
+  u32x4 w;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if constexpr (T::kSize == 4)
+      w[c] = __float_as_uint(f[c]);
+    else
+      w[c] = pack_bf16(f[2 * c], f[2 * c + 1]);
+  }
+  return w;
+}
+
+template <bool NT>
+__device__ __forceinline__ u32x4 ld_unit(const char* p) {
+  if constexpr (NT)
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+  else
+    return *reinterpret_cast<const u32x4_a2*>(p);
+}
+template <bool NT>
+__device__ __forceinline__ void st_unit(char* p, u32x4 v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
+  else
+    *reinterpret_cast<u32x4_a2*>(p) = v;
+}
+
+// The first `n` (0 < n < a unit) elements of a row's last unit; the others
+// read as 0.
+template <typename T>
+__device__ __forceinline__ u32x4 ld_part(const char* p, uint32_t n) {
+  u32x4 v = {0, 0, 0, 0};
+  if constexpr (T::kSize == 4) {
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i)
+      if (i < n) v[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+  } else {
+#pragma unroll
+    for (uint32_t i = 0; i < 7; ++i)
+      if (i < n) v[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(p + 2 * i) << (16 * (i & 1));
+  }
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void st_part(char* p, u32x4 v, uint32_t n) {
+  if constexpr (T::kSize == 4) {
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i)
+      if (i < n) *reinterpret_cast<uint32_t*>(p + 4 * i) = v[i];
+  } else {
+#pragma unroll
+    for (uint32_t i = 0; i < 7; ++i)
+      if (i < n) *reinterpret_cast<uint16_t*>(p + 2 * i) = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// A wave's piece of a row: U units per lane, unit j of lane l being the
+// row's unit u0 + 64 j + l.  `left`: elements of the row from unit u0 on.  A
+// whole piece takes the branch-free form, so that its loads go out together.
+template <typename T, int U>
+__device__ __forceinline__ bool whole_piece(uint32_t left) {
+  return left >= 64u * U * kUnit<T>;
+}
+
+template <typename T, int U, bool NT>
+__device__ __forceinline__ void ld_piece(const char* row, uint32_t left, u32x4 (&v)[U]) {
+  const uint32_t lane = threadIdx.x & 63u;
+  if (whole_piece<T, U>(left)) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) v[j] = ld_unit<NT>(row + (j * 64u + lane) * 16u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t u = j * 64u + lane, e = u * kUnit<T>;
+      v[j] = u32x4{0, 0, 0, 0};
+      if (e + kUnit<T> <= left)
+        v[j] = ld_unit<NT>(row + u * 16u);
+      else if (e < left)
+        v[j] = ld_part<T>(row + u * 16u, left - e);
+    }
+  }
+}
+
+template <typename T, int U, bool NT>
+__device__ __forceinline__ void st_piece(char* row, uint32_t left, const u32x4 (&v)[U]) {
+  const uint32_t lane = threadIdx.x & 63u;
+  if (whole_piece<T, U>(left)) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) st_unit<NT>(row + (j * 64u + lane) * 16u, v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t u = j * 64u + lane, e = u * kUnit<T>;
+      if (e + kUnit<T> <= left)
+        st_unit<NT>(row + u * 16u, v[j]);
+      else if (e < left)
+        st_part<T>(row + u * 16u, v[j], left - e);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t wave_id() { return uniform(threadIdx.x >> 6); }
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x = x + __shfl_xor(x, m);
+  return x;
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x = x + __shfl_xor(x, m);
+  return x;
+}
+// the largest of 64 values that are not NaN (a NaN is passed over)
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
+// id of item i of an id array of 4- or 8-byte elements
+__device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, uint64_t i) {
+  return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : (int64_t) static_cast<const int32_t*>(ids)[i];
+}
+
+}  // namespace snac
