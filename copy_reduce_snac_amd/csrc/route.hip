@@ -2,6 +2,8 @@
 // (snac_route, snac_route_backward in include/snac_ops.h).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ops.hpp"
 #include "rows.hpp"
 
@@ -10,6 +12,7 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr uint64_t kRouteManyTokens = 2048;
 
 // A binary64 as an unsigned number of the same order; 0 for -infinity
 // (masked), NaN above everything, -0 as +0.
@@ -20,13 +23,21 @@ __device__ __forceinline__ uint64_t order64(double x) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) {
-    const uint64_t y = __shfl_xor((unsigned long long)x, m);
-    x = y > x ? y : x;
-  }
-  return x;
+__device__ __forceinline__ uint64_t wave_max64(uint64_t x) {
+  const uint32_t hi = lanes_max<64>((uint32_t)(x >> 32));
+  const uint32_t lo = lanes_max<64>((uint32_t)(x >> 32) == hi ? (uint32_t)x : 0);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// The value that lane `l` (the same in all lanes) holds.
+__device__ __forceinline__ uint32_t from_lane(uint32_t x, uint32_t l) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, (int)l);
+}
+__device__ __forceinline__ uint64_t from_lane(uint64_t x, uint32_t l) {
+  return (uint64_t)from_lane((uint32_t)(x >> 32), l) << 32 | from_lane((uint32_t)x, l);
+}
+__device__ __forceinline__ double from_lane(double x, uint32_t l) {
+  return __longlong_as_double((long long)from_lane((uint64_t)__double_as_longlong(x), l));
 }
 
 template <typename T>
@@ -34,144 +45,400 @@ __device__ __forceinline__ float load_logit(const char* row, uint32_t e) {
   return load_elem<T>(row + (uint64_t)e * T::kSize);
 }
 
-// One wave a token, lane l holding experts l V .. l V + V - 1, so that the
-// lowest lane of several with equal keys holds the lowest expert.
+// One token by a whole wave with its keys in binary64, lane l holding experts
+// l V .. l V + V - 1, so that the lowest lane of several with equal keys holds
+// the lowest expert.  Right for every input; route_kernel calls it for the
+// tokens whose order it cannot be sure of.
 template <typename T, int V>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a) {
+__device__ void route_exact(const RouteArgs& a, uint64_t t) {
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t E = (uint32_t)a.r.experts, G = (uint32_t)a.r.groups, K = (uint32_t)a.r.topk;
   const uint32_t gs = E / G;
   const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX;
   const float inf = __builtin_inff();
-  for (uint64_t t = (uint64_t)blockIdx.x * kRouteWaves + wave_id(); t < a.tokens;
-       t += (uint64_t)gridDim.x * kRouteWaves) {
-    const char* row = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
-    float x[V];
-    bool bad = false;
-    float top = -inf;
+  const char* row = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
+  float x[V];
+  bool bad = false;
+  float top = -inf;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t e = lane * V + j;
-      x[j] = e < E ? load_logit<T>(row, e) : -inf;
-      bad |= x[j] != x[j];
-      top = fmaxf(top, x[j]);
+  for (int j = 0; j < V; ++j) {
+    const uint32_t e = lane * V + j;
+    x[j] = e < E ? load_logit<T>(row, e) : -inf;
+    bad |= x[j] != x[j];
+    top = fmaxf(top, x[j]);
+  }
+  top = wave_max(top);
+  // softmax of a row with a NaN or +infinity is NaN throughout
+  const bool poison = softmax && (__any(bad) || top == inf);
+  double s[V];
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (softmax) {
+      s[j] = x[j] == -inf ? 0.0 : exp((double)x[j] - (double)top);
+      sum += s[j];
+    } else {
+      s[j] = 1.0 / (1.0 + exp(-(double)x[j]));
     }
-    top = snac::wave_max(top);
-    // softmax of a row with a NaN or +infinity is NaN throughout
-    const bool poison = softmax && (__any(bad) || top == inf);
-    double s[V];
-    double sum = 0.0;
+  }
+  if (softmax) sum = wave_sum(sum);
+  uint64_t key[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (softmax) {
-        s[j] = x[j] == -inf ? 0.0 : exp((double)x[j] - (double)top);
-        sum += s[j];
-      } else {
-        s[j] = 1.0 / (1.0 + exp(-(double)x[j]));
-      }
-    }
-    if (softmax) sum = wave_sum(sum);
-    uint64_t key[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t e = lane * V + j;
-      if (softmax) s[j] = poison ? __builtin_nan("") : s[j] / sum;
-      const double k = x[j] == -inf ? -HUGE_VAL : (a.bias && e < E ? s[j] + (double)a.bias[e] : s[j]);
-      key[j] = order64(k);
-      s[j] = k;  // from here on the key itself
-    }
-    if (G > 1) {
-      // lane g: the worth of group g
-      uint64_t worth = 0;
-      for (uint32_t g = 0; g < G; ++g) {
-        uint64_t best[2] = {0, 0};
-        double val[2] = {-HUGE_VAL, -HUGE_VAL};
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const uint32_t e = lane * V + j;
-          if (e < E && e / gs == g) {
-            if (key[j] > best[0]) {
-              best[1] = best[0], val[1] = val[0];
-              best[0] = key[j], val[0] = s[j];
-            } else if (key[j] > best[1]) {
-              best[1] = key[j], val[1] = s[j];
-            }
-          }
-        }
-        const uint64_t m0 = wave_max(best[0]);
-        const uint64_t at0 = __ballot(best[0] == m0);
-        const uint32_t l0 = (uint32_t)__ffsll((unsigned long long)at0) - 1;
-        double w = __shfl(val[0], (int)l0);
-        if (a.r.group_top == 2 && gs > 1) {
-          if (lane == l0) best[0] = best[1], val[0] = val[1];
-          const uint64_t m1 = wave_max(best[0]);
-          const uint32_t l1 = (uint32_t)__ffsll((unsigned long long)__ballot(best[0] == m1)) - 1;
-          w = w + __shfl(val[0], (int)l1);
-        }
-        if (lane == g) worth = order64(w);
-      }
-      uint32_t before = 0;
-      for (uint32_t g = 0; g < G; ++g) {
-        const uint64_t o = __shfl((unsigned long long)worth, (int)g);
-        before += o > worth || (o == worth && g < lane);
-      }
-      const uint64_t kept = __ballot(lane < G && worth != 0 && before < (uint32_t)a.r.topk_groups);
+  for (int j = 0; j < V; ++j) {
+    const uint32_t e = lane * V + j;
+    if (softmax) s[j] = poison ? __builtin_nan("") : s[j] / sum;
+    const double k = x[j] == -inf ? -HUGE_VAL : (a.bias && e < E ? s[j] + (double)a.bias[e] : s[j]);
+    key[j] = order64(k);
+    s[j] = k;  // from here on the key itself
+  }
+  if (G > 1) {
+    // lane g: the worth of group g
+    uint64_t worth = 0;
+    for (uint32_t g = 0; g < G; ++g) {
+      uint64_t best[2] = {0, 0};
+      double val[2] = {-HUGE_VAL, -HUGE_VAL};
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const uint32_t e = lane * V + j;
-        if (e >= E || !((kept >> (e / gs)) & 1)) key[j] = 0;
+        if (e < E && e / gs == g) {
+          if (key[j] > best[0]) {
+            best[1] = best[0], val[1] = val[0];
+            best[0] = key[j], val[0] = s[j];
+          } else if (key[j] > best[1]) {
+            best[1] = key[j], val[1] = s[j];
+          }
+        }
+      }
+      const uint64_t m0 = wave_max64(best[0]);
+      const uint64_t at0 = __ballot(best[0] == m0);
+      const uint32_t l0 = (uint32_t)__ffsll((unsigned long long)at0) - 1;
+      double w = from_lane(val[0], l0);
+      if (a.r.group_top == 2 && gs > 1) {
+        if (lane == l0) best[0] = best[1], val[0] = val[1];
+        const uint64_t m1 = wave_max64(best[0]);
+        const uint32_t l1 = (uint32_t)__ffsll((unsigned long long)__ballot(best[0] == m1)) - 1;
+        w = w + from_lane(val[0], l1);
+      }
+      if (lane == g) worth = order64(w);
+    }
+    uint32_t before = 0;
+    for (uint32_t g = 0; g < G; ++g) {
+      const uint64_t o = from_lane(worth, g);
+      before += o > worth || (o == worth && g < lane);
+    }
+    const uint64_t kept = __ballot(lane < G && worth != 0 && before < (uint32_t)a.r.topk_groups);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t e = lane * V + j;
+      if (e >= E || !((kept >> (e / gs)) & 1)) key[j] = 0;
+    }
+  }
+  // lane k: the k-th choice
+  int32_t my_id = -1;
+  float my_x = -inf;
+  for (uint32_t k = 0; k < K; ++k) {
+    uint64_t best = key[0];
+    int at = 0;
+    float bx = x[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j)
+      if (key[j] > best) best = key[j], at = j, bx = x[j];
+    const uint64_t m = wave_max64(best);
+    if (m == 0) break;
+    const int l = __ffsll((unsigned long long)__ballot(best == m)) - 1;
+    const int id = (int)from_lane(lane * V + (uint32_t)at, (uint32_t)l);
+    const float vx = __uint_as_float(from_lane(__float_as_uint(bx), (uint32_t)l));
+    if (lane == k) my_id = id, my_x = vx;
+    if ((int)lane == l) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j == at) key[j] = 0;
+    }
+  }
+  const bool have = my_id >= 0;
+  float w;
+  if (softmax) {
+    const float m = a.r.renorm ? wave_max(my_x) : top;
+    const float p = have ? expf(my_x - m) : 0.0f;
+    float total;
+    if (a.r.renorm) {
+      total = wave_sum(p);
+    } else {
+      total = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : expf(x[j] - m);
+      total = wave_sum(total);
+    }
+    w = poison ? __builtin_nanf("") : p / total;
+  } else if (a.r.renorm) {
+    // s_i / sum s_j with both sides times exp(-m), m the largest chosen
+    // logit where that is negative: nothing underflows
+    const float m = fminf(wave_max(my_x), 0.0f);
+    const float p = !have ? 0.0f : m < 0.0f ? expf(my_x - m) / (1.0f + expf(my_x)) : 1.0f / (1.0f + expf(-my_x));
+    w = p / wave_sum(p);
+  } else {
+    w = 1.0f / (1.0f + expf(-my_x));
+  }
+  if (lane < K) {
+    a.weights[t * K + lane] = have ? w * a.r.scale : 0.0f;
+    a.ids[t * K + lane] = my_id;
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_exact_kernel(const RouteArgs a) {
+  for (uint64_t t = (uint64_t)blockIdx.x * kRouteWaves + wave_id(); t < a.tokens;
+       t += (uint64_t)gridDim.x * kRouteWaves)
+    route_exact<T, V>(a, t);
+}
+
+// Batcher's odd-even merge sort of N (a power of two) registers, largest
+// first.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t x = k[i + j], y = k[i + j + q];
+            k[i + j] = x > y ? x : y;
+            k[i + j + q] = x > y ? y : x;
+          }
+}
+
+// V neighbouring elements of a row from element e0 on, the first `n` of them
+// (those past it as -infinity); whole: n is 0 or V in every lane.
+template <typename T, int V>
+__device__ __forceinline__ void load_elems(const char* row, uint32_t e0, uint32_t n, bool whole, float (&x)[V]) {
+  const char* p = row + (uint64_t)e0 * T::kSize;
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = -__builtin_inff();
+  if (V * T::kSize >= 16 && whole) {
+    if (n) {
+      constexpr int N = kUnit<T>;
+#pragma unroll
+      for (int u = 0; u < V / N; ++u) {
+        float f[N];
+        unpack<T>(ld_unit<false>(p + u * 16), f);
+#pragma unroll
+        for (int c = 0; c < N; ++c) x[u * N + c] = f[c];
       }
     }
-    // lane k: the k-th choice
-    int32_t my_id = -1;
-    float my_x = -inf;
-    for (uint32_t k = 0; k < K; ++k) {
-      uint64_t best = key[0];
-      int at = 0;
-      float bx = x[0];
+  } else {
 #pragma unroll
-      for (int j = 1; j < V; ++j)
-        if (key[j] > best) best = key[j], at = j, bx = x[j];
-      const uint64_t m = wave_max(best);
-      if (m == 0) break;
-      const int l = __ffsll((unsigned long long)__ballot(best == m)) - 1;
-      const int id = __shfl((int)(lane * V) + at, l);
-      const float vx = __shfl(bx, l);
-      if (lane == k) my_id = id, my_x = vx;
-      if ((int)lane == l) {
+    for (int j = 0; j < V; ++j)
+      if ((uint32_t)j < n) x[j] = load_elem<T>(p + j * T::kSize);
+  }
+}
+
+// L lanes a token, V experts a lane (in neighbouring slots; a group of
+// experts begins at a lane of its own and has 1 << ps lanes).
+//
+// Choosing is bound by instructions, not by memory, so a key is one 32-bit
+// number: the score's distance from the row's best, QB bits of it, above the
+// complement of the slot's number.  All keys of a token differ, they order as
+// the scores do down to their last bits, and the maximum over lanes is 4 to 6
+// instructions.  A lane sorts its V keys once; a round takes the largest
+// head over the lanes and shifts that lane's keys down.  What QB bits and
+// binary32 scores cannot tell apart is seen by comparing every choice with
+// the next one (one round more than topk): where they come as near as `tol`
+// steps without being equal in logit and bias, or are not finite, the token
+// is done again by route_exact.
+//   no bias (keys order as the logits): the distance as a floating number of
+//     QB bits.  Distance and cut keep the order, so only equal codes of
+//     different logits are in doubt.
+//   else: the distance in fixed point over S = 2 max(|best|, largest score).
+//     A binary32 score with its bias is off by less than 3.5 S 2^-24 (sigmoid)
+//     or 16 S 2^-24 (softmax: 24 additions in the sum), the subtraction and the
+//     scaling by at most S 2^-24 each, cutting by one step: two keys by 12 or
+//     37 steps at QB = 24.
+template <typename T, int L, int V, int KB>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a, const uint32_t ps) {
+  constexpr uint32_t TPW = 64 / L;
+  constexpr uint32_t IB = __builtin_ctz(L * V), QB = IB < 8 ? 24 : 32 - IB, QMAX = (1u << QB) - 1;
+  constexpr int VX = L * V <= 64 ? 1 : L * V / 64;
+  const uint32_t lane = threadIdx.x & 63u, l = lane % L, sub = lane / L;
+  const uint32_t E = (uint32_t)a.r.experts, G = (uint32_t)a.r.groups, K = (uint32_t)a.r.topk;
+  const uint32_t gs = E / G;
+  const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX;
+  const bool by_logit = !a.bias && (G == 1 || a.r.group_top == 1 || gs == 1);
+  const float inf = __builtin_inff();
+  constexpr float log2e = 1.44269504f;
+  // the lane's experts
+  const uint32_t g = l >> ps, in = (l & ((1u << ps) - 1)) * V;
+  const uint32_t e0 = g * gs + in, n = g >= G || in >= gs ? 0 : gs - in < V ? gs - in : V;
+  const bool whole = gs % V == 0;
+  float b[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) b[j] = 0.0f;
+  if (a.bias) load_elems<F32, V>(reinterpret_cast<const char*>(a.bias), e0, n, whole, b);
+
+  for (uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW; t0 < a.tokens;
+       t0 += (uint64_t)gridDim.x * kRouteWaves * TPW) {
+    const uint64_t t = t0 + sub;
+    const bool live = t < a.tokens;
+    const char* row = static_cast<const char*>(a.logits) + (live ? t : t0) * a.ld * T::kSize;
+    float x[V];
+    load_elems<T, V>(row, e0, n, whole, x);
+    bool doubt = false;
+    float top = -inf;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      doubt |= x[j] != x[j];
+      top = fmaxf(top, x[j]);
+    }
+    top = lanes_max<L>(top);
+    doubt |= top == inf;
+    float total = 0.0f;  // softmax: sum of exp(x - top)
+    if (softmax && !(by_logit && a.r.renorm)) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : __builtin_amdgcn_exp2f((x[j] - top) * log2e);
+      total = lanes_sum<L>(total);
+    }
+    uint32_t key[V];
+    uint32_t tol = 0;
+    if (by_logit) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t q = (0x7fffffffu - __float_as_uint(top - x[j])) >> (31 - QB);
+        key[j] = x[j] == -inf ? 0 : q << IB | (L * V - 1 - (l * V + j));
+      }
+    } else {
+      float v[V];
+      float best = -inf;
+      const float inv = 1.0f / total;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float s = softmax ? __builtin_amdgcn_exp2f((x[j] - top) * log2e) * inv
+                                : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-log2e * x[j]));
+        v[j] = x[j] == -inf ? -inf : s + b[j];
+        doubt |= v[j] != v[j];
+        best = fmaxf(best, v[j]);
+      }
+      best = lanes_max<L>(best);
+      doubt |= best == inf;
+      const float most = softmax ? inv : 1.0f;  // the largest score
+      const float scale = (float)(1u << (QB - 1)) / fmaxf(fabsf(best), most);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t d = (uint32_t)fminf((best - v[j]) * scale, (float)(QMAX - 1));
+        key[j] = v[j] == -inf ? 0 : (QMAX - d) << IB | (L * V - 1 - (l * V + j));
+      }
+      tol = ((softmax ? 37u : 12u) >> (24 - QB)) + (QB < 24);
+    }
+    sort_down<V>(key);
+    if (G > 1) {
+      // the group's two largest keys, over its lanes
+      uint32_t m0 = key[0], m1 = V > 1 ? key[V > 1 ? 1 : 0] : 0;
+      auto merge = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        uint32_t o0, o1;
+        if constexpr (D <= 8) {
+          constexpr int C = D == 1 ? kDppXor1 : D == 2 ? kDppXor2 : D == 4 ? kDppHalfMirror : kDppMirror;
+          o0 = dpp<C>(m0), o1 = dpp<C>(m1);
+        } else if constexpr (D == 16) {
+          const auto r0 = __builtin_amdgcn_permlane16_swap(m0, m0, false, false);
+          const auto r1 = __builtin_amdgcn_permlane16_swap(m1, m1, false, false);
+          m0 = r0[0], o0 = r0[1], m1 = r1[0], o1 = r1[1];
+        } else {
+          const auto r0 = __builtin_amdgcn_permlane32_swap(m0, m0, false, false);
+          const auto r1 = __builtin_amdgcn_permlane32_swap(m1, m1, false, false);
+          m0 = r0[0], o0 = r0[1], m1 = r1[0], o1 = r1[1];
+        }
+        const uint32_t lo = m0 < o0 ? m0 : o0, hi = m1 > o1 ? m1 : o1;
+        m0 = m0 > o0 ? m0 : o0;
+        m1 = lo > hi ? lo : hi;
+      };
+      if (ps > 0) merge(std::integral_constant<int, 1>{});
+      if (ps > 1) merge(std::integral_constant<int, 2>{});
+      if (ps > 2) merge(std::integral_constant<int, 4>{});
+      if (ps > 3) merge(std::integral_constant<int, 8>{});
+      if (L > 16 && ps > 4) merge(std::integral_constant<int, 16>{});
+      const bool two = a.r.group_top == 2 && gs > 1;
+      uint32_t worth = m0 >> IB;
+      if (two) worth = m1 ? worth + (m1 >> IB) : 0;
+      const bool cut = !by_logit && ((m0 >> IB) == 1 || (two && (m1 >> IB) == 1));
+      const uint32_t mine = worth && g < G ? worth << 6 | (63 - g) : 0;
+      // the topk_groups-th largest, and the next
+      uint32_t left = mine, last = 0, next = 0;
+      for (uint32_t k = 0; k < (uint32_t)a.r.topk_groups; ++k) {
+        last = lanes_max<L>(left);
+        left = left == last ? 0 : left;
+      }
+      next = lanes_max<L>(left);
+      const bool kept = mine && mine >= last;
+      doubt |= last && next && (last >> 6) - (next >> 6) <= 2 * tol;
+      doubt |= kept && cut;
+      if (!kept) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = 0;
+      }
+    }
+    // lane k: the k-th choice (0: none); lane topk: the next one
+    uint32_t won = 0;
+#pragma unroll
+    for (int k = 0; k <= KB; ++k) {
+      if ((uint32_t)k <= K) {
+        const uint32_t m = lanes_max<L>(key[0]);
+        won = l == (uint32_t)k ? m : won;
+        const bool pop = key[0] == m;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          if (j == at) key[j] = 0;
+          if (j < KB - k) {
+            const uint32_t stay = key[j], next = j + 1 < V ? key[j + 1 < V ? j + 1 : j] + 0 : 0;
+            key[j] = pop ? next : stay;
+          }
       }
     }
-    const bool have = my_id >= 0;
+    const uint32_t q = won >> IB, slot = L * V - 1 - (won & ((1u << IB) - 1));
+    const uint32_t wl = slot / V;  // its lane
+    const uint32_t id = (wl >> ps) * gs + (wl & ((1u << ps) - 1)) * V + slot % V;
+    const float cx = won ? load_logit<T>(row, id) : -inf;
+    const float cb = won && a.bias ? a.bias[id] : 0.0f;
+    const uint32_t next = from_next_lane(won, 0);
+    const float nx = __uint_as_float(from_next_lane(__float_as_uint(cx), 0));
+    const float nb = __uint_as_float(from_next_lane(__float_as_uint(cb), 0));
+    if (l < K && won) {
+      // binary64 scores of different logits may be equal where they saturate
+      // (sigmoids of logits above 20 nearly so), underflow or lie too near
+      doubt |= by_logit ? (softmax ? top - cx > 700.0f : cx > 20.0f || cx < -700.0f) : q == 1;
+      doubt |= by_logit && next && cx != nx && cx - nx < 1e-13f;
+      if (next && q - (next >> IB) <= tol) {
+        const bool equal = cx == nx && cb == nb;
+        // past an equal pair at the end there may be more, not looked at: two
+        // bf16 logits of one code are equal unless far below the best
+        const bool sure = l + 1 < K || (T::kSize == 2 && by_logit && (float)(1u << (QB - 17)) * fabsf(cx) >= top - cx);
+        doubt |= !(equal && sure);
+      }
+    }
+    const uint64_t again = __ballot(doubt && live);
+    // the weights of the chosen, lane k the k-th
+    const bool have = l < K && won;
+    const float sx = have ? cx : -inf;
     float w;
     if (softmax) {
-      const float m = a.r.renorm ? snac::wave_max(my_x) : top;
-      const float p = have ? expf(my_x - m) : 0.0f;
-      float total;
-      if (a.r.renorm) {
-        total = wave_sum(p);
-      } else {
-        total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : expf(x[j] - m);
-        total = wave_sum(total);
-      }
-      w = poison ? __builtin_nanf("") : p / total;
+      const float m = a.r.renorm ? lanes_max<L>(sx) : top;
+      const float p = have ? expf(cx - m) : 0.0f;
+      w = p / (a.r.renorm ? lanes_sum<L>(p) : total);
     } else if (a.r.renorm) {
-      // s_i / sum s_j with both sides times exp(-m), m the largest chosen
-      // logit where that is negative: nothing underflows
-      const float m = fminf(snac::wave_max(my_x), 0.0f);
-      const float p = !have ? 0.0f : m < 0.0f ? expf(my_x - m) / (1.0f + expf(my_x)) : 1.0f / (1.0f + expf(-my_x));
-      w = p / wave_sum(p);
+      const float m = fminf(lanes_max<L>(sx), 0.0f);
+      const float p = !have ? 0.0f : m < 0.0f ? expf(cx - m) / (1.0f + expf(cx)) : 1.0f / (1.0f + expf(-cx));
+      w = p / lanes_sum<L>(p);
     } else {
-      w = 1.0f / (1.0f + expf(-my_x));
+      w = 1.0f / (1.0f + expf(-cx));
     }
-    if (lane < K) {
-      a.weights[t * K + lane] = have ? w * a.r.scale : 0.0f;
-      a.ids[t * K + lane] = my_id;
+    const uint64_t sub_lanes = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (sub * L % 64);
+    if (l < K && live && !(again & sub_lanes)) {
+      a.weights[t * K + l] = have ? w * a.r.scale : 0.0f;
+      a.ids[t * K + l] = have ? (int32_t)id : -1;
     }
+    for (uint32_t s = 0; s < TPW; ++s)
+      if (again >> (s * L % 64) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) route_exact<T, VX>(a, t0 + s);
   }
 }
 
@@ -202,7 +469,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
         x[j] = e < E ? load_logit<T>(row, e) : -inf;
         top = fmaxf(top, x[j]);
       }
-      top = snac::wave_max(top);
+      top = wave_max(top);
       float total = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -222,7 +489,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
     } else {
       float g;
       if (softmax) {
-        const float m = snac::wave_max(cx);
+        const float m = wave_max(cx);
         const float p = !have || cx == -inf ? 0.0f : expf(cx - m);
         const float total = wave_sum(p);
         const float r = total == 0.0f ? 0.0f : p / total;
@@ -230,7 +497,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
       } else {
         const float far = 1.0f / (1.0f + expf(cx));
         if (a.r.renorm) {
-          const float m = fminf(snac::wave_max(cx), 0.0f);
+          const float m = fminf(wave_max(cx), 0.0f);
           const float p = !have || cx == -inf ? 0.0f : m < 0.0f ? expf(cx - m) * far : 1.0f / (1.0f + expf(-cx));
           const float total = wave_sum(p);
           const float r = total == 0.0f ? 0.0f : p / total;
@@ -256,15 +523,43 @@ uint32_t route_grid(uint64_t tokens) {
   return (uint32_t)(want < most ? want : most);
 }
 
+// Lanes of a group when a lane holds V experts: 1 << ps.
+uint32_t group_shift(const snac_router& r, uint32_t V) {
+  const uint32_t gs = (uint32_t)(r.experts / r.groups);
+  uint32_t ps = 0;
+  while ((V << ps) < gs) ++ps;
+  return ps;
+}
+
+template <typename T, int L, int V, int KB>
+bool route_fits(const RouteArgs& a, hipStream_t stream) {
+  uint32_t ps = group_shift(a.r, V);
+  if (a.r.topk > KB || a.r.topk + 1 > L || (uint64_t)a.r.groups << ps > L) return false;
+  if (a.r.groups == 1) ps = __builtin_ctz(L);
+  const uint64_t per = kRouteWaves * (64 / L);
+  const uint64_t want = (a.tokens + per - 1) / per;
+  const int cus = device_cu_count();
+  const uint64_t most = (uint64_t)(cus > 0 ? cus : 1) * 16;
+  hipLaunchKernelGGL((route_kernel<T, L, V, KB>), dim3((uint32_t)(want < most ? want : most)), dim3(kRouteThreads), 0,
+                     stream, a, ps);
+  return true;
+}
+
+// The narrowest shape that holds the experts; few tokens take a wave each.
 template <typename T>
 void route_any(const RouteArgs& a, hipStream_t stream) {
+  if (a.tokens >= kRouteManyTokens &&
+      (route_fits<T, 16, 1, 8>(a, stream) || route_fits<T, 16, 4, 8>(a, stream) || route_fits<T, 16, 8, 8>(a, stream) ||
+       route_fits<T, 16, 16, 8>(a, stream) || route_fits<T, 32, 16, 8>(a, stream)))
+    return;
+  if (route_fits<T, 64, 1, 8>(a, stream) || route_fits<T, 64, 4, 8>(a, stream) || route_fits<T, 64, 16, 8>(a, stream))
+    return;
+  if (route_fits<T, 64, 1, 32>(a, stream) || route_fits<T, 64, 4, 32>(a, stream) || route_fits<T, 64, 16, 32>(a, stream))
+    return;
   const dim3 grid(route_grid(a.tokens)), block(kRouteThreads);
   const int e = a.r.experts;
-  if (e <= 64) hipLaunchKernelGGL((route_kernel<T, 1>), grid, block, 0, stream, a);
-  else if (e <= 128) hipLaunchKernelGGL((route_kernel<T, 2>), grid, block, 0, stream, a);
-  else if (e <= 256) hipLaunchKernelGGL((route_kernel<T, 4>), grid, block, 0, stream, a);
-  else if (e <= 512) hipLaunchKernelGGL((route_kernel<T, 8>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((route_kernel<T, 16>), grid, block, 0, stream, a);
+  if (e <= 256) hipLaunchKernelGGL((route_exact_kernel<T, 4>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((route_exact_kernel<T, 16>), grid, block, 0, stream, a);
 }
 
 template <typename T>

@@ -135,20 +135,66 @@ __device__ __forceinline__ void st_piece(char* row, uint32_t left, const u32x4 (
 
 __device__ __forceinline__ uint32_t wave_id() { return uniform(threadIdx.x >> 6); }
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) x = x + __shfl_xor(x, m);
+// ---- reductions over L = 16, 32 or 64 neighbouring lanes, every lane with
+// the same result: exchanges inside a row of 16 lanes by DPP (lanes 1, 2,
+// then mirrored halves, so that both sides of a sum add the same two
+// numbers), across rows by gfx950's lane swaps.  All 64 lanes must be active.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+// x = f(x, the x of the lane's partner) at distance D (1, 2, 4, 8, 16, 32)
+template <int D, typename F>
+__device__ __forceinline__ uint32_t exchange(uint32_t x, F f) {
+  if constexpr (D == 1) return f(x, dpp<kDppXor1>(x));
+  else if constexpr (D == 2) return f(x, dpp<kDppXor2>(x));
+  else if constexpr (D == 4) return f(x, dpp<kDppHalfMirror>(x));
+  else if constexpr (D == 8) return f(x, dpp<kDppMirror>(x));
+  else if constexpr (D == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return f(r[0], r[1]);
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return f(r[0], r[1]);
+  }
+}
+
+template <int L, typename F>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t x, F f) {
+  x = exchange<1>(x, f);
+  x = exchange<2>(x, f);
+  x = exchange<4>(x, f);
+  x = exchange<8>(x, f);
+  if constexpr (L >= 32) x = exchange<16>(x, f);
+  if constexpr (L >= 64) x = exchange<32>(x, f);
   return x;
 }
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+  return __uint_as_float(lanes_reduce<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+// the largest of the values that are not NaN
+template <int L>
+__device__ __forceinline__ float lanes_max(float x) {
+  return __uint_as_float(lanes_reduce<L>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+  return lanes_reduce<L>(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+__device__ __forceinline__ float wave_sum(float x) { return lanes_sum<64>(x); }
+__device__ __forceinline__ float wave_max(float x) { return lanes_max<64>(x); }
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
   for (int m = 32; m; m >>= 1) x = x + __shfl_xor(x, m);
-  return x;
-}
-// the largest of 64 values that are not NaN (a NaN is passed over)
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
   return x;
 }
 

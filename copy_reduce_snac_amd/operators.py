@@ -20,8 +20,15 @@ _FLOAT = {torch.bfloat16: "bf16", torch.float32: "f32"}
 _ID = {torch.int32: 4, torch.int64: 8}
 
 
+# torch's current stream as a hipStream_t: torch.cuda.current_stream() makes a
+# Stream object for it, which takes longer (2.5 us) than a call's other checks
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    return stream if stream is not None else torch.cuda.current_stream()
+    if stream is not None:
+        return stream
+    return _raw_stream(torch.cuda.current_device()) if _raw_stream else torch.cuda.current_stream()
 
 
 def _float(t, what: str) -> str:

@@ -124,12 +124,68 @@ def test_keys_one_step_apart(score, groups):
         check(x, 8, "f32", bias=bias, score=score, groups=groups, topk_groups=max(1, groups // 2))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("cfg", [c for c in CONFIGS if c["topk"] <= 8] + [
+    dict(n=10, topk=8), dict(n=500, topk=8, groups=5, topk_groups=3), dict(n=96, topk=5, groups=48, topk_groups=7),
+    dict(n=1020, topk=7, groups=3, topk_groups=2), dict(n=900, topk=3, groups=30, topk_groups=4)],
+    ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_many_tokens(dtype, score, biased, cfg):
+    """Several tokens a wave; coarse logits (ties), fine ones, masked experts; every row's choice, in NumPy at once."""
+    cfg = dict(cfg)
+    n, topk = cfg.pop("n"), cfg.pop("topk")
+    g = np.random.default_rng(n * 11 + topk)
+    tokens = 4099
+    x = g.normal(size=(tokens, n)) * 2
+    x[::3] = np.round(x[::3] * 16) / 16
+    x[::7, g.random(n) < 0.2] = -np.inf
+    x[5] = -np.inf
+    bias = g.normal(size=n) * 0.05 if biased else None
+    xs, w, ids = run(x, topk, dtype, bias=bias, score=score, **cfg)
+    b = None if bias is None else np.asarray(bias, np.float32).astype(np.float64)
+    with np.errstate(all="ignore"):
+        m = xs.max(axis=1, keepdims=True)
+        s = 1 / (1 + np.exp(-xs)) if score == "sigmoid" else np.exp(xs - m) / np.exp(xs - m).sum(axis=1, keepdims=True)
+    key = np.where(xs == -np.inf, -np.inf, s if b is None else s + b)
+    gr = cfg.get("groups", 1)
+    if gr > 1:
+        k3 = np.sort(key.reshape(tokens, gr, n // gr), axis=2)[:, :, ::-1]
+        worth = k3[:, :, 0] + k3[:, :, 1] if cfg.get("group_top", 2) == 2 and n // gr > 1 else k3[:, :, 0]
+        best = np.argsort(-worth, axis=1, kind="stable")[:, :cfg["topk_groups"]]
+        ok = np.zeros((tokens, gr), bool)
+        np.put_along_axis(ok, best, np.take_along_axis(worth, best, 1) > -np.inf, 1)
+        key = np.where(np.repeat(ok, n // gr, axis=1), key, -np.inf)
+    want = np.argsort(-key, axis=1, kind="stable")[:, :topk]
+    want = np.where(np.take_along_axis(key, want, 1) == -np.inf, -1, want)
+    bad = np.flatnonzero((ids != want).any(axis=1))
+    assert bad.size == 0, f"rows {bad[:5]}: {ids[bad[:3]]} {want[bad[:3]]}"
+    for t in range(0, tokens, 41):
+        rw, _ = ref.route(xs[t], topk, bias=b, score=score, **cfg)
+        assert np.all(np.abs(w[t] - rw) <= 96 * U * np.abs(rw) + 1e-37), t
+
+
 def test_ties_go_to_the_lowest_index():
     g = np.random.default_rng(9)
     x = g.integers(-2, 3, size=(200, 128)).astype(np.float64) / 4
     for kw in (dict(score="softmax"), dict(score="sigmoid", bias=np.zeros(128)),
                dict(score="sigmoid", groups=8, topk_groups=3, bias=g.integers(0, 2, 128) / 8)):
         check(x, 9, "bf16", **kw)
+
+
+@pytest.mark.parametrize("tokens", [6, 3000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_equal_in_binary64(tokens, score):
+    """Different logits whose binary64 scores saturate or underflow: equal keys, the lower index first."""
+    g = np.random.default_rng(13)
+    x = g.normal(size=(6, 64)) * 20
+    x[0] += 60
+    x[1] -= 800
+    x[2, 5:] -= 1500
+    x[3] = 18 + g.normal(size=64) * 3
+    x[4, 1:] = 1e-20 * g.random(63)
+    check(np.resize(x, (6, 64)), 7, "f32", score=score)
+    xs, w, ids = run(np.tile(x, (tokens // 6, 1)), 7, "f32", score=score)
+    assert (ids.reshape(-1, 6, 7) == ids[:6]).all()
 
 
 def test_signed_zeros_are_equal():
