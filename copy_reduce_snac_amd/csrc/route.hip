@@ -13,6 +13,7 @@ namespace {
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr uint64_t kRouteManyTokens = 2048;
+constexpr int kMoreRounds = 3;  // choices looked at past the next one, where two are too near
 
 // A binary64 as an unsigned number of the same order; 0 for -infinity
 // (masked), NaN above everything, -0 as +0.
@@ -51,8 +52,11 @@ __device__ __forceinline__ float load_logit(const char* row, uint32_t e) {
 // tokens whose order it cannot be sure of.
 template <typename T, int V>
 __device__ void route_exact(const RouteArgs& a, uint64_t t) {
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t E = (uint32_t)a.r.experts, G = (uint32_t)a.r.groups, K = (uint32_t)a.r.topk;
+  uint32_t lane = threadIdx.x & 63u, E = (uint32_t)a.r.experts;
+  // opaque here, so that nothing of this rare path is worked out before the
+  // branch to it (it took 290 of 1000 instructions of route_kernel)
+  asm volatile("" : "+v"(lane), "+s"(E));
+  const uint32_t G = (uint32_t)a.r.groups, K = (uint32_t)a.r.topk;
   const uint32_t gs = E / G;
   const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX;
   const float inf = __builtin_inff();
@@ -212,29 +216,41 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[N]) {
 }
 
 // V neighbouring elements of a row from element e0 on, the first `n` of them
-// (those past it as -infinity); whole: n is 0 or V in every lane.
+// (those past it as `rest`).  whole: n is 0 or V in every lane, full: V.  No
+// branch per lane: a lane without an element reads the row's first.
 template <typename T, int V>
-__device__ __forceinline__ void load_elems(const char* row, uint32_t e0, uint32_t n, bool whole, float (&x)[V]) {
-  const char* p = row + (uint64_t)e0 * T::kSize;
+__device__ __forceinline__ void load_elems(const char* row, uint32_t e0, uint32_t n, bool whole, bool full, float rest,
+                                           float (&x)[V]) {
+  constexpr int N = kUnit<T>;
+  if constexpr (V >= N) {
+    if (whole) {
+      const char* p = row + (uint64_t)(n ? e0 : 0) * T::kSize;
+      u32x4 w[V / N];
 #pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = -__builtin_inff();
-  if (V * T::kSize >= 16 && whole) {
-    if (n) {
-      constexpr int N = kUnit<T>;
+      for (int u = 0; u < V / N; ++u) w[u] = ld_unit<false>(p + u * 16);
 #pragma unroll
       for (int u = 0; u < V / N; ++u) {
         float f[N];
-        unpack<T>(ld_unit<false>(p + u * 16), f);
+        unpack<T>(w[u], f);
 #pragma unroll
         for (int c = 0; c < N; ++c) x[u * N + c] = f[c];
       }
-    }
-  } else {
+      if (!full) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if ((uint32_t)j < n) x[j] = load_elem<T>(p + j * T::kSize);
+        for (int j = 0; j < V; ++j) x[j] = n ? x[j] + 0.0f : rest;
+      }
+      return;
+    }
   }
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = load_elem<T>(row + (uint64_t)((uint32_t)j < n ? e0 + j : 0) * T::kSize);
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = (uint32_t)j < n ? x[j] + 0.0f : rest;
 }
+
+// What a key is: kByLogit where there is no bias and no sum of scores (keys
+// order as the logits), else the score (with its bias).
+enum : int { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 
 // L lanes a token, V experts a lane (in neighbouring slots; a group of
 // experts begins at a lane of its own and has 1 << ps lanes).
@@ -257,26 +273,36 @@ __device__ __forceinline__ void load_elems(const char* row, uint32_t e0, uint32_
 //     or 16 S 2^-24 (softmax: 24 additions in the sum), the subtraction and the
 //     scaling by at most S 2^-24 each, cutting by one step: two keys by 12 or
 //     37 steps at QB = 24.
-template <typename T, int L, int V, int KB>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a, const uint32_t ps) {
+template <typename T, int L, int V, int KB, int KEY>
+__global__ __launch_bounds__(kRouteThreads, V <= 8 ? 6 : L == 16 ? 4 : 1) void route_kernel(const RouteArgs a, const uint32_t ps, const uint32_t gs) {
   constexpr uint32_t TPW = 64 / L;
   constexpr uint32_t IB = __builtin_ctz(L * V), QB = IB < 8 ? 24 : 32 - IB, QMAX = (1u << QB) - 1;
   constexpr int VX = L * V <= 64 ? 1 : L * V / 64;
   const uint32_t lane = threadIdx.x & 63u, l = lane % L, sub = lane / L;
   const uint32_t E = (uint32_t)a.r.experts, G = (uint32_t)a.r.groups, K = (uint32_t)a.r.topk;
-  const uint32_t gs = E / G;
-  const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX;
-  const bool by_logit = !a.bias && (G == 1 || a.r.group_top == 1 || gs == 1);
+  const bool softmax = KEY == kBySoftmax || (KEY == kByLogit && a.r.score == SNAC_SCORE_SOFTMAX);
+  constexpr bool by_logit = KEY == kByLogit;
   const float inf = __builtin_inff();
   constexpr float log2e = 1.44269504f;
   // the lane's experts
   const uint32_t g = l >> ps, in = (l & ((1u << ps) - 1)) * V;
   const uint32_t e0 = g * gs + in, n = g >= G || in >= gs ? 0 : gs - in < V ? gs - in : V;
-  const bool whole = gs % V == 0;
+  const bool whole = gs % V == 0, full = G << ps == L && gs == (uint32_t)V << ps;
   float b[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) b[j] = 0.0f;
-  if (a.bias) load_elems<F32, V>(reinterpret_cast<const char*>(a.bias), e0, n, whole, b);
+  if (!by_logit && a.bias) load_elems<F32, V>(reinterpret_cast<const char*>(a.bias), e0, n, whole, full, 0.0f, b);
+
+  // a packed key's expert (0: none), its logit and bias
+  struct Choice {
+    int32_t id;
+    float x, b;
+  };
+  auto chosen = [&](const char* row, uint32_t won) {
+    const uint32_t slot = L * V - 1 - (won & ((1u << IB) - 1)), wl = slot / V;
+    const uint32_t id = (wl >> ps) * gs + (wl & ((1u << ps) - 1)) * V + slot % V;
+    return Choice{won ? (int32_t)id : -1, won ? load_logit<T>(row, id) : -inf, won && a.bias ? a.bias[id] : 0.0f};
+  };
 
   for (uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW; t0 < a.tokens;
        t0 += (uint64_t)gridDim.x * kRouteWaves * TPW) {
@@ -284,7 +310,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     const bool live = t < a.tokens;
     const char* row = static_cast<const char*>(a.logits) + (live ? t : t0) * a.ld * T::kSize;
     float x[V];
-    load_elems<T, V>(row, e0, n, whole, x);
+    load_elems<T, V>(row, e0, n, whole, full, -inf, x);
     bool doubt = false;
     float top = -inf;
 #pragma unroll
@@ -294,6 +320,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     }
     top = lanes_max<L>(top);
     doubt |= top == inf;
+    auto score64 = [&](float x, float b) {
+      const double s = softmax ? exp((double)x - (double)top) : 1.0 / (1.0 + exp(-(double)x));
+      return by_logit ? s : s + (double)b;
+    };
     float total = 0.0f;  // softmax: sum of exp(x - top)
     if (softmax && !(by_logit && a.r.renorm)) {
 #pragma unroll
@@ -302,7 +332,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     }
     uint32_t key[V];
     uint32_t tol = 0;
-    if (by_logit) {
+    if constexpr (by_logit) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const uint32_t q = (0x7fffffffu - __float_as_uint(top - x[j])) >> (31 - QB);
@@ -371,8 +401,38 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
         left = left == last ? 0 : left;
       }
       next = lanes_max<L>(left);
-      const bool kept = mine && mine >= last;
-      doubt |= last && next && (last >> 6) - (next >> 6) <= 2 * tol;
+      bool kept = mine && mine >= last;
+      const bool near = last && next && (last >> 6) - (next >> 6) <= 2 * tol;
+      if (__any(near && live)) {
+        if constexpr (KEY == kBySoftmax) {
+          doubt |= near;
+        } else {
+          // by the worths in binary64, every lane its own group's; the keys
+          // that they sum have to be clear of the next one
+          uint32_t third = 0;
+#pragma unroll
+          for (int j = V > 2 ? 2 : V - 1; j >= 0; --j) third = key[j] != m0 && (!two || key[j] != m1) ? key[j] + 0 : third;
+          for (uint32_t d = 1; d < 1u << ps; d *= 2) {
+            const uint32_t o = __shfl_xor(third, (int)d, L);
+            third = o > third ? o : third;
+          }
+          const int away = (int)(mine >> 6) - (int)(last >> 6);
+          doubt |= near && mine && third && (uint32_t)abs(away) <= 4 * tol &&
+                   ((two ? m1 : m0) >> IB) - (third >> IB) <= tol;
+          uint64_t w64 = 0;
+          if (mine) {
+            const Choice c0 = chosen(row, m0), c1 = chosen(row, two ? m1 : m0);
+            const double s0 = score64(c0.x, c0.b), s1 = score64(c1.x, c1.b);
+            w64 = order64(two ? s0 + s1 : s0);
+          }
+          uint32_t before = 0;
+          for (uint32_t o = 0; o < G; ++o) {
+            const uint64_t v = __shfl((unsigned long long)w64, (int)(o << ps), L);
+            before += v > w64 || (v == w64 && o < g);
+          }
+          kept = near ? mine && before < (uint32_t)a.r.topk_groups : kept;
+        }
+      }
       doubt |= kept && cut;
       if (!kept) {
 #pragma unroll
@@ -381,29 +441,27 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     }
     // lane k: the k-th choice (0: none); lane topk: the next one
     uint32_t won = 0;
+    auto round = [&](uint32_t k, int keep) {
+      const uint32_t m = lanes_max<L>(key[0]);
+      won = l == k ? m : won;
+      const bool pop = key[0] == m;
 #pragma unroll
-    for (int k = 0; k <= KB; ++k) {
-      if ((uint32_t)k <= K) {
-        const uint32_t m = lanes_max<L>(key[0]);
-        won = l == (uint32_t)k ? m : won;
-        const bool pop = key[0] == m;
+      for (int j = 0; j < V; ++j)
+        if (j < keep) {
+          const uint32_t stay = key[j], next = j + 1 < V ? key[j + 1 < V ? j + 1 : j] + 0 : 0;
+          key[j] = pop ? next : stay;
+        }
+    };
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j < KB - k) {
-            const uint32_t stay = key[j], next = j + 1 < V ? key[j + 1 < V ? j + 1 : j] + 0 : 0;
-            key[j] = pop ? next : stay;
-          }
-      }
-    }
-    const uint32_t q = won >> IB, slot = L * V - 1 - (won & ((1u << IB) - 1));
-    const uint32_t wl = slot / V;  // its lane
-    const uint32_t id = (wl >> ps) * gs + (wl & ((1u << ps) - 1)) * V + slot % V;
-    const float cx = won ? load_logit<T>(row, id) : -inf;
-    const float cb = won && a.bias ? a.bias[id] : 0.0f;
-    const uint32_t next = from_next_lane(won, 0);
-    const float nx = __uint_as_float(from_next_lane(__float_as_uint(cx), 0));
-    const float nb = __uint_as_float(from_next_lane(__float_as_uint(cb), 0));
+    for (int k = 0; k <= KB; ++k)
+      if ((uint32_t)k <= K) round((uint32_t)k, KB + kMoreRounds - k);
+    Choice c = chosen(row, won);
+    const uint32_t q = won >> IB, next = from_next_lane(won, 0);
+    const float nx = __uint_as_float(from_next_lane(__float_as_uint(c.x), 0));
+    const float nb = __uint_as_float(from_next_lane(__float_as_uint(c.b), 0));
+    bool near = false;
     if (l < K && won) {
+      const float cx = c.x, cb = c.b;
       // binary64 scores of different logits may be equal where they saturate
       // (sigmoids of logits above 20 nearly so), underflow or lie too near
       doubt |= by_logit ? (softmax ? top - cx > 700.0f : cx > 20.0f || cx < -700.0f) : q == 1;
@@ -413,10 +471,35 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
         // past an equal pair at the end there may be more, not looked at: two
         // bf16 logits of one code are equal unless far below the best
         const bool sure = l + 1 < K || (T::kSize == 2 && by_logit && (float)(1u << (QB - 17)) * fabsf(cx) >= top - cx);
-        doubt |= !(equal && sure);
+        near = !(equal && sure);
+      }
+    }
+    if (__any(near && live)) {
+      if constexpr (KEY == kBySoftmax) {
+        doubt |= near;
+      } else {
+        // by the binary64 scores of the choices and of kMoreRounds after
+        // them, the last of which has to be clear of the topk-th
+#pragma unroll
+        for (int r = 1; r <= kMoreRounds; ++r) round(K + r, kMoreRounds - r);
+        const uint32_t end = __shfl(won, (int)(K + kMoreRounds), L);
+        doubt |= l + 1 == K && end && q - (end >> IB) <= tol;
+        c = chosen(row, won);
+        const uint64_t k64 = won ? order64(score64(c.x, c.b)) : 0;
+        uint32_t rank = 0;
+        for (uint32_t o = 0; o <= K + kMoreRounds; ++o) {
+          const uint64_t v = __shfl((unsigned long long)k64, (int)o, L);
+          const int32_t v_id = __shfl(c.id, (int)o, L);
+          rank += v > k64 || (v == k64 && v_id < c.id);
+        }
+        // to the lane of its rank (the lanes that nothing is sent to get 0)
+        const uint32_t to = won ? rank : L - 1;
+        won = (uint32_t)__builtin_amdgcn_ds_permute((int)((sub * L + to) * 4), (int)won);
+        c = chosen(row, won);
       }
     }
     const uint64_t again = __ballot(doubt && live);
+    const float cx = c.x;
     // the weights of the chosen, lane k the k-th
     const bool have = l < K && won;
     const float sx = have ? cx : -inf;
@@ -435,83 +518,133 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     const uint64_t sub_lanes = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (sub * L % 64);
     if (l < K && live && !(again & sub_lanes)) {
       a.weights[t * K + l] = have ? w * a.r.scale : 0.0f;
-      a.ids[t * K + l] = have ? (int32_t)id : -1;
+      a.ids[t * K + l] = have ? c.id : -1;
     }
     for (uint32_t s = 0; s < TPW; ++s)
       if (again >> (s * L % 64) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) route_exact<T, VX>(a, t0 + s);
   }
 }
 
-template <typename T, int V>
+// The gradient, L lanes a token, lane l holding logits l V .. l V + V - 1, so
+// that a token's logits are read and its gradients written in whole 16-byte
+// units where the row allows.  The chosen experts' terms come to their lanes
+// by way of LDS: lane k < topk works choice k out and adds it to the row's
+// slot.  Bound by HBM: the row is read once (not at all where only the chosen
+// logits matter) and written once.
+template <typename T, int L, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const RouteBackwardArgs a) {
-  __shared__ float lds[kRouteWaves][64 * V];
-  const uint32_t lane = threadIdx.x & 63u;
+  constexpr uint32_t TPW = 64 / L;
+  constexpr int N = kUnit<T>;
+  __shared__ __align__(16) float lds[kRouteWaves][TPW][L * V];
+  const uint32_t lane = threadIdx.x & 63u, l = lane % L, sub = lane / L;
   const uint32_t E = (uint32_t)a.r.experts, K = (uint32_t)a.r.topk;
-  const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX;
+  const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX, renorm = a.r.renorm != 0;
   const float inf = __builtin_inff();
-  float* up = lds[wave_id()];
-  for (uint64_t t = (uint64_t)blockIdx.x * kRouteWaves + wave_id(); t < a.tokens;
-       t += (uint64_t)gridDim.x * kRouteWaves) {
+  float* row_up = lds[wave_id()][sub];
+  float* up = row_up + l * V;
+  const uint32_t e0 = l * V, n = E > e0 ? (E - e0 < V ? E - e0 : V) : 0;
+  const bool whole = E % V == 0, full = E == L * V;
+  for (uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW; t0 < a.tokens;
+       t0 += (uint64_t)gridDim.x * kRouteWaves * TPW) {
+    const bool live = t0 + sub < a.tokens;
+    const uint64_t t = live ? t0 + sub : t0;
     const char* row = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
-    char* drow = static_cast<char*>(a.dlogits) + t * a.ld_d * T::kSize;
-    const int32_t id = lane < K ? a.ids[t * K + lane] : -1;
-    const bool have = id >= 0 && (uint32_t)id < E;
-    const float dw = have ? a.dweights[t * K + lane] * a.r.scale : 0.0f;
-    const float cx = have ? load_logit<T>(row, (uint32_t)id) : -inf;
+    float x[V];
+    if (softmax && !renorm) load_elems<T, V>(row, e0, n, whole, full, -inf, x);
+    // the choices of this lane: one, or two where topk is above L
+    constexpr int C = L < SNAC_MAX_TOPK ? 2 : 1;
+    int32_t id[C];
+    bool have[C];
+    float dw[C], cx[C];
 #pragma unroll
-    for (int j = 0; j < V; ++j) up[j * 64 + lane] = 0.0f;
-    if (softmax && !a.r.renorm) {
-      float x[V];
-      float top = -inf;
+    for (int c = 0; c < C; ++c) {
+      const uint32_t k = l + c * L;
+      id[c] = k < K ? a.ids[t * K + k] : -1;
+      have[c] = id[c] >= 0 && (uint32_t)id[c] < E;
+      dw[c] = have[c] ? a.dweights[t * K + k] * a.r.scale : 0.0f;
+      cx[c] = have[c] ? load_logit<T>(row, (uint32_t)id[c]) : -inf;
+    }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t e = j * 64u + lane;
-        x[j] = e < E ? load_logit<T>(row, e) : -inf;
-        top = fmaxf(top, x[j]);
-      }
-      top = wave_max(top);
+    for (int j = 0; j < V; ++j) up[j] = 0.0f;
+    float g[C];  // what goes to the chosen slots
+    float inv = 0.0f, dot = 0.0f, top = -inf;
+    if (softmax && !renorm) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
+      top = lanes_max<L>(top);
       float total = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         x[j] = x[j] == -inf ? 0.0f : expf(x[j] - top);
         total += x[j];
       }
-      total = wave_sum(total);
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit masked
-      const float r = !have || cx == -inf ? 0.0f : expf(cx - top) * inv;
-      const float dot = wave_sum(have ? r * dw : 0.0f);
-      if (have) atomicAdd(&up[id], dw);
+      total = lanes_sum<L>(total);
+      inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit masked
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t e = j * 64u + lane;
-        if (e < E) store_elem<T>(drow + (uint64_t)e * T::kSize, x[j] * inv * (up[e] - dot));
+      for (int c = 0; c < C; ++c) {
+        const float r = !have[c] || cx[c] == -inf ? 0.0f : expf(cx[c] - top) * inv;
+        dot += have[c] ? r * dw[c] : 0.0f;
+        g[c] = dw[c];
       }
+      dot = lanes_sum<L>(dot);
     } else {
-      float g;
-      if (softmax) {
-        const float m = wave_max(cx);
-        const float p = !have || cx == -inf ? 0.0f : expf(cx - m);
-        const float total = wave_sum(p);
-        const float r = total == 0.0f ? 0.0f : p / total;
-        g = r * (dw - wave_sum(have ? r * dw : 0.0f));
-      } else {
-        const float far = 1.0f / (1.0f + expf(cx));
-        if (a.r.renorm) {
-          const float m = fminf(wave_max(cx), 0.0f);
-          const float p = !have || cx == -inf ? 0.0f : m < 0.0f ? expf(cx - m) * far : 1.0f / (1.0f + expf(-cx));
-          const float total = wave_sum(p);
-          const float r = total == 0.0f ? 0.0f : p / total;
-          g = r * far * (dw - wave_sum(have ? r * dw : 0.0f));
-        } else {
-          g = dw * far / (1.0f + expf(-cx));
-        }
-      }
-      if (have) atomicAdd(&up[id], g);
+      float m = cx[0], r[C], total = 0.0f;
+      if constexpr (C == 2) m = fmaxf(m, cx[1]);
+      if (renorm) m = lanes_max<L>(m);
+      if (!softmax) m = fminf(m, 0.0f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t e = j * 64u + lane;
-        if (e < E) store_elem<T>(drow + (uint64_t)e * T::kSize, up[e]);
+      for (int c = 0; c < C; ++c) {
+        r[c] = 0.0f;
+        if (have[c] && cx[c] != -inf)
+          r[c] = softmax || (renorm && m < 0.0f) ? expf(cx[c] - m) : 1.0f / (1.0f + expf(-cx[c]));
+        // the sigmoid's slope is its score times that of -x
+        g[c] = softmax ? 1.0f : 1.0f / (1.0f + expf(cx[c]));
+        if (!softmax && renorm && m < 0.0f) r[c] *= g[c];
+        total += r[c];
       }
+      if (renorm) {
+        total = lanes_sum<L>(total);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          r[c] = total == 0.0f ? 0.0f : r[c] / total;
+          dot += have[c] ? r[c] * dw[c] : 0.0f;
+        }
+        dot = lanes_sum<L>(dot);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) g[c] = r[c] * g[c] * (dw[c] - dot);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (have[c]) atomicAdd(&row_up[id[c]], g[c]);
+    float d[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = up[j];
+    if (softmax && !renorm) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = x[j] * inv * (d[j] - dot);
+    }
+    if (!live) continue;
+    char* p = static_cast<char*>(a.dlogits) + (t * a.ld_d + e0) * T::kSize;
+    bool done = false;
+    if constexpr (V >= N) {
+      if (whole) {
+        if (n) {
+#pragma unroll
+          for (int u = 0; u < V / N; ++u) {
+            float f[N];
+#pragma unroll
+            for (int c = 0; c < N; ++c) f[c] = d[u * N + c];
+            st_unit<false>(p + u * 16, pack<T>(f));
+          }
+        }
+        done = true;
+      }
+    }
+    if (!done) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if ((uint32_t)j < n) store_elem<T>(p + j * T::kSize, d[j]);
     }
   }
 }
@@ -531,7 +664,7 @@ uint32_t group_shift(const snac_router& r, uint32_t V) {
   return ps;
 }
 
-template <typename T, int L, int V, int KB>
+template <typename T, int L, int V, int KB, int KEY>
 bool route_fits(const RouteArgs& a, hipStream_t stream) {
   uint32_t ps = group_shift(a.r, V);
   if (a.r.topk > KB || a.r.topk + 1 > L || (uint64_t)a.r.groups << ps > L) return false;
@@ -540,21 +673,21 @@ bool route_fits(const RouteArgs& a, hipStream_t stream) {
   const uint64_t want = (a.tokens + per - 1) / per;
   const int cus = device_cu_count();
   const uint64_t most = (uint64_t)(cus > 0 ? cus : 1) * 16;
-  hipLaunchKernelGGL((route_kernel<T, L, V, KB>), dim3((uint32_t)(want < most ? want : most)), dim3(kRouteThreads), 0,
-                     stream, a, ps);
+  hipLaunchKernelGGL((route_kernel<T, L, V, KB, KEY>), dim3((uint32_t)(want < most ? want : most)), dim3(kRouteThreads),
+                     0, stream, a, ps, (uint32_t)(a.r.experts / a.r.groups));
   return true;
 }
 
 // The narrowest shape that holds the experts; few tokens take a wave each.
-template <typename T>
+template <typename T, int KEY>
 void route_any(const RouteArgs& a, hipStream_t stream) {
   if (a.tokens >= kRouteManyTokens &&
-      (route_fits<T, 16, 1, 8>(a, stream) || route_fits<T, 16, 4, 8>(a, stream) || route_fits<T, 16, 8, 8>(a, stream) ||
-       route_fits<T, 16, 16, 8>(a, stream) || route_fits<T, 32, 16, 8>(a, stream)))
+      (route_fits<T, 16, 1, 8, KEY>(a, stream) || route_fits<T, 16, 4, 8, KEY>(a, stream) || route_fits<T, 16, 8, 8, KEY>(a, stream) ||
+       route_fits<T, 16, 16, 8, KEY>(a, stream) || route_fits<T, 32, 16, 8, KEY>(a, stream)))
     return;
-  if (route_fits<T, 64, 1, 8>(a, stream) || route_fits<T, 64, 4, 8>(a, stream) || route_fits<T, 64, 16, 8>(a, stream))
+  if (route_fits<T, 64, 1, 8, KEY>(a, stream) || route_fits<T, 64, 4, 8, KEY>(a, stream) || route_fits<T, 64, 16, 8, KEY>(a, stream))
     return;
-  if (route_fits<T, 64, 1, 32>(a, stream) || route_fits<T, 64, 4, 32>(a, stream) || route_fits<T, 64, 16, 32>(a, stream))
+  if (route_fits<T, 64, 1, 32, KEY>(a, stream) || route_fits<T, 64, 4, 32, KEY>(a, stream) || route_fits<T, 64, 16, 32, KEY>(a, stream))
     return;
   const dim3 grid(route_grid(a.tokens)), block(kRouteThreads);
   const int e = a.r.experts;
@@ -563,21 +696,35 @@ void route_any(const RouteArgs& a, hipStream_t stream) {
 }
 
 template <typename T>
+void route_by_key(const RouteArgs& a, hipStream_t stream) {
+  const snac_router& r = a.r;
+  if (!a.bias && (r.groups == 1 || r.group_top == 1 || r.groups == r.experts)) route_any<T, kByLogit>(a, stream);
+  else if (r.score == SNAC_SCORE_SIGMOID) route_any<T, kBySigmoid>(a, stream);
+  else route_any<T, kBySoftmax>(a, stream);
+}
+
+template <typename T, int L, int V>
+void route_backward_in(const RouteBackwardArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((route_backward_kernel<T, L, V>), dim3(route_grid((a.tokens + 64 / L - 1) / (64 / L))),
+                     dim3(kRouteThreads), 0, stream, a);
+}
+
+template <typename T>
 void route_backward_any(const RouteBackwardArgs& a, hipStream_t stream) {
-  const dim3 grid(route_grid(a.tokens)), block(kRouteThreads);
   const int e = a.r.experts;
-  if (e <= 64) hipLaunchKernelGGL((route_backward_kernel<T, 1>), grid, block, 0, stream, a);
-  else if (e <= 128) hipLaunchKernelGGL((route_backward_kernel<T, 2>), grid, block, 0, stream, a);
-  else if (e <= 256) hipLaunchKernelGGL((route_backward_kernel<T, 4>), grid, block, 0, stream, a);
-  else if (e <= 512) hipLaunchKernelGGL((route_backward_kernel<T, 8>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((route_backward_kernel<T, 16>), grid, block, 0, stream, a);
+  if (e <= 16) route_backward_in<T, 16, 1>(a, stream);
+  else if (e <= 64) route_backward_in<T, 16, 4>(a, stream);
+  else if (e <= 128) route_backward_in<T, 16, 8>(a, stream);
+  else if (e <= 256) route_backward_in<T, 32, 8>(a, stream);
+  else if (e <= 512) route_backward_in<T, 64, 8>(a, stream);
+  else route_backward_in<T, 64, 16>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16) route_any<BF16>(a, stream);
-  else route_any<F32>(a, stream);
+  if (bf16) route_by_key<BF16>(a, stream);
+  else route_by_key<F32>(a, stream);
   return hipGetLastError();
 }
 

@@ -112,16 +112,31 @@ def test_token_counts(tokens):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [1, 4])
-def test_keys_one_step_apart(score, groups):
-    """Logits one binary32 step apart, whose scores agree in binary32, and biases that do not part them."""
+@pytest.mark.parametrize("copies", [1, 1200])
+def test_keys_one_step_apart(score, groups, copies):
+    """Logits one binary32 step apart, whose scores agree in binary32, and biases that do not part them; few of them
+    and all, so that the choice is in doubt at its end, inside it and between groups; one token a wave and several."""
     n = 64
     g = np.random.default_rng(3)
     base = np.float32(2.0)
     steps = g.permutation(n)
     x = np.stack([np.float32(base) + steps.astype(np.float32) * np.float32(2.0 ** -22),
                   np.float32(base) - steps.astype(np.float32) * np.float32(2.0 ** -22)])
+    far = g.normal(size=(40, n)) - 3
+    for row in far:  # pairs and threes
+        at = g.permutation(n)[:12].reshape(6, 2)
+        for i, (p, q) in enumerate(at):
+            row[p] = 3 - 0.4 * i
+            row[q] = np.float32(row[p]) + np.float32(2.0 ** -22) * g.integers(-1, 2)
+    x = np.concatenate([x, far]).astype(np.float32)
+    kw = dict(score=score, groups=groups, topk_groups=max(1, groups // 2))
     for bias in (None, np.zeros(n), np.full(n, 0.125)):
-        check(x, 8, "f32", bias=bias, score=score, groups=groups, topk_groups=max(1, groups // 2))
+        check(x, 8, "f32", bias=bias, **kw)
+        if copies > 1:
+            _, w1, ids1 = run(x, 8, "f32", bias=bias, **kw)
+            _, w, ids = run(np.tile(x, (copies // 20, 1)), 8, "f32", bias=bias, **kw)
+            assert (ids.reshape(-1, *ids1.shape) == ids1).all()
+            assert np.abs(w.reshape(-1, *w1.shape) - w1).max() <= 192 * U
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
