@@ -43,129 +43,230 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
   }
 }
 
-// The gradient runs over the sorted positions in chunks of kEmbedChunk.  One
-// wave takes a chunk's 64 units of columns, adds the rows of equal tokens in
+// ------------------------------------------------------------- gradient
+//
+// The sorted positions are cut into chunks of kEmbedChunk.  One wave takes a
+// chunk's slab of columns (a unit a lane), adds the rows of equal tokens in
 // order and writes a run that lies inside the chunk; the sums of the runs
 // that cross its ends go to partial[chunk][0] (begun before it) and [1]
-// (begun in it), and embedding_join_kernel adds those up in order.
-template <typename TG>
-__device__ __forceinline__ void put_row(const EmbedGradArgs& a, uint32_t key, uint32_t first, uint32_t n,
-                                        const float* acc) {
-  // n elements (at most the lane's) at column `first` of row `key`
+// (begun in it), and embedding_join_kernel adds those up in order.  So a
+// token that makes up half the text is spread over as many waves as a
+// hundred rare ones, no atomics are needed, and the order of every sum is
+// fixed by the ids alone.  The work is bound by HBM (dout once, dtable once),
+// so the workgroups that write the zeros of the rows without a token run in
+// between those that read, in the same launch.
+
+// kUnit<T> sums of one lane -> columns first .. first + n of row `key`.
+template <typename T, typename TG, bool ACC>
+__device__ __forceinline__ void put_unit(const EmbedGradArgs& a, uint32_t key, uint32_t first, uint32_t n,
+                                         const float (&acc)[kUnit<T>]) {
+  constexpr uint32_t N = kUnit<T>, NG = kUnit<TG>;
   char* p = a.dtable + (uint64_t)key * a.ld_dtable + (uint64_t)first * TG::kSize;
-  for (uint32_t c = 0; c < n; ++c) {
-    float v = acc[c] * a.scale;
-    if (a.accumulate) v = load_elem<TG>(p + c * TG::kSize) + v;
-    store_elem<TG>(p + c * TG::kSize, v);
-  }
-}
-
-template <typename T, typename TG>
-__global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const EmbedGradArgs a, uint32_t pieces,
-                                                                     uint64_t items) {
-  constexpr uint32_t N = kUnit<T>;
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wide = (a.width + 7u) & ~7u;
-  for (uint64_t it = (uint64_t)blockIdx.x * kEmbWaves + wave_id(); it < items; it += (uint64_t)gridDim.x * kEmbWaves) {
-    const uint32_t chunk = (uint32_t)(it / pieces);
-    const uint32_t first = ((uint32_t)(it - (uint64_t)chunk * pieces) * 64u + lane) * N;
-    const uint32_t left = first < a.width ? a.width - first : 0;
-    const uint32_t n = left < N ? left : N;
-    const uint32_t lo = chunk * kEmbedChunk, hi = a.n - lo < kEmbedChunk ? a.n : lo + kEmbedChunk;
-    uint32_t cur = a.keys[lo];
-    bool head = lo > 0 && a.keys[lo - 1] == cur;
-    float acc[N];
+  // pieces of whole units of the gradient's type, or of half a unit (f32
+  // rows of dout, bf16 gradient)
 #pragma unroll
-    for (uint32_t c = 0; c < N; ++c) acc[c] = 0.0f;
-    auto flush = [&](bool tail) {
-      if (cur >= a.vocab || n == 0) return;
-      if (head || tail) {
-        float* p = a.partial + ((uint64_t)chunk * 2 + (head ? 0 : 1)) * wide + first;
-        for (uint32_t c = 0; c < n; ++c) p[c] = acc[c];
-      } else {
-        put_row<TG>(a, cur, first, n, acc);
+  for (uint32_t c0 = 0; c0 < N; c0 += N < NG ? N : NG) {
+    constexpr uint32_t M = N < NG ? N : NG;
+    if (c0 >= n) return;
+    char* q = p + c0 * TG::kSize;
+    const uint32_t m = n - c0 < M ? n - c0 : M;
+    if (M == NG && m == M) {
+      float f[NG];
+#pragma unroll
+      for (uint32_t c = 0; c < NG; ++c) f[c] = c < M ? acc[c0 + (c < M ? c : 0)] * a.scale : 0.0f;
+      if constexpr (ACC) {
+        float old[NG];
+        unpack<TG>(ld_unit<false>(q), old);
+#pragma unroll
+        for (uint32_t c = 0; c < NG; ++c) f[c] = old[c] + f[c];
       }
-    };
-    for (uint32_t i = lo; i < hi; ++i) {
-      const uint32_t key = a.keys[i];
-      if (key != cur) {
-        flush(false);
-        head = false;
-        cur = key;
+      st_unit<false>(q, pack<TG>(f));
+    } else {
 #pragma unroll
-        for (uint32_t c = 0; c < N; ++c) acc[c] = 0.0f;
+      for (uint32_t c = 0; c < M; ++c) {
+        if (c < m) {
+          float v = acc[c0 + c] * a.scale;
+          if constexpr (ACC) v = load_elem<TG>(q + c * TG::kSize) + v;
+          store_elem<TG>(q + c * TG::kSize, v);
+        }
       }
-      if (key >= a.vocab) break;  // the rest have no gradient
-      const char* p = a.dout + (uint64_t)(uint32_t)a.tokens[i] * a.ld_dout + (uint64_t)first * T::kSize;
-      u32x4 v = {0, 0, 0, 0};
-      if (n == N) v = ld_unit<true>(p);
-      else if (n) v = ld_part<T>(p, n);
-      float f[N];
-      unpack<T>(v, f);
-#pragma unroll
-      for (uint32_t c = 0; c < N; ++c) acc[c] += f[c];
     }
-    flush(hi < a.n && a.keys[hi] == cur);
   }
-}
-
-template <typename TG>
-__global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const EmbedGradArgs a, uint32_t pieces,
-                                                                     uint64_t items) {
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wide = (a.width + 7u) & ~7u;
-  const uint64_t it = (uint64_t)blockIdx.x * kEmbWaves + wave_id();
-  if (it >= items) return;
-  uint32_t chunk = (uint32_t)(it / pieces);
-  const uint32_t col = (uint32_t)(it - (uint64_t)chunk * pieces) * 64u + lane;
-  const uint32_t lo = chunk * kEmbedChunk, hi = lo + kEmbedChunk;
-  if (hi >= a.n) return;
-  const uint32_t key = a.keys[hi - 1];
-  // only where a run begins in this chunk and goes on after it
-  if (key >= a.vocab || a.keys[hi] != key || (a.keys[lo] == key && lo > 0 && a.keys[lo - 1] == key)) return;
-  if (col >= a.width) return;
-  float acc = a.partial[((uint64_t)chunk * 2 + 1) * wide + col];
-  while (true) {
-    ++chunk;
-    acc += a.partial[(uint64_t)chunk * 2 * wide + col];
-    const uint64_t end = ((uint64_t)chunk + 1) * kEmbedChunk;
-    if (end >= a.n || a.keys[end] != key) break;
-  }
-  put_row<TG>(a, key, col, 1, &acc);
 }
 
 // Zeros for the rows that no token names: a workgroup takes kZeroRows rows,
-// finds their part of the sorted keys by bisection and marks those that it
+// finds their part of the sorted keys (64 probes a step) and marks those that it
 // meets.
-constexpr uint32_t kZeroRows = 64;
+constexpr uint32_t kZeroRows = 16;
 
 template <typename TG>
-__global__ __launch_bounds__(kEmbThreads) void embedding_zero_kernel(const EmbedGradArgs a) {
-  __shared__ uint32_t met[kZeroRows];
-  __shared__ uint32_t ends[2];
-  const uint32_t lo = blockIdx.x * kZeroRows;
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, uint32_t lo, uint32_t* met, uint32_t* ends) {
   const uint32_t rows = a.vocab - lo < kZeroRows ? a.vocab - lo : kZeroRows;
   if (threadIdx.x < kZeroRows) met[threadIdx.x] = 0;
-  if (threadIdx.x < 2) {
-    const uint32_t key = lo + (threadIdx.x ? rows : 0);
-    uint32_t b = 0, e = a.n;  // the first position whose key is not below `key`
+  if (wave_id() < 2) {
+    // the first position whose key is not below `key`, 64 probes at a time
+    const uint32_t key = lo + (wave_id() ? rows : 0), lane = threadIdx.x & 63u;
+    uint32_t b = 0, e = a.n;
     while (b < e) {
-      const uint32_t m = b + (e - b) / 2;
-      if (a.keys[m] < key) b = m + 1;
-      else e = m;
+      const uint32_t step = (e - b + 63) / 64;
+      const uint32_t at = b + lane * step;  // lanes whose probe lies past the end answer no
+      const uint32_t below = (uint32_t)__popcll(__ballot(at < e && a.keys[at < e ? at : b] < key));
+      // probes 0 .. below - 1 are below: the answer lies after the last of them
+      if (below == 0) {
+        e = b;
+      } else {
+        e = below < 64 && b + below * step < e ? b + below * step : e;
+        b += (below - 1) * step + 1;
+      }
     }
-    ends[threadIdx.x] = b;
+    if (lane == 0) ends[wave_id()] = b;
   }
   __syncthreads();
   for (uint32_t i = ends[0] + threadIdx.x; i < ends[1]; i += kEmbThreads) met[a.keys[i] - lo] = 1;
   __syncthreads();
-  const u32x4 zero[1] = {u32x4{0, 0, 0, 0}};
-  constexpr uint32_t step = 64u * kUnit<TG>;
+  const u32x4 zero[4] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  constexpr uint32_t step = 64u * 4 * kUnit<TG>;
   for (uint32_t r = wave_id(); r < rows; r += kEmbWaves) {
     if (met[r]) continue;
     char* row = a.dtable + (uint64_t)(lo + r) * a.ld_dtable;
-    for (uint32_t e = 0; e < a.width; e += step) st_piece<TG, 1, true>(row + (uint64_t)e * TG::kSize, a.width - e, zero);
+    for (uint32_t e = 0; e < a.width; e += step) st_piece<TG, 4, true>(row + (uint64_t)e * TG::kSize, a.width - e, zero);
   }
+}
+
+// One chunk's slab of 64 units of columns, by one wave.  WHOLE: all of them
+// exist; the form without their checks is a third of the code, which the
+// unrolled loop repeats for each row.
+template <typename T, typename TG, bool ACC, bool WHOLE>
+__device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk, uint32_t slab) {
+  constexpr uint32_t N = kUnit<T>;
+  static_assert(kEmbedChunk + 2 <= 64, "a lane for each key of a chunk and its neighbours");
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wide = (a.width + 7u) & ~7u;
+  const uint32_t first = (slab * 64u + lane) * N;
+  const uint32_t left = first < a.width ? a.width - first : 0;
+  const uint32_t n = WHOLE ? N : left < N ? left : N;
+  constexpr int kLoads = WHOLE ? kEmbedChunk : 4;  // rows of dout in flight
+  const uint32_t lo = chunk * kEmbedChunk, hi = a.n - lo < kEmbedChunk ? a.n : lo + kEmbedChunk;
+  // lane i: the key and token of position lo + i; lane 62: the key before the
+  // chunk, lane 63: the key after it (`vocab`, no gradient, where there is none)
+  uint32_t my_key = a.vocab, my_token = 0;
+  if (lane < hi - lo) my_key = a.keys[lo + lane], my_token = (uint32_t)a.tokens[lo + lane];
+  if (lane == 62 && lo > 0) my_key = a.keys[lo - 1];
+  if (lane == 63 && hi < a.n) my_key = a.keys[hi];
+  // the positions that have a gradient come first
+  const uint32_t count = (uint32_t)__popcll(__ballot(lane < hi - lo && my_key < a.vocab));
+  if (count == 0) return;
+  auto key_of = [&](uint32_t i) { return (uint32_t)__builtin_amdgcn_readlane((int)my_key, (int)i); };
+  uint32_t cur = key_of(0);
+  bool head = key_of(62) == cur && lo > 0;
+  float acc[N];
+#pragma unroll
+  for (uint32_t c = 0; c < N; ++c) acc[c] = 0.0f;
+  auto flush = [&](bool tail) {
+    if (head || tail) {
+      float* p = a.partial + ((uint64_t)chunk * 2 + (head ? 0 : 1)) * wide + first;
+      // rows of `wide` floats: a lane's columns up to the next multiple of 8
+      if (n) {
+#pragma unroll
+        for (uint32_t c = 0; c < N; c += 4)
+          *reinterpret_cast<u32x4*>(p + c) = u32x4{__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
+                                                   __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3])};
+      }
+    } else {
+      put_unit<T, TG, ACC>(a, cur, first, n, acc);
+    }
+  };
+  const char* col = a.dout + (uint64_t)first * T::kSize;
+  for (uint32_t i0 = 0; i0 < count; i0 += kLoads) {
+    u32x4 v[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const uint32_t i = i0 + j < count ? i0 + j : count - 1;  // past the end: the last row again, not used
+      const char* p = col + (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)my_token, (int)i) * a.ld_dout;
+      if constexpr (WHOLE) {
+        v[j] = ld_unit<true>(p);
+      } else {
+        v[j] = u32x4{0, 0, 0, 0};
+        if (n == N) v[j] = ld_unit<true>(p);
+        else if (n) v[j] = ld_part<T>(p, n);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      if (i0 + j < count) {
+        const uint32_t key = key_of(i0 + j);
+        if (key != cur) {
+          flush(false);
+          head = false;
+          cur = key;
+#pragma unroll
+          for (uint32_t c = 0; c < N; ++c) acc[c] = 0.0f;
+        }
+        float f[N];
+        unpack<T>(v[j], f);
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c) acc[c] += f[c];
+      }
+    }
+  }
+  flush(key_of(63) == cur);
+}
+
+// The first `adds` workgroups add, the rest write zeros as those finish.
+template <typename T, typename TG, bool ACC>
+__global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const EmbedGradArgs a, uint32_t slabs,
+                                                                     uint64_t items, uint32_t adds) {
+  __shared__ uint32_t met[kZeroRows];
+  __shared__ uint32_t ends[2];
+  if (!ACC && blockIdx.x >= adds) {
+    zero_rows<TG>(a, (blockIdx.x - adds) * kZeroRows, met, ends);
+    return;
+  }
+  const uint64_t it = (uint64_t)blockIdx.x * kEmbWaves + wave_id();
+  if (it >= items) return;
+  const uint32_t chunk = (uint32_t)(it / slabs), slab = (uint32_t)(it % slabs);
+  if ((slab + 1) * 64u * kUnit<T> <= a.width) add_chunk<T, TG, ACC, true>(a, chunk, slab);
+  else add_chunk<T, TG, ACC, false>(a, chunk, slab);
+}
+
+// The runs that cross chunks: the chunk that a run begins in adds up its
+// partial sums, a lane for each 4 columns, kJoinLoads rows of them in flight.
+constexpr int kJoinLoads = 16;
+
+template <typename TG, bool ACC>
+__global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const EmbedGradArgs a, uint32_t slabs) {
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wide = (a.width + 7u) & ~7u;
+  const uint32_t chunk = blockIdx.x / slabs;
+  const uint32_t lo = chunk * kEmbedChunk, hi = lo + kEmbedChunk;  // hi < a.n: not the last chunk
+  const uint32_t key = a.keys[hi - 1], next = a.keys[hi], begin = a.keys[lo], prev = a.keys[lo ? lo - 1 : 0];
+  // only where a run begins in this chunk and goes on after it
+  if (key >= a.vocab || next != key || (begin == key && lo > 0 && prev == key)) return;
+  // how many chunks after this one it reaches into
+  uint32_t more = 0;
+  while (true) {
+    const uint64_t end = ((uint64_t)chunk + 2 + more + lane) * kEmbedChunk;  // past the more + lane + 1st
+    const uint64_t on = __ballot(end < a.n && a.keys[end < a.n ? end : 0] == key);
+    more += on == ~0ull ? 64 : (uint32_t)__ffsll((unsigned long long)~on) - 1;
+    if (on != ~0ull) break;
+  }
+  ++more;
+  const uint32_t col = ((blockIdx.x % slabs) * kEmbThreads + threadIdx.x) * 4;
+  if (col >= a.width) return;
+  const float* p = a.partial + (uint64_t)chunk * 2 * wide + col;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  f32x4 acc = *reinterpret_cast<const f32x4*>(p + wide);
+  for (uint32_t m = 1; m <= more; m += kJoinLoads) {
+    f32x4 v[kJoinLoads];
+#pragma unroll
+    for (int j = 0; j < kJoinLoads; ++j)
+      v[j] = *reinterpret_cast<const f32x4*>(p + (uint64_t)(m + j <= more ? m + j : more) * 2 * wide);
+#pragma unroll
+    for (int j = 0; j < kJoinLoads; ++j)
+      if (m + j <= more) acc += v[j];
+  }
+  const float sum[4] = {acc[0], acc[1], acc[2], acc[3]};
+  put_unit<F32, TG, ACC>(a, key, col, a.width - col < 4 ? a.width - col : 4, sum);
 }
 
 uint32_t emb_grid(uint64_t items) {
@@ -183,26 +284,21 @@ hipError_t embedding_any(const EmbeddingArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename T, typename TG>
+template <typename T, typename TG, bool ACC>
 hipError_t embedding_grad_any(const EmbedGradArgs& a, hipStream_t stream) {
-  hipError_t e = hipSuccess;
-  if (!a.accumulate) {
-    hipLaunchKernelGGL((embedding_zero_kernel<TG>), dim3((a.vocab + kZeroRows - 1) / kZeroRows), dim3(kEmbThreads), 0,
-                       stream, a);
-    e = hipGetLastError();
-  }
-  if (e != hipSuccess || a.n == 0) return e;
   const uint32_t chunks = (a.n + kEmbedChunk - 1) / kEmbedChunk;
-  uint32_t pieces = (a.width + 64u * kUnit<T> - 1) / (64u * kUnit<T>);
-  uint64_t items = (uint64_t)chunks * pieces;
-  hipLaunchKernelGGL((embedding_grad_kernel<T, TG>), dim3(emb_grid(items)), dim3(kEmbThreads), 0, stream, a, pieces,
-                     items);
-  e = hipGetLastError();
-  if (e != hipSuccess || chunks == 1) return e;
-  pieces = (a.width + 63u) / 64u;
-  items = (uint64_t)(chunks - 1) * pieces;
-  hipLaunchKernelGGL((embedding_join_kernel<TG>), dim3((uint32_t)((items + kEmbWaves - 1) / kEmbWaves)),
-                     dim3(kEmbThreads), 0, stream, a, pieces, items);
+  uint32_t slabs = (a.width + 64u * kUnit<T> - 1) / (64u * kUnit<T>);
+  const uint64_t items = (uint64_t)chunks * slabs;
+  const uint64_t adds = (items + kEmbWaves - 1) / kEmbWaves;
+  const uint64_t zeros = ACC ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
+  if (adds + zeros == 0) return hipSuccess;
+  if (adds + zeros > 0x7fffffffull) return hipErrorInvalidValue;  // not reached within the documented limits
+  hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC>), dim3((uint32_t)(adds + zeros)), dim3(kEmbThreads), 0, stream, a,
+                     slabs, items, (uint32_t)adds);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || chunks < 2) return e;
+  slabs = (a.width + 4 * kEmbThreads - 1) / (4 * kEmbThreads);
+  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC>), dim3((chunks - 1) * slabs), dim3(kEmbThreads), 0, stream, a, slabs);
   return hipGetLastError();
 }
 
@@ -213,8 +309,13 @@ hipError_t launch_embedding(const EmbeddingArgs& a, bool bf16, hipStream_t strea
 }
 
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, bool bf16, bool grad_bf16, hipStream_t stream) {
-  if (bf16) return grad_bf16 ? embedding_grad_any<BF16, BF16>(a, stream) : embedding_grad_any<BF16, F32>(a, stream);
-  return grad_bf16 ? embedding_grad_any<F32, BF16>(a, stream) : embedding_grad_any<F32, F32>(a, stream);
+  auto go = [&](auto t, auto tg) {
+    using T = decltype(t);
+    using TG = decltype(tg);
+    return a.accumulate ? embedding_grad_any<T, TG, true>(a, stream) : embedding_grad_any<T, TG, false>(a, stream);
+  };
+  if (bf16) return grad_bf16 ? go(BF16{}, BF16{}) : go(BF16{}, F32{});
+  return grad_bf16 ? go(F32{}, BF16{}) : go(F32{}, F32{});
 }
 
 }  // namespace snac

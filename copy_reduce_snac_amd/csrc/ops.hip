@@ -154,7 +154,7 @@ EmbedScratch embed_scratch(uint64_t tokens, uint64_t width) {
     s.items[i] = at, at += arr;
   }
   s.hist = at;
-  at += blocks > 1 ? up256((uint64_t)blocks * (1u << kDigitBits) * 4) : 0;
+  at += up256(sort_hist_words(blocks, 1u << kDigitBits) * 4);
   s.partial = at;
   const uint64_t chunks = (tokens + kEmbedChunk - 1) / kEmbedChunk;
   at += chunks * 2 * ((width + 7) & ~(uint64_t)7) * 4;
@@ -225,8 +225,9 @@ snac_status snac_dispatch_plan(snac_ctx* ctx, const void* ids, int id_bytes, siz
   a.bins = (uint32_t)experts + 1;
   a.mask = 0xffffffffu;
   sort_shape(a.n, &a.blocks, &a.chunk);
+  a.hist_ld = sort_hist_ld(a.blocks);
   char* scratch = nullptr;
-  TRY(ctx_scratch(ctx, a.blocks > 1 ? (uint64_t)a.blocks * a.bins * 4 : 0, "snac_dispatch_plan", &scratch));
+  TRY(ctx_scratch(ctx, sort_hist_words(a.blocks, a.bins) * 4, "snac_dispatch_plan", &scratch));
   a.hist = reinterpret_cast<uint32_t*>(scratch);
   a.counts = counts;
   a.row_of_slot = row_of_slot;
@@ -373,14 +374,15 @@ snac_status snac_embedding_backward(snac_ctx* ctx, const void* dout, size_t ld_d
     a.pad = pad_id;
     a.vocab = vocab;
     a.n = (uint32_t)tokens;
-    a.hist = reinterpret_cast<uint32_t*>(scratch + at.hist);
     sort_shape(a.n, &a.blocks, &a.chunk);
+    a.hist_ld = sort_hist_ld(a.blocks);
     const uint32_t bits = key_bits(vocab), passes = key_passes(vocab);
     const uint32_t digit = (bits + passes - 1) / passes;  // equal digits
     for (uint32_t p = 0; p < passes; ++p) {
       a.shift = p * digit;
       a.mask = (1u << digit) - 1;
       a.bins = 1u << digit;
+      a.hist = reinterpret_cast<uint32_t*>(scratch + at.hist);
       a.key_out = reinterpret_cast<uint32_t*>(scratch + at.keys[p & 1]);
       a.item_out = reinterpret_cast<int32_t*>(scratch + at.items[p & 1]);
       const hipError_t e = launch_sort_pass(a, false, (hipStream_t)stream);

@@ -53,16 +53,17 @@ constexpr uint32_t kSortMaxBins = SNAC_MAX_EXPERTS + 1;
 struct SortArgs {
   // the items' keys: from ids (key = id - first where that is in 0 .. vocab
   // - 1 and id is not pad, else vocab), or from an earlier pass
-  const void* ids;  // nullptr: key_in and item_in
+  const void* ids;
   int32_t id_bytes;
   int64_t first, pad;
   uint64_t vocab;
-  const uint32_t* key_in;
-  const int32_t* item_in;  // nullptr: item i is i
+  const uint32_t* key_in;  // nullptr: from ids, item i being i
+  const int32_t* item_in;
   uint32_t n;
   uint32_t shift, bins;  // bin = (key >> shift) % (mask + 1)
   uint32_t mask;
-  uint32_t* hist;  // [blocks][bins] when blocks > 1
+  uint32_t* hist;    // [bins][hist_ld] when blocks > 1: every run's counts
+  uint32_t hist_ld;  // sort_hist_ld(blocks)
   uint32_t blocks, chunk;
   // outputs of a radix pass
   uint32_t* key_out;
@@ -74,6 +75,8 @@ struct SortArgs {
 };
 // blocks and chunk of a pass over n items
 void sort_shape(uint32_t n, uint32_t* blocks, uint32_t* chunk);
+constexpr uint32_t sort_hist_ld(uint32_t blocks) { return (blocks + 3) & ~3u; }
+uint64_t sort_hist_words(uint32_t blocks, uint32_t bins);  // of one pass
 hipError_t launch_sort_pass(const SortArgs& a, bool plan, hipStream_t stream);
 
 // ------------------------------------------------- dispatch and combine

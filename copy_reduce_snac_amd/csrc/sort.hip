@@ -11,7 +11,16 @@
 // runs (they stay in L2), which costs less than a launch of its own.  In a
 // run each wave owns a contiguous part and its own 16-bit counters, and a
 // lane's rank among equal bins of its wave comes from ballots over the bin's
-// bits, so that the order needs no atomics and is the same every time.
+// bits, so that the order needs no atomics and is the same every time.  (Counting a radix
+// pass's bins with integer atomics while the pass before it places took 19 us
+// more than a launch of sort_hist_kernel, 4.8 us: frequent tokens make them
+// meet.)
+//
+// The passes are bound by latency, launches and first loads: 131072 slots of
+// 256 experts take 4.8 us (counting) and 8.3 us (placing) in 64 runs of 2048;
+// placing took 21 us in 32 runs of 4096 by 1024 threads with the bins'
+// ballots made twice.  The code is kept short (no source of keys but the
+// pass's own is built in), since each launch fetches it anew.
 #include <hip/hip_runtime.h>
 
 #include "ops.hpp"
@@ -20,91 +29,135 @@
 namespace snac {
 namespace {
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kRunThreads = 512;    // several runs
+constexpr int kAloneThreads = 1024;  // one run: the whole sort is one workgroup's
+
+// Where a pass finds its keys: in an earlier pass's output, or from ids of 4
+// or 8 bytes.
+enum : int { kFromKeys = 0, kFromIds4 = 4, kFromIds8 = 8 };
 
 // key of item position i
+template <int FROM>
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i) {
-  if (a.key_in) return a.key_in[i];
-  const int64_t id = load_id(a.ids, a.id_bytes, i);
-  // the difference wraps for far ids; as unsigned it is then no key either
-  const uint64_t k = (uint64_t)id - (uint64_t)a.first;
-  return k < a.vocab && id != a.pad ? (uint32_t)k : (uint32_t)a.vocab;
+  if constexpr (FROM == kFromKeys) {
+    return a.key_in[i];
+  } else {
+    const int64_t id = load_id(a.ids, FROM, i);
+    // the difference wraps for far ids; as unsigned it is then no key either
+    const uint64_t k = (uint64_t)id - (uint64_t)a.first;
+    return k < a.vocab && id != a.pad ? (uint32_t)k : (uint32_t)a.vocab;
+  }
 }
 
-__global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const SortArgs a) {
+__device__ __forceinline__ uint32_t sort_bin(const SortArgs& a, uint32_t key) { return (key >> a.shift) & a.mask; }
+
+template <int FROM>
+__global__ __launch_bounds__(kRunThreads) void sort_hist_kernel(const SortArgs a) {
   __shared__ uint32_t count[kSortMaxBins];
-  for (uint32_t b = threadIdx.x; b < a.bins; b += kSortThreads) count[b] = 0;
+  for (uint32_t b = threadIdx.x; b < a.bins; b += kRunThreads) count[b] = 0;
   __syncthreads();
   const uint32_t lo = blockIdx.x * a.chunk;
   const uint32_t hi = a.n - lo < a.chunk ? a.n : lo + a.chunk;
-  for (uint32_t i = lo + threadIdx.x; i < hi; i += kSortThreads) atomicAdd(&count[(sort_key(a, i) >> a.shift) & a.mask], 1u);
+#pragma unroll 4
+  for (uint32_t i = lo + threadIdx.x; i < hi; i += kRunThreads) atomicAdd(&count[sort_bin(a, sort_key<FROM>(a, i))], 1u);
   __syncthreads();
-  for (uint32_t b = threadIdx.x; b < a.bins; b += kSortThreads) a.hist[(uint64_t)blockIdx.x * a.bins + b] = count[b];
+  for (uint32_t b = threadIdx.x; b < a.bins; b += kRunThreads) a.hist[b * a.hist_ld + blockIdx.x] = count[b];
 }
 
 // Lanes of the wave with the same bin (those with `on` only).
 __device__ __forceinline__ uint64_t same_bin(uint32_t bin, bool on, uint32_t bits) {
-  uint64_t m = __ballot(on);
+  const uint64_t all = __ballot(on);
+  uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
   for (uint32_t b = 0; b < bits; ++b) {
-    const bool set = (bin >> b) & 1u;
-    const uint64_t v = __ballot(set);
-    m &= set ? v : ~v;
+    const uint32_t set = (uint32_t)((int32_t)(bin << (31 - b)) >> 31);  // the bit in all places
+    const uint64_t v = __ballot(set != 0);
+    lo &= ~((uint32_t)v ^ set);
+    hi &= ~((uint32_t)(v >> 32) ^ set);
   }
-  return m;
+  return (uint64_t)hi << 32 | lo;
 }
 
-template <bool PLAN>
-__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs a) {
-  __shared__ uint16_t wave_count[kSortWaves][kSortMaxBins + 1];
-  __shared__ uint32_t base[kSortMaxBins];
-  __shared__ uint32_t scan[kSortWaves + 1];
+// Place of this lane's item among the wave's items of its bin, counting it.
+__device__ __forceinline__ uint32_t place_in_wave(uint16_t* count, uint32_t bin, bool on, uint32_t bits, uint32_t lane) {
+  const uint64_t same = same_bin(bin, on, bits);
+  uint32_t place = 0;
+  if (on) {
+    place = count[bin] + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+    if ((same >> lane) == 1) count[bin] = (uint16_t)(place + 1);  // the last of them
+  }
+  return place;
+}
+
+template <bool PLAN, int TH, int FROM>
+__global__ __launch_bounds__(TH) void sort_place_kernel(const SortArgs a) {
+  constexpr uint32_t W = TH / 64;
+  constexpr uint32_t BINS = kSortMaxBins + 1;  // an even number
+  __shared__ __align__(4) uint16_t wave_count[W][BINS];
+  __shared__ uint32_t base[BINS], early[BINS];
+  __shared__ uint32_t scan[W];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = wave_id();
   const uint32_t bits = 32u - (uint32_t)__clz((int)(a.bins - 1) | 1);
-  for (uint32_t i = tid; i < kSortWaves * (kSortMaxBins + 1); i += kSortThreads) (&wave_count[0][0])[i] = 0;
-  __syncthreads();
   // this wave's part of the run
   const uint32_t lo = blockIdx.x * a.chunk;
   const uint32_t hi = a.n - lo < a.chunk ? a.n : lo + a.chunk;
-  const uint32_t per = ((hi - lo + kSortThreads - 1) / kSortThreads) * 64u;
+  const uint32_t per = ((hi - lo + TH - 1) / TH) * 64u;
   const uint32_t wlo = lo + wave * per < hi ? lo + wave * per : hi;
   const uint32_t whi = hi - wlo < per ? hi : wlo + per;
   uint16_t* mine = wave_count[wave];
-  for (uint32_t i0 = wlo; i0 < whi; i0 += 64) {
-    const bool on = i0 + lane < whi;
-    const uint32_t bin = on ? (sort_key(a, i0 + lane) >> a.shift) & a.mask : 0;
-    const uint64_t same = same_bin(bin, on, bits);
-    if (on && (same >> lane) == 1) mine[bin] = (uint16_t)(mine[bin] + __popcll(same));
-  }
-  __syncthreads();
-  // per bin: counts of the waves before each wave, the run's own total, and
-  // the totals over all runs and over the earlier ones.  Thread i takes bins
-  // 2 i and 2 i + 1 (kSortMaxBins < 2 kSortThreads).
-  uint32_t total[2] = {0, 0}, early[2] = {0, 0};
+  for (uint32_t b = lane; b < BINS / 2; b += 64) reinterpret_cast<uint32_t*>(mine)[b] = 0;
+  // R keys a lane at a time; a wave's part is seldom more, and then they stay
+  constexpr uint32_t R = TH == kAloneThreads ? 8 : 4;
+  uint32_t key[R], place[R];
+  auto load = [&](uint32_t i0) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t b = 2 * tid + h;
-    if (b < a.bins) {
-      uint32_t run = 0;
-      for (int w = 0; w < kSortWaves; ++w) {
-        const uint32_t c = wave_count[w][b];
-        wave_count[w][b] = (uint16_t)run;
-        run += c;
-      }
-      if (a.blocks == 1) {
-        total[h] = run;
-      } else {
-        for (uint32_t k = 0; k < a.blocks; ++k) {
-          const uint32_t c = a.hist[(uint64_t)k * a.bins + b];
-          total[h] += c;
-          early[h] += k < blockIdx.x ? c : 0;
-        }
-      }
+    for (uint32_t r = 0; r < R; ++r) key[r] = i0 + r * 64 + lane < whi ? sort_key<FROM>(a, i0 + r * 64 + lane) : 0;
+  };
+  for (uint32_t i0 = wlo; i0 < whi; i0 += 64 * R) {
+    load(i0);
+#pragma unroll
+    for (uint32_t r = 0; r < R; ++r) {
+      if (i0 + r * 64 >= whi) break;
+      const bool on = i0 + r * 64 + lane < whi;
+      place[r] = place_in_wave(mine, on ? sort_bin(a, key[r]) : 0, on, bits, lane);
     }
   }
-  // exclusive sum of the totals over the bins
-  uint32_t sum = total[0] + total[1];
-  const uint32_t own = sum;
+  // per bin: the totals over all runs and over the earlier ones
+  if (a.blocks > 1) {
+    for (uint32_t b = tid; b < a.bins; b += TH) {
+      const u32x4* h = reinterpret_cast<const u32x4*>(a.hist + (uint64_t)b * a.hist_ld);
+      uint32_t all = 0, bef = 0;
+#pragma unroll 4
+      for (uint32_t k = 0; k < a.blocks; k += 4) {
+        const u32x4 c = h[k / 4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t v = k + i < a.blocks ? c[i] : 0;
+          all += v;
+          bef += k + i < blockIdx.x ? v : 0;
+        }
+      }
+      base[b] = all;
+      early[b] = bef;
+    }
+  }
+  __syncthreads();
+  // and the counts of the waves before each wave
+  for (uint32_t b = tid; b < a.bins; b += TH) {
+    uint32_t run = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < W; ++w) {
+      const uint32_t c = wave_count[w][b];
+      wave_count[w][b] = (uint16_t)run;
+      run += c;
+    }
+    if (a.blocks == 1) base[b] = run, early[b] = 0;
+  }
+  __syncthreads();
+  // exclusive sum of the totals over the bins, `span` neighbours a thread
+  const uint32_t span = (a.bins + TH - 1) / TH;
+  uint32_t own = 0;
+  for (uint32_t b = tid * span; b < (tid + 1) * span && b < a.bins; ++b) own += base[b];
+  uint32_t sum = own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint32_t o = __shfl_up(sum, d);
@@ -112,41 +165,38 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs
   }
   if (lane == 63) scan[wave] = sum;
   __syncthreads();
-  if (tid == 0) {
-    uint32_t run = 0;
-    for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = scan[w];
-      scan[w] = run;
-      run += c;
-    }
+  uint32_t before = sum - own;
+#pragma unroll
+  for (uint32_t w = 0; w < W; ++w) before += w < wave ? scan[w] : 0;
+  for (uint32_t b = tid * span; b < (tid + 1) * span && b < a.bins; ++b) {
+    const uint32_t all = base[b];
+    if (PLAN && blockIdx.x == 0 && b < a.vocab) a.counts[b] = (int32_t)all;
+    base[b] = before + early[b];
+    before += all;
   }
   __syncthreads();
-  const uint32_t before = scan[wave] + sum - own;
-  if (2 * tid < a.bins) base[2 * tid] = before + early[0];
-  if (2 * tid + 1 < a.bins) base[2 * tid + 1] = before + total[0] + early[1];
-  if (PLAN && blockIdx.x == 0) {
-    if (2 * tid < a.vocab) a.counts[2 * tid] = (int32_t)total[0];
-    if (2 * tid + 1 < a.vocab) a.counts[2 * tid + 1] = (int32_t)total[1];
-  }
-  __syncthreads();
-  for (uint32_t i0 = wlo; i0 < whi; i0 += 64) {
-    const uint32_t i = i0 + lane;
-    const bool on = i < whi;
-    const uint32_t key = on ? sort_key(a, i) : 0;
-    const uint32_t bin = (key >> a.shift) & a.mask;
-    const uint64_t same = same_bin(on ? bin : 0, on, bits);
-    if (on) {
-      const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
-      const uint32_t seen = mine[bin];
-      const uint32_t at = base[bin] + seen + rank;
-      if ((same >> lane) == 1) mine[bin] = (uint16_t)(seen + rank + 1);
-      if constexpr (PLAN) {
-        const bool kept = bin < a.vocab;
-        a.row_of_slot[i] = kept ? (int32_t)at : -1;
-        a.slot_of_row[at] = kept ? (int32_t)i : -1;
-      } else {
-        a.key_out[at] = key;
-        a.item_out[at] = a.item_in ? a.item_in[i] : (int32_t)i;
+  // the place in the wave is known from counting; with more than R steps it is
+  // counted again, on from the waves before
+  const bool once = whi - wlo <= 64 * R;
+  for (uint32_t i0 = wlo; i0 < whi; i0 += 64 * R) {
+    if (!once) load(i0);
+#pragma unroll
+    for (uint32_t r = 0; r < R; ++r) {
+      if (i0 + r * 64 >= whi) break;
+      const uint32_t i = i0 + r * 64 + lane;
+      const bool on = i < whi;
+      const uint32_t bin = on ? sort_bin(a, key[r]) : 0;
+      const uint32_t in = once ? mine[bin] + place[r] : place_in_wave(mine, bin, on, bits, lane);
+      if (on) {
+        const uint32_t at = base[bin] + in;
+        if constexpr (PLAN) {
+          const bool kept = bin < a.vocab;
+          a.row_of_slot[i] = kept ? (int32_t)at : -1;
+          a.slot_of_row[at] = kept ? (int32_t)i : -1;
+        } else {
+          a.key_out[at] = key[r];
+          a.item_out[at] = FROM == kFromKeys ? a.item_in[i] : (int32_t)i;
+        }
       }
     }
   }
@@ -154,29 +204,46 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs
 
 }  // namespace
 
-// One run up to 8192 items (one launch); else runs of at least 4096 items,
-// at most 256 of them while a run's items fit the 16-bit counters.
+// One run up to 8192 items (one launch a pass); else runs of 2048 items or,
+// past 256 of them, of as many more as keep to that, while a run's items fit
+// the 16-bit counters.
 void sort_shape(uint32_t n, uint32_t* blocks, uint32_t* chunk) {
   if (n <= 8192) {
     *blocks = 1;
     *chunk = n ? n : 1;
     return;
   }
-  uint32_t c = 4096;
+  uint32_t c = 2048;
   while (c < 32768 && (n + c - 1) / c > 256) c *= 2;
   *chunk = c;
   *blocks = (n + c - 1) / c;
 }
 
-hipError_t launch_sort_pass(const SortArgs& a, bool plan, hipStream_t stream) {
-  if (a.blocks > 1) {
-    hipLaunchKernelGGL(sort_hist_kernel, dim3(a.blocks), dim3(kSortThreads), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+uint64_t sort_hist_words(uint32_t blocks, uint32_t bins) {
+  return blocks > 1 ? (uint64_t)bins * sort_hist_ld(blocks) : 0;
+}
+
+namespace {
+
+template <bool PLAN, int FROM>
+hipError_t sort_pass(const SortArgs& a, hipStream_t stream) {
+  if (a.blocks == 1) {
+    hipLaunchKernelGGL((sort_place_kernel<PLAN, kAloneThreads, FROM>), dim3(1), dim3(kAloneThreads), 0, stream, a);
+    return hipGetLastError();
   }
-  if (plan) hipLaunchKernelGGL((sort_place_kernel<true>), dim3(a.blocks), dim3(kSortThreads), 0, stream, a);
-  else hipLaunchKernelGGL((sort_place_kernel<false>), dim3(a.blocks), dim3(kSortThreads), 0, stream, a);
+  hipLaunchKernelGGL((sort_hist_kernel<FROM>), dim3(a.blocks), dim3(kRunThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((sort_place_kernel<PLAN, kRunThreads, FROM>), dim3(a.blocks), dim3(kRunThreads), 0, stream, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_sort_pass(const SortArgs& a, bool plan, hipStream_t stream) {
+  if (plan) return a.id_bytes == 8 ? sort_pass<true, kFromIds8>(a, stream) : sort_pass<true, kFromIds4>(a, stream);
+  if (a.key_in) return sort_pass<false, kFromKeys>(a, stream);
+  return a.id_bytes == 8 ? sort_pass<false, kFromIds8>(a, stream) : sort_pass<false, kFromIds4>(a, stream);
 }
 
 }  // namespace snac

@@ -110,8 +110,9 @@ snac_status snac_route_backward(const snac_router* router, const void* logits, s
  *   counts       [experts] rows of each expert
  *   row_of_slot  [slots] packed row of each slot, -1 where it is dropped
  *   slot_of_row  [slots] slot of each packed row, -1 past the last one
- * Scratch is the context's staging rings (as in SNAC_REDUCE_ATOMIC), at most
- * 4 * (experts + 1) * slots / 1024 bytes; SNAC_E_ARG if they are smaller.
+ * Scratch is the context's staging rings (as in SNAC_REDUCE_ATOMIC), none up
+ * to 8192 slots and at most 2 KiB * (experts + 1); SNAC_E_ARG if they are
+ * smaller.
  */
 snac_status snac_dispatch_plan(snac_ctx* ctx, const void* ids, int id_bytes, size_t slots, int experts,
                                int32_t* counts, int32_t* row_of_slot, int32_t* slot_of_row, snac_stream stream);
