@@ -14,7 +14,7 @@ Each HIP source is compiled to an object in parallel, then linked into
                                       keep the compiler from forming packed
                                       fp32 instructions;
 * no ``-ffast-math`` and no denormal flushing;
-* ``collectives.hip`` and ``probes.hip`` also get
+* ``collectives.hip``, ``probes.hip`` and ``grads.hip`` also get
   ``-mllvm -amdgpu-atomic-optimizer-strategy=None`` (see SOURCE_FLAGS).
 """
 from __future__ import annotations
@@ -81,13 +81,13 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
-# Per-source flags.  collectives.hip and probes.hip: the compiler's atomic
-# optimizer off.
+# Per-source flags.  collectives.hip, probes.hip and grads.hip: the compiler's
+# atomic optimizer off.
 # It turns an atomic on one address into a wave-wide reduction whose result
 # it waits for at once; the shared tile counter's fetch must instead stay in
 # flight while the current tile moves (TilePool in snac_device.hpp).
 _NO_ATOMIC_OPT = ["-mllvm", "-amdgpu-atomic-optimizer-strategy=None"]
-SOURCE_FLAGS = {"collectives.hip": _NO_ATOMIC_OPT, "probes.hip": _NO_ATOMIC_OPT}
+SOURCE_FLAGS = {"collectives.hip": _NO_ATOMIC_OPT, "probes.hip": _NO_ATOMIC_OPT, "grads.hip": _NO_ATOMIC_OPT}
 
 
 def build(verbose: bool = False) -> str:

@@ -7,6 +7,7 @@
 #include <new>
 #include <vector>
 
+#include "internal.hpp"
 #include "ops.hpp"
 
 using namespace snac;
@@ -14,9 +15,10 @@ using namespace snac;
 struct snac_grads {
   int device;
   uint32_t ntiles;
-  GradTile* tiles;   // device; then the partial sums and the ticket
+  GradTile* tiles;   // device; then the partial sums, the ticket and the counters
   double* partial;   // kGradMaxBlocks
   uint32_t* ticket;  // 0 between calls
+  unsigned long long* pool;  // tile counters of snac_clip_grads, 0 between calls
 };
 
 namespace {
@@ -417,7 +419,7 @@ snac_status snac_grads_init(const void* const* src, void* const* dst, const size
       const Span a = array("dst", d, counts[i] * es, true), b = array("src", src[i], counts[i] * es, false);
       if (overlap(a, b)) return fail(SNAC_E_ARG, "dst[%zu] overlaps src[%zu] (not in place)", i, i);
     }
-    ntiles += (((uintptr_t)src[i] & 15u) + counts[i] * es + kGradTileBytes - 1) / kGradTileBytes;
+    ntiles += (((uintptr_t)d & (kGradAlign - 1)) + counts[i] * es + kGradTileBytes - 1) / kGradTileBytes;
   }
   if (ntiles > 0x7fffffffull) return fail(SNAC_E_ARG, "too many elements in one list");
   snac_grads* g = nullptr;
@@ -430,8 +432,8 @@ snac_status snac_grads_init(const void* const* src, void* const* dst, const size
       const char* s = static_cast<const char*>(src[i]);
       char* d = dst ? static_cast<char*>(dst[i]) : static_cast<char*>(const_cast<void*>(src[i]));
       uint64_t left = counts[i] * es;
-      // the first tile ends on a 16-byte boundary, the others keep to it
-      uint64_t room = kGradTileBytes - ((uintptr_t)s & 15u);
+      // the first tile ends where whole lines begin, the others keep to them
+      uint64_t room = kGradTileBytes - ((uintptr_t)d & (kGradAlign - 1));
       while (left) {
         const uint64_t take = left < room ? left : room;
         tiles.push_back({s, d, (uint32_t)(take / es), dtypes[i] == SNAC_BF16 ? 1u : 0u});
@@ -448,7 +450,8 @@ snac_status snac_grads_init(const void* const* src, void* const* dst, const size
       return hip_fail(e, "hipGetDevice");
     }
     const uint64_t table = up256(tiles.size() * sizeof(GradTile));
-    const uint64_t bytes = table + kGradMaxBlocks * sizeof(double) + 256;
+    const uint64_t words = (kGradCounters + 2) * (uint64_t)kFlagStride;  // the ticket's line, the counters', the done count's
+    const uint64_t bytes = table + kGradMaxBlocks * sizeof(double) + words * 8;
     e = hipMalloc(reinterpret_cast<void**>(&mem), bytes);
     if (e != hipSuccess) {
       delete g;
@@ -460,8 +463,8 @@ snac_status snac_grads_init(const void* const* src, void* const* dst, const size
     g->ticket = reinterpret_cast<uint32_t*>(mem + table + kGradMaxBlocks * sizeof(double));
     if (g->ntiles)
       e = hipMemcpyAsync(mem, tiles.data(), tiles.size() * sizeof(GradTile), hipMemcpyHostToDevice, (hipStream_t)stream);
-    const uint32_t zero = 0;
-    if (e == hipSuccess) e = hipMemcpyAsync(g->ticket, &zero, sizeof zero, hipMemcpyHostToDevice, (hipStream_t)stream);
+    g->pool = reinterpret_cast<unsigned long long*>(g->ticket) + kFlagStride;
+    if (e == hipSuccess) e = fill_u64(reinterpret_cast<uint64_t*>(g->ticket), words, 0, (hipStream_t)stream);
     if (e == hipSuccess) e = hipStreamSynchronize((hipStream_t)stream);
     if (e != hipSuccess) {
       (void)hipFree(mem);
@@ -508,7 +511,7 @@ snac_status snac_grad_norm(snac_grads* grads, float* norm, snac_stream stream) {
 snac_status snac_clip_grads(snac_grads* grads, const float* norm, float max_norm, snac_stream stream) {
   TRY(check_max_norm(max_norm));
   TRY(check_grads(grads, norm));
-  const hipError_t e = launch_clip(grads->tiles, grads->ntiles, norm, max_norm, (hipStream_t)stream);
+  const hipError_t e = launch_clip(grads->tiles, grads->ntiles, norm, max_norm, grads->pool, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_clip_grads launch");
 }
 

@@ -167,9 +167,14 @@ struct GradTile {
   uint32_t bf16;
 };
 constexpr uint32_t kGradTileBytes = 16384;
+constexpr uint32_t kGradAlign = 256;  // tiles of a tensor begin on such addresses, but the first
 constexpr uint32_t kGradMaxBlocks = 2048;
 hipError_t launch_grad_norm(const GradTile* tiles, uint32_t ntiles, double* partial, uint32_t* ticket, float* norm,
                             hipStream_t stream);
-hipError_t launch_clip(const GradTile* tiles, uint32_t ntiles, const float* norm, float max_norm, hipStream_t stream);
+// `pool`: kGradCounters zeroed counters and a done count, kFlagStride words
+// apart; a launch leaves them zeroed.
+constexpr uint32_t kGradCounters = 4;
+hipError_t launch_clip(const GradTile* tiles, uint32_t ntiles, const float* norm, float max_norm,
+                       unsigned long long* pool, hipStream_t stream);
 
 }  // namespace snac

@@ -44,19 +44,27 @@ __device__ __forceinline__ u32x4 pack(const float (&f)[kUnit<T>]) {
   return w;
 }
 
+// The pointers are to global memory and say so: one that was itself loaded
+// from memory would otherwise be accessed as a flat address, whose loads also
+// wait for LDS.
+template <typename U>
+using global_ptr = __attribute__((address_space(1))) U*;
+
 template <bool NT>
 __device__ __forceinline__ u32x4 ld_unit(const char* p) {
+  const auto g = (global_ptr<const u32x4_a2>)(p);
   if constexpr (NT)
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+    return __builtin_nontemporal_load(g);
   else
-    return *reinterpret_cast<const u32x4_a2*>(p);
+    return *g;
 }
 template <bool NT>
 __device__ __forceinline__ void st_unit(char* p, u32x4 v) {
+  const auto g = (global_ptr<u32x4_a2>)(p);
   if constexpr (NT)
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
+    __builtin_nontemporal_store(v, g);
   else
-    *reinterpret_cast<u32x4_a2*>(p) = v;
+    *g = v;
 }
 
 // The first `n` (0 < n < a unit) elements of a row's last unit; the others

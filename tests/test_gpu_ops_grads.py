@@ -86,6 +86,36 @@ def test_norm_and_clip(torch, which, where, clips):
     lst.close()
 
 
+@pytest.mark.parametrize("where", ["in place", "apart"])
+def test_large_list(torch, where):
+    """Enough tiles for the counters that hand them out (128 MiB on 256 CUs), three calls in a row: whole outputs, in
+    binary64 on the GPU."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    sizes = [(50_000_003, torch.bfloat16, 3), (17, torch.float32, 1), (40_000_001, torch.float32, 5),
+             (9_000_000, torch.bfloat16, 0)]
+    bufs = [torch.empty(n + 16, dtype=d, device="cuda").normal_(generator=g) for n, d, _ in sizes]
+    ts = [b[o:o + n] for b, (n, _, o) in zip(bufs, sizes)]
+    obufs = bufs if where == "in place" else [torch.full_like(b, 77.0) for b in bufs]
+    outs = ts if where == "in place" else [b[o + 1:o + 1 + n] for b, (n, _, o) in zip(obufs, sizes)]
+    lst = ops().GradList(ts, None if where == "in place" else outs)
+    norm = torch.empty(1, device="cuda")
+    for _ in range(3):
+        xs = [t.clone() for t in ts]
+        want = float(sum(x.double().square().sum() for x in xs)) ** 0.5
+        max_norm = float(np.float32(want / 2))
+        ops().clip_grad_norm(lst, max_norm, norm)
+        assert abs(float(norm) - want) <= 1.01 * U * want
+        for x, y in zip(xs, outs):
+            e = x.double() * (max_norm / (want + 1e-6))
+            half = ref.half_step("bf16" if x.dtype == torch.bfloat16 else "f32")
+            assert bool(((y.double() - e).abs() <= (5 * U + half) * e.abs() * 1.01 + 1e-37).all())
+        if where == "apart":
+            assert all(torch.equal(t, x) for t, x in zip(ts, xs))
+            assert all(bool((b[:o + 1] == 77).all()) and bool((b[o + 1 + n:] == 77).all())
+                       for b, (n, _, o) in zip(obufs, sizes))
+
+
 def test_empty_list(torch):
     norm = torch.full((1,), 9.0, device="cuda")
     for ts in ([], [torch.empty(0, device="cuda")]):
