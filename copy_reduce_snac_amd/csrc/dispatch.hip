@@ -3,9 +3,13 @@
 // snac_combine_backward in include/snac_ops.h).
 //
 // All three move rows and are bound by HBM.  A wave takes one piece of one
-// token's row (kPieceUnits units of 16 bytes a lane) and walks the token's
-// topk slots, so that a token's row is read once (dispatch) or written once
-// (combine), and its slots' rows are whole lines each.
+// token's row (U units of 16 bytes a lane) and walks the token's topk slots,
+// so that a token's row is read once (dispatch) or written once (combine), and
+// its slots' rows are whole lines each.  Rows that are used once stream
+// (stores that stay in the caches: 130 us for 115, 121 for 103).  16384 tokens,
+// rows of 4 KiB: dispatch to 8 rows 100 us (5.9 TB/s), combine of 8 rows 101 us
+// (6.0 TB/s; two or four rows in flight at a time 102 to 104), combine_backward
+// of 4 rows 95 us (6.1 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "ops.hpp"
@@ -16,56 +20,56 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kPieceUnits = 4;
+constexpr int kPieceUnits = 4;  // of combine_backward, and of the others' large calls
 
-template <typename T>
-constexpr uint32_t kPieceElems = 64u * kPieceUnits * kUnit<T>;
+template <typename T, int U>
+constexpr uint32_t kPieceElems = 64u * U * kUnit<T>;
 
-template <typename T>
+template <typename T, int U>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const DispatchArgs a, uint32_t pieces, uint64_t items) {
   for (uint64_t it = (uint64_t)blockIdx.x * kRowWaves + wave_id(); it < items; it += (uint64_t)gridDim.x * kRowWaves) {
     const uint64_t t = it / pieces;
-    const uint32_t first = (uint32_t)(it - t * pieces) * kPieceElems<T>;
+    const uint32_t first = (uint32_t)(it - t * pieces) * kPieceElems<T, U>;
     const uint64_t off = (uint64_t)first * T::kSize;
-    u32x4 v[kPieceUnits];
-    ld_piece<T, kPieceUnits, false>(a.x + t * a.ld_x + off, a.width - first, v);
+    u32x4 v[U];
+    ld_piece<T, U, false>(a.x + t * a.ld_x + off, a.width - first, v);
     for (int32_t k = 0; k < a.topk; ++k) {
       const uint32_t row = uniform((uint32_t)a.row_of_slot[t * a.topk + k]);
-      if (row < a.rows) st_piece<T, kPieceUnits, true>(a.out + (uint64_t)row * a.ld_out + off, a.width - first, v);
+      if (row < a.rows) st_piece<T, U, true>(a.out + (uint64_t)row * a.ld_out + off, a.width - first, v);
     }
   }
 }
 
-template <typename T>
+template <typename T, int U>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const CombineArgs a, uint32_t pieces, uint64_t items) {
   constexpr uint32_t N = kUnit<T>;
   for (uint64_t it = (uint64_t)blockIdx.x * kRowWaves + wave_id(); it < items; it += (uint64_t)gridDim.x * kRowWaves) {
     const uint64_t t = it / pieces;
-    const uint32_t first = (uint32_t)(it - t * pieces) * kPieceElems<T>;
+    const uint32_t first = (uint32_t)(it - t * pieces) * kPieceElems<T, U>;
     const uint64_t off = (uint64_t)first * T::kSize;
-    float acc[kPieceUnits][N];
+    float acc[U][N];
 #pragma unroll
-    for (int j = 0; j < kPieceUnits; ++j)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c) acc[j][c] = 0.0f;
     for (int32_t k = 0; k < a.topk; ++k) {
       const uint32_t row = uniform((uint32_t)a.row_of_slot[t * a.topk + k]);
       if (row >= a.rows) continue;
       const float w = a.weights ? a.weights[t * a.topk + k] : 1.0f;
-      u32x4 v[kPieceUnits];
-      ld_piece<T, kPieceUnits, true>(a.y + (uint64_t)row * a.ld_y + off, a.width - first, v);
+      u32x4 v[U];
+      ld_piece<T, U, true>(a.y + (uint64_t)row * a.ld_y + off, a.width - first, v);
 #pragma unroll
-      for (int j = 0; j < kPieceUnits; ++j) {
+      for (int j = 0; j < U; ++j) {
         float f[N];
         unpack<T>(v[j], f);
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c) acc[j][c] = __builtin_fmaf(w, f[c], acc[j][c]);
       }
     }
-    u32x4 v[kPieceUnits];
+    u32x4 v[U];
 #pragma unroll
-    for (int j = 0; j < kPieceUnits; ++j) v[j] = pack<T>(acc[j]);
-    st_piece<T, kPieceUnits, true>(a.out + t * a.ld_out + off, a.width - first, v);
+    for (int j = 0; j < U; ++j) v[j] = pack<T>(acc[j]);
+    st_piece<T, U, true>(a.out + t * a.ld_out + off, a.width - first, v);
   }
 }
 
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const Com
     const char* y = a.y + (uint64_t)row * a.ld_y;
     char* dy = a.dy + (uint64_t)row * a.ld_dy;
     float dot = 0.0f;
-    for (uint32_t e = 0; e < a.width; e += kPieceElems<T>) {
+    for (uint32_t e = 0; e < a.width; e += kPieceElems<T, kPieceUnits>) {
       const uint64_t off = (uint64_t)e * T::kSize;
       u32x4 vg[kPieceUnits], vy[kPieceUnits];
       ld_piece<T, kPieceUnits, false>(g + off, a.width - e, vg);
@@ -112,28 +116,48 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const Com
   }
 }
 
-// workgroups for `items` waves of work, grid-stride past 16 a CU
+// Workgroups for `items` waves of work: one item a wave (grid-stride only past
+// 2^22 workgroups).  combine_backward of 65536 rows of 4 KiB: 95 us, against
+// 103, 107 and 102 with 16, 8 and 4 workgroups a CU striding over the items.
 uint32_t row_grid(uint64_t items) {
-  const int cus = device_cu_count();
-  const uint64_t most = (uint64_t)(cus > 0 ? cus : 1) * 16;
   const uint64_t want = (items + kRowWaves - 1) / kRowWaves;
-  return (uint32_t)(want < most ? want : most);
+  return (uint32_t)(want < (1u << 22) ? want : 1u << 22);
+}
+
+// Pieces of a row for `tokens` rows of `width` elements: of kPieceUnits units,
+// or of one where those would leave SIMDs without a wave (4 a CU): 64 tokens,
+// 8 rows of 16 KiB each, took 8.3 us with one and 10 with four.
+template <typename T>
+bool small_pieces(uint64_t tokens, uint32_t width) {
+  const int cus = device_cu_count();
+  const uint32_t pieces = (width + kPieceElems<T, kPieceUnits> - 1) / kPieceElems<T, kPieceUnits>;
+  return tokens < (uint64_t)(cus > 0 ? cus : 1) * 4 && tokens * pieces < (uint64_t)(cus > 0 ? cus : 1) * 4;
+}
+
+template <typename T, int U>
+hipError_t dispatch_in(const DispatchArgs& a, hipStream_t stream) {
+  const uint32_t pieces = (a.width + kPieceElems<T, U> - 1) / kPieceElems<T, U>;
+  const uint64_t items = a.tokens * pieces;
+  hipLaunchKernelGGL((dispatch_kernel<T, U>), dim3(row_grid(items)), dim3(kRowThreads), 0, stream, a, pieces, items);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t dispatch_any(const DispatchArgs& a, hipStream_t stream) {
-  const uint32_t pieces = (a.width + kPieceElems<T> - 1) / kPieceElems<T>;
+  return small_pieces<T>(a.tokens, a.width) ? dispatch_in<T, 1>(a, stream) : dispatch_in<T, kPieceUnits>(a, stream);
+}
+
+template <typename T, int U>
+hipError_t combine_in(const CombineArgs& a, hipStream_t stream) {
+  const uint32_t pieces = (a.width + kPieceElems<T, U> - 1) / kPieceElems<T, U>;
   const uint64_t items = a.tokens * pieces;
-  hipLaunchKernelGGL((dispatch_kernel<T>), dim3(row_grid(items)), dim3(kRowThreads), 0, stream, a, pieces, items);
+  hipLaunchKernelGGL((combine_kernel<T, U>), dim3(row_grid(items)), dim3(kRowThreads), 0, stream, a, pieces, items);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t combine_any(const CombineArgs& a, hipStream_t stream) {
-  const uint32_t pieces = (a.width + kPieceElems<T> - 1) / kPieceElems<T>;
-  const uint64_t items = a.tokens * pieces;
-  hipLaunchKernelGGL((combine_kernel<T>), dim3(row_grid(items)), dim3(kRowThreads), 0, stream, a, pieces, items);
-  return hipGetLastError();
+  return small_pieces<T>(a.tokens, a.width) ? combine_in<T, 1>(a, stream) : combine_in<T, kPieceUnits>(a, stream);
 }
 
 template <typename T>

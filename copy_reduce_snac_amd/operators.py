@@ -46,19 +46,18 @@ def _ids(t, what: str) -> int:
 
 
 def _device(what: str, *ts) -> None:
-    dev = ts[0].device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensors must be on the current device, not on {dev}")
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: every tensor must be on {dev}")
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{what}: every tensor must be on the current device, not on {t.device}")
 
 
 def _matrix(t, what: str) -> int:
     """Row stride of a matrix with contiguous rows."""
-    if t.dim() != 2:
-        raise ValueError(f"{what} must have two dimensions, not {t.dim()}")
-    rows, width = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have two dimensions, not {len(shape)}")
+    rows, width = shape
     ld, step = t.stride()
     if step != 1 and width > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
@@ -70,7 +69,7 @@ def _matrix(t, what: str) -> int:
 
 
 def _packed(t, shape, dtype, what: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
@@ -212,7 +211,7 @@ def embedding(table, ids, out, *, first: int = 0, scale: float = 1.0, stream=Non
 
 def _tokens(ids, rows, width: int, what: str, name: str):
     """Number of ids, and the row stride of the tensor with a row for each."""
-    if tuple(rows.shape) != (*ids.shape, width):
+    if rows.shape != (*ids.shape, width):
         raise ValueError(f"{what}: {name} must have shape {(*ids.shape, width)}, not {tuple(rows.shape)}")
     if not ids.is_contiguous():
         raise ValueError(f"{what}: ids must be contiguous")

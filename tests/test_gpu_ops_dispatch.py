@@ -117,7 +117,7 @@ def test_plan_without_room(torch):
 
 
 # tokens, topk, width, column shifts of x and out, columns after them
-SHAPES = [(1, 1, 1, 0, 0), (1, 8, 2048, 0, 0), (3, 2, 7, 1, 2), (5, 3, 8, 0, 8), (33, 4, 515, 3, 2), (17, 8, 1030, 0, 2),
+SHAPES = [(1, 1, 1, 0, 0), (300, 3, 8195, 1, 2), (1, 8, 2048, 0, 0), (3, 2, 7, 1, 2), (5, 3, 8, 0, 8), (33, 4, 515, 3, 2), (17, 8, 1030, 0, 2),
           (9, 32, 64, 0, 0), (40, 2, 2049, 1, 0), (6, 1, 8192, 0, 0), (2000, 4, 100, 0, 4), (11, 5, 4097, 2, 1)]
 
 

@@ -65,7 +65,7 @@ def far_ids(ids, id_type):
 
 
 # tokens, vocab, first, width, column shifts
-SHAPES = [(1, 1, 0, 1, 0), (1, 50, 3, 2048, 0), (5, 7, 100, 9, 1), (64, 33, 0, 515, 3), (300, 1000, 0, 64, 0),
+SHAPES = [(1, 1, 0, 1, 0), (400, 50, 9, 8195, 1), (1, 50, 3, 2048, 0), (5, 7, 100, 9, 1), (64, 33, 0, 515, 3), (300, 1000, 0, 64, 0),
           (1000, 40, 20, 130, 2), (20, 300, 7, 8192, 0), (40, 64, 0, 2050, 0)]
 
 
