@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr float kLog2e = 1.44269504f;
 constexpr uint64_t kRouteManyTokens = 2048;
 constexpr int kMoreRounds = 3;  // choices looked at past the next one, where two are too near
 
@@ -274,7 +275,7 @@ enum : int { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 //     scaling by at most S 2^-24 each, cutting by one step: two keys by 12 or
 //     37 steps at QB = 24.
 template <typename T, int L, int V, int KB, int KEY>
-__global__ __launch_bounds__(kRouteThreads, V <= 8 ? 6 : L == 16 ? 4 : 1) void route_kernel(const RouteArgs a, const uint32_t ps, const uint32_t gs) {
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a, const uint32_t ps, const uint32_t gs) {
   constexpr uint32_t TPW = 64 / L;
   constexpr uint32_t IB = __builtin_ctz(L * V), QB = IB < 8 ? 24 : 32 - IB, QMAX = (1u << QB) - 1;
   constexpr int VX = L * V <= 64 ? 1 : L * V / 64;
@@ -283,7 +284,6 @@ __global__ __launch_bounds__(kRouteThreads, V <= 8 ? 6 : L == 16 ? 4 : 1) void r
   const bool softmax = KEY == kBySoftmax || (KEY == kByLogit && a.r.score == SNAC_SCORE_SOFTMAX);
   constexpr bool by_logit = KEY == kByLogit;
   const float inf = __builtin_inff();
-  constexpr float log2e = 1.44269504f;
   // the lane's experts
   const uint32_t g = l >> ps, in = (l & ((1u << ps) - 1)) * V;
   const uint32_t e0 = g * gs + in, n = g >= G || in >= gs ? 0 : gs - in < V ? gs - in : V;
@@ -304,234 +304,235 @@ __global__ __launch_bounds__(kRouteThreads, V <= 8 ? 6 : L == 16 ? 4 : 1) void r
     return Choice{won ? (int32_t)id : -1, won ? load_logit<T>(row, id) : -inf, won && a.bias ? a.bias[id] : 0.0f};
   };
 
-  for (uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW; t0 < a.tokens;
-       t0 += (uint64_t)gridDim.x * kRouteWaves * TPW) {
-    const uint64_t t = t0 + sub;
-    const bool live = t < a.tokens;
-    const char* row = static_cast<const char*>(a.logits) + (live ? t : t0) * a.ld * T::kSize;
-    float x[V];
-    load_elems<T, V>(row, e0, n, whole, full, -inf, x);
-    bool doubt = false;
-    float top = -inf;
+  const uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW;
+  if (t0 >= a.tokens) return;
+  const uint64_t t = t0 + sub;
+  const bool live = t < a.tokens;
+  const char* row = static_cast<const char*>(a.logits) + (live ? t : t0) * a.ld * T::kSize;
+  float x[V];
+  load_elems<T, V>(row, e0, n, whole, full, -inf, x);
+  bool doubt = false;
+  float top = -inf;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    doubt |= x[j] != x[j];
+    top = fmaxf(top, x[j]);
+  }
+  top = lanes_max<L>(top);
+  doubt |= top == inf;
+  auto score64 = [&](float x, float b) {
+    const double s = softmax ? exp((double)x - (double)top) : 1.0 / (1.0 + exp(-(double)x));
+    return by_logit ? s : s + (double)b;
+  };
+  float total = 0.0f;  // softmax: sum of exp(x - top)
+  if (softmax && !(by_logit && a.r.renorm)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
+    total = lanes_sum<L>(total);
+  }
+  uint32_t key[V];
+  uint32_t tol = 0;
+  if constexpr (by_logit) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      doubt |= x[j] != x[j];
-      top = fmaxf(top, x[j]);
+      const uint32_t q = (0x7fffffffu - __float_as_uint(top - x[j])) >> (31 - QB);
+      key[j] = x[j] == -inf ? 0 : q << IB | (L * V - 1 - (l * V + j));
     }
-    top = lanes_max<L>(top);
-    doubt |= top == inf;
-    auto score64 = [&](float x, float b) {
-      const double s = softmax ? exp((double)x - (double)top) : 1.0 / (1.0 + exp(-(double)x));
-      return by_logit ? s : s + (double)b;
+  } else {
+    float v[V];
+    float best = -inf;
+    const float inv = 1.0f / total;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float s = softmax ? __builtin_amdgcn_exp2f((x[j] - top) * kLog2e) * inv
+                              : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x[j]));
+      v[j] = x[j] == -inf ? -inf : s + b[j];
+      doubt |= v[j] != v[j];
+      best = fmaxf(best, v[j]);
+    }
+    best = lanes_max<L>(best);
+    doubt |= best == inf;
+    const float most = softmax ? inv : 1.0f;  // the largest score
+    const float scale = (float)(1u << (QB - 1)) / fmaxf(fabsf(best), most);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t d = (uint32_t)fminf((best - v[j]) * scale, (float)(QMAX - 1));
+      key[j] = v[j] == -inf ? 0 : (QMAX - d) << IB | (L * V - 1 - (l * V + j));
+    }
+    tol = ((softmax ? 37u : 12u) >> (24 - QB)) + (QB < 24);
+  }
+  sort_down<V>(key);
+  if (G > 1) {
+    // the group's two largest keys, over its lanes
+    uint32_t m0 = key[0], m1 = V > 1 ? key[V > 1 ? 1 : 0] : 0;
+    auto merge = [&](auto d) {
+      constexpr int D = decltype(d)::value;
+      uint32_t o0, o1;
+      if constexpr (D <= 8) {
+        constexpr int C = D == 1 ? kDppXor1 : D == 2 ? kDppXor2 : D == 4 ? kDppHalfMirror : kDppMirror;
+        o0 = dpp<C>(m0), o1 = dpp<C>(m1);
+      } else if constexpr (D == 16) {
+        const auto r0 = __builtin_amdgcn_permlane16_swap(m0, m0, false, false);
+        const auto r1 = __builtin_amdgcn_permlane16_swap(m1, m1, false, false);
+        m0 = r0[0], o0 = r0[1], m1 = r1[0], o1 = r1[1];
+      } else {
+        const auto r0 = __builtin_amdgcn_permlane32_swap(m0, m0, false, false);
+        const auto r1 = __builtin_amdgcn_permlane32_swap(m1, m1, false, false);
+        m0 = r0[0], o0 = r0[1], m1 = r1[0], o1 = r1[1];
+      }
+      const uint32_t lo = m0 < o0 ? m0 : o0, hi = m1 > o1 ? m1 : o1;
+      m0 = m0 > o0 ? m0 : o0;
+      m1 = lo > hi ? lo : hi;
     };
-    float total = 0.0f;  // softmax: sum of exp(x - top)
-    if (softmax && !(by_logit && a.r.renorm)) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : __builtin_amdgcn_exp2f((x[j] - top) * log2e);
-      total = lanes_sum<L>(total);
+    if (ps > 0) merge(std::integral_constant<int, 1>{});
+    if (ps > 1) merge(std::integral_constant<int, 2>{});
+    if (ps > 2) merge(std::integral_constant<int, 4>{});
+    if (ps > 3) merge(std::integral_constant<int, 8>{});
+    if (L > 16 && ps > 4) merge(std::integral_constant<int, 16>{});
+    const bool two = a.r.group_top == 2 && gs > 1;
+    uint32_t worth = m0 >> IB;
+    if (two) worth = m1 ? worth + (m1 >> IB) : 0;
+    const bool cut = !by_logit && ((m0 >> IB) == 1 || (two && (m1 >> IB) == 1));
+    const uint32_t mine = worth && g < G ? worth << 6 | (63 - g) : 0;
+    // the topk_groups-th largest, and the next
+    uint32_t left = mine, last = 0, next = 0;
+    for (uint32_t k = 0; k < (uint32_t)a.r.topk_groups; ++k) {
+      last = lanes_max<L>(left);
+      left = left == last ? 0 : left;
     }
-    uint32_t key[V];
-    uint32_t tol = 0;
-    if constexpr (by_logit) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t q = (0x7fffffffu - __float_as_uint(top - x[j])) >> (31 - QB);
-        key[j] = x[j] == -inf ? 0 : q << IB | (L * V - 1 - (l * V + j));
-      }
-    } else {
-      float v[V];
-      float best = -inf;
-      const float inv = 1.0f / total;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float s = softmax ? __builtin_amdgcn_exp2f((x[j] - top) * log2e) * inv
-                                : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-log2e * x[j]));
-        v[j] = x[j] == -inf ? -inf : s + b[j];
-        doubt |= v[j] != v[j];
-        best = fmaxf(best, v[j]);
-      }
-      best = lanes_max<L>(best);
-      doubt |= best == inf;
-      const float most = softmax ? inv : 1.0f;  // the largest score
-      const float scale = (float)(1u << (QB - 1)) / fmaxf(fabsf(best), most);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t d = (uint32_t)fminf((best - v[j]) * scale, (float)(QMAX - 1));
-        key[j] = v[j] == -inf ? 0 : (QMAX - d) << IB | (L * V - 1 - (l * V + j));
-      }
-      tol = ((softmax ? 37u : 12u) >> (24 - QB)) + (QB < 24);
-    }
-    sort_down<V>(key);
-    if (G > 1) {
-      // the group's two largest keys, over its lanes
-      uint32_t m0 = key[0], m1 = V > 1 ? key[V > 1 ? 1 : 0] : 0;
-      auto merge = [&](auto d) {
-        constexpr int D = decltype(d)::value;
-        uint32_t o0, o1;
-        if constexpr (D <= 8) {
-          constexpr int C = D == 1 ? kDppXor1 : D == 2 ? kDppXor2 : D == 4 ? kDppHalfMirror : kDppMirror;
-          o0 = dpp<C>(m0), o1 = dpp<C>(m1);
-        } else if constexpr (D == 16) {
-          const auto r0 = __builtin_amdgcn_permlane16_swap(m0, m0, false, false);
-          const auto r1 = __builtin_amdgcn_permlane16_swap(m1, m1, false, false);
-          m0 = r0[0], o0 = r0[1], m1 = r1[0], o1 = r1[1];
-        } else {
-          const auto r0 = __builtin_amdgcn_permlane32_swap(m0, m0, false, false);
-          const auto r1 = __builtin_amdgcn_permlane32_swap(m1, m1, false, false);
-          m0 = r0[0], o0 = r0[1], m1 = r1[0], o1 = r1[1];
-        }
-        const uint32_t lo = m0 < o0 ? m0 : o0, hi = m1 > o1 ? m1 : o1;
-        m0 = m0 > o0 ? m0 : o0;
-        m1 = lo > hi ? lo : hi;
-      };
-      if (ps > 0) merge(std::integral_constant<int, 1>{});
-      if (ps > 1) merge(std::integral_constant<int, 2>{});
-      if (ps > 2) merge(std::integral_constant<int, 4>{});
-      if (ps > 3) merge(std::integral_constant<int, 8>{});
-      if (L > 16 && ps > 4) merge(std::integral_constant<int, 16>{});
-      const bool two = a.r.group_top == 2 && gs > 1;
-      uint32_t worth = m0 >> IB;
-      if (two) worth = m1 ? worth + (m1 >> IB) : 0;
-      const bool cut = !by_logit && ((m0 >> IB) == 1 || (two && (m1 >> IB) == 1));
-      const uint32_t mine = worth && g < G ? worth << 6 | (63 - g) : 0;
-      // the topk_groups-th largest, and the next
-      uint32_t left = mine, last = 0, next = 0;
-      for (uint32_t k = 0; k < (uint32_t)a.r.topk_groups; ++k) {
-        last = lanes_max<L>(left);
-        left = left == last ? 0 : left;
-      }
-      next = lanes_max<L>(left);
-      bool kept = mine && mine >= last;
-      const bool near = last && next && (last >> 6) - (next >> 6) <= 2 * tol;
-      if (__any(near && live)) {
-        if constexpr (KEY == kBySoftmax) {
-          doubt |= near;
-        } else {
-          // by the worths in binary64, every lane its own group's; the keys
-          // that they sum have to be clear of the next one
-          uint32_t third = 0;
-#pragma unroll
-          for (int j = V > 2 ? 2 : V - 1; j >= 0; --j) third = key[j] != m0 && (!two || key[j] != m1) ? key[j] + 0 : third;
-          for (uint32_t d = 1; d < 1u << ps; d *= 2) {
-            const uint32_t o = __shfl_xor(third, (int)d, L);
-            third = o > third ? o : third;
-          }
-          const int away = (int)(mine >> 6) - (int)(last >> 6);
-          doubt |= near && mine && third && (uint32_t)abs(away) <= 4 * tol &&
-                   ((two ? m1 : m0) >> IB) - (third >> IB) <= tol;
-          uint64_t w64 = 0;
-          if (mine) {
-            const Choice c0 = chosen(row, m0), c1 = chosen(row, two ? m1 : m0);
-            const double s0 = score64(c0.x, c0.b), s1 = score64(c1.x, c1.b);
-            w64 = order64(two ? s0 + s1 : s0);
-          }
-          uint32_t before = 0;
-          for (uint32_t o = 0; o < G; ++o) {
-            const uint64_t v = __shfl((unsigned long long)w64, (int)(o << ps), L);
-            before += v > w64 || (v == w64 && o < g);
-          }
-          kept = near ? mine && before < (uint32_t)a.r.topk_groups : kept;
-        }
-      }
-      doubt |= kept && cut;
-      if (!kept) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = 0;
-      }
-    }
-    // lane k: the k-th choice (0: none); lane topk: the next one
-    uint32_t won = 0;
-    auto round = [&](uint32_t k, int keep) {
-      const uint32_t m = lanes_max<L>(key[0]);
-      won = l == k ? m : won;
-      const bool pop = key[0] == m;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (j < keep) {
-          const uint32_t stay = key[j], next = j + 1 < V ? key[j + 1 < V ? j + 1 : j] + 0 : 0;
-          key[j] = pop ? next : stay;
-        }
-    };
-#pragma unroll
-    for (int k = 0; k <= KB; ++k)
-      if ((uint32_t)k <= K) round((uint32_t)k, KB + kMoreRounds - k);
-    Choice c = chosen(row, won);
-    const uint32_t q = won >> IB, next = from_next_lane(won, 0);
-    const float nx = __uint_as_float(from_next_lane(__float_as_uint(c.x), 0));
-    const float nb = __uint_as_float(from_next_lane(__float_as_uint(c.b), 0));
-    bool near = false;
-    if (l < K && won) {
-      const float cx = c.x, cb = c.b;
-      // binary64 scores of different logits may be equal where they saturate
-      // (sigmoids of logits above 20 nearly so), underflow or lie too near
-      doubt |= by_logit ? (softmax ? top - cx > 700.0f : cx > 20.0f || cx < -700.0f) : q == 1;
-      doubt |= by_logit && next && cx != nx && cx - nx < 1e-13f;
-      if (next && q - (next >> IB) <= tol) {
-        const bool equal = cx == nx && cb == nb;
-        // past an equal pair at the end there may be more, not looked at: two
-        // bf16 logits of one code are equal unless far below the best
-        const bool sure = l + 1 < K || (T::kSize == 2 && by_logit && (float)(1u << (QB - 17)) * fabsf(cx) >= top - cx);
-        near = !(equal && sure);
-      }
-    }
+    next = lanes_max<L>(left);
+    bool kept = mine && mine >= last;
+    const bool near = last && next && (last >> 6) - (next >> 6) <= 2 * tol;
     if (__any(near && live)) {
       if constexpr (KEY == kBySoftmax) {
         doubt |= near;
       } else {
-        // by the binary64 scores of the choices and of kMoreRounds after
-        // them, the last of which has to be clear of the topk-th
+        // by the worths in binary64, every lane its own group's; the keys
+        // that they sum have to be clear of the next one
+        uint32_t third = 0;
 #pragma unroll
-        for (int r = 1; r <= kMoreRounds; ++r) round(K + r, kMoreRounds - r);
-        const uint32_t end = __shfl(won, (int)(K + kMoreRounds), L);
-        doubt |= l + 1 == K && end && q - (end >> IB) <= tol;
-        c = chosen(row, won);
-        const uint64_t k64 = won ? order64(score64(c.x, c.b)) : 0;
-        uint32_t rank = 0;
-        for (uint32_t o = 0; o <= K + kMoreRounds; ++o) {
-          const uint64_t v = __shfl((unsigned long long)k64, (int)o, L);
-          const int32_t v_id = __shfl(c.id, (int)o, L);
-          rank += v > k64 || (v == k64 && v_id < c.id);
+        for (int j = V > 2 ? 2 : V - 1; j >= 0; --j) third = key[j] != m0 && (!two || key[j] != m1) ? key[j] + 0 : third;
+        for (uint32_t d = 1; d < 1u << ps; d *= 2) {
+          const uint32_t o = __shfl_xor(third, (int)d, L);
+          third = o > third ? o : third;
         }
-        // to the lane of its rank (the lanes that nothing is sent to get 0)
-        const uint32_t to = won ? rank : L - 1;
-        won = (uint32_t)__builtin_amdgcn_ds_permute((int)((sub * L + to) * 4), (int)won);
-        c = chosen(row, won);
+        const int away = (int)(mine >> 6) - (int)(last >> 6);
+        doubt |= near && mine && third && (uint32_t)abs(away) <= 4 * tol &&
+                 ((two ? m1 : m0) >> IB) - (third >> IB) <= tol;
+        uint64_t w64 = 0;
+        if (mine) {
+          const Choice c0 = chosen(row, m0), c1 = chosen(row, two ? m1 : m0);
+          const double s0 = score64(c0.x, c0.b), s1 = score64(c1.x, c1.b);
+          w64 = order64(two ? s0 + s1 : s0);
+        }
+        uint32_t before = 0;
+        for (uint32_t o = 0; o < G; ++o) {
+          const uint64_t v = __shfl((unsigned long long)w64, (int)(o << ps), L);
+          before += v > w64 || (v == w64 && o < g);
+        }
+        kept = near ? mine && before < (uint32_t)a.r.topk_groups : kept;
       }
     }
-    const uint64_t again = __ballot(doubt && live);
-    const float cx = c.x;
-    // the weights of the chosen, lane k the k-th
-    const bool have = l < K && won;
-    const float sx = have ? cx : -inf;
-    float w;
-    if (softmax) {
-      const float m = a.r.renorm ? lanes_max<L>(sx) : top;
-      const float p = have ? expf(cx - m) : 0.0f;
-      w = p / (a.r.renorm ? lanes_sum<L>(p) : total);
-    } else if (a.r.renorm) {
-      const float m = fminf(lanes_max<L>(sx), 0.0f);
-      const float p = !have ? 0.0f : m < 0.0f ? expf(cx - m) / (1.0f + expf(cx)) : 1.0f / (1.0f + expf(-cx));
-      w = p / lanes_sum<L>(p);
-    } else {
-      w = 1.0f / (1.0f + expf(-cx));
+    doubt |= kept && cut;
+    if (!kept) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) key[j] = 0;
     }
-    const uint64_t sub_lanes = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (sub * L % 64);
-    if (l < K && live && !(again & sub_lanes)) {
-      a.weights[t * K + l] = have ? w * a.r.scale : 0.0f;
-      a.ids[t * K + l] = have ? c.id : -1;
-    }
-    for (uint32_t s = 0; s < TPW; ++s)
-      if (again >> (s * L % 64) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) route_exact<T, VX>(a, t0 + s);
   }
+  // lane k: the k-th choice (0: none); lane topk: the next one
+  uint32_t won = 0;
+  auto round = [&](uint32_t k, int keep) {
+    const uint32_t m = lanes_max<L>(key[0]);
+    won = l == k ? m : won;
+    const bool pop = key[0] == m;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < keep) {
+        const uint32_t stay = key[j], next = j + 1 < V ? key[j + 1 < V ? j + 1 : j] + 0 : 0;
+        key[j] = pop ? next : stay;
+      }
+  };
+#pragma unroll
+  for (int k = 0; k <= KB; ++k)
+    if ((uint32_t)k <= K) round((uint32_t)k, KB + kMoreRounds - k);
+  Choice c = chosen(row, won);
+  const uint32_t q = won >> IB, next = from_next_lane(won, 0);
+  const float nx = __uint_as_float(from_next_lane(__float_as_uint(c.x), 0));
+  const float nb = __uint_as_float(from_next_lane(__float_as_uint(c.b), 0));
+  bool near = false;
+  if (l < K && won) {
+    const float cx = c.x, cb = c.b;
+    // binary64 scores of different logits may be equal where they saturate
+    // (sigmoids of logits above 20 nearly so), underflow or lie too near
+    doubt |= by_logit ? (softmax ? top - cx > 700.0f : cx > 20.0f || cx < -700.0f) : q == 1;
+    doubt |= by_logit && next && cx != nx && cx - nx < 1e-13f;
+    if (next && q - (next >> IB) <= tol) {
+      const bool equal = cx == nx && cb == nb;
+      // past an equal pair at the end there may be more, not looked at: two
+      // bf16 logits of one code are equal unless far below the best
+      const bool sure = l + 1 < K || (T::kSize == 2 && by_logit && (float)(1u << (QB - 17)) * fabsf(cx) >= top - cx);
+      near = !(equal && sure);
+    }
+  }
+  if (__any(near && live)) {
+    if constexpr (KEY == kBySoftmax) {
+      doubt |= near;
+    } else {
+      // by the binary64 scores of the choices and of kMoreRounds after
+      // them, the last of which has to be clear of the topk-th
+#pragma unroll
+      for (int r = 1; r <= kMoreRounds; ++r) round(K + r, kMoreRounds - r);
+      const uint32_t end = __shfl(won, (int)(K + kMoreRounds), L);
+      doubt |= l + 1 == K && end && q - (end >> IB) <= tol;
+      c = chosen(row, won);
+      const uint64_t k64 = won ? order64(score64(c.x, c.b)) : 0;
+      uint32_t rank = 0;
+      for (uint32_t o = 0; o <= K + kMoreRounds; ++o) {
+        const uint64_t v = __shfl((unsigned long long)k64, (int)o, L);
+        const int32_t v_id = __shfl(c.id, (int)o, L);
+        rank += v > k64 || (v == k64 && v_id < c.id);
+      }
+      // to the lane of its rank (the lanes that nothing is sent to get 0)
+      const uint32_t to = won ? rank : L - 1;
+      won = (uint32_t)__builtin_amdgcn_ds_permute((int)((sub * L + to) * 4), (int)won);
+      c = chosen(row, won);
+    }
+  }
+  const uint64_t again = __ballot(doubt && live);
+  const float cx = c.x;
+  // the weights of the chosen, lane k the k-th
+  const bool have = l < K && won;
+  const float sx = have ? cx : -inf;
+  float w;
+  if (softmax) {
+    const float m = a.r.renorm ? lanes_max<L>(sx) : top;
+    const float p = have ? expf(cx - m) : 0.0f;
+    w = p / (a.r.renorm ? lanes_sum<L>(p) : total);
+  } else if (a.r.renorm) {
+    const float m = fminf(lanes_max<L>(sx), 0.0f);
+    const float p = !have ? 0.0f : m < 0.0f ? expf(cx - m) / (1.0f + expf(cx)) : 1.0f / (1.0f + expf(-cx));
+    w = p / lanes_sum<L>(p);
+  } else {
+    w = 1.0f / (1.0f + expf(-cx));
+  }
+  const uint64_t sub_lanes = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (sub * L % 64);
+  if (l < K && live && !(again & sub_lanes)) {
+    a.weights[t * K + l] = have ? w * a.r.scale : 0.0f;
+    a.ids[t * K + l] = have ? c.id : -1;
+  }
+  for (uint32_t s = 0; s < TPW; ++s)
+    if (again >> (s * L % 64) & (L == 64 ? ~0ull : (1ull << (L & 63)) - 1)) route_exact<T, VX>(a, t0 + s);
 }
 
-// The gradient, L lanes a token, lane l holding logits l V .. l V + V - 1, so
-// that a token's logits are read and its gradients written in whole 16-byte
-// units where the row allows.  The chosen experts' terms come to their lanes
+// The gradient, L lanes a token, V logits a lane.  UNITS: in 16-byte units,
+// unit u of lane l being the row's unit u L + l, for rows of whole units; else
+// by elements, j L + l.  Either way neighbouring lanes touch neighbouring
+// memory (32768 x 128 f32: 8.5 us; with a lane's 8 logits side by side, in two
+// units of every other 16 bytes, 10.1; 32 lanes of 4 logits 9.3).  The chosen experts' terms come to their lanes
 // by way of LDS: lane k < topk works choice k out and adds it to the row's
 // slot.  Bound by HBM: the row is read once (not at all where only the chosen
 // logits matter) and written once.
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool UNITS>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const RouteBackwardArgs a) {
   constexpr uint32_t TPW = 64 / L;
   constexpr int N = kUnit<T>;
@@ -541,111 +542,121 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
   const bool softmax = a.r.score == SNAC_SCORE_SOFTMAX, renorm = a.r.renorm != 0;
   const float inf = __builtin_inff();
   float* row_up = lds[wave_id()][sub];
-  float* up = row_up + l * V;
-  const uint32_t e0 = l * V, n = E > e0 ? (E - e0 < V ? E - e0 : V) : 0;
-  const bool whole = E % V == 0, full = E == L * V;
-  for (uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW; t0 < a.tokens;
-       t0 += (uint64_t)gridDim.x * kRouteWaves * TPW) {
-    const bool live = t0 + sub < a.tokens;
-    const uint64_t t = live ? t0 + sub : t0;
-    const char* row = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
-    float x[V];
-    if (softmax && !renorm) load_elems<T, V>(row, e0, n, whole, full, -inf, x);
-    // the choices of this lane: one, or two where topk is above L
-    constexpr int C = L < SNAC_MAX_TOPK ? 2 : 1;
-    int32_t id[C];
-    bool have[C];
-    float dw[C], cx[C];
+  // the row's element that is this lane's j-th
+  auto at = [&](int j) { return UNITS ? ((j / N) * L + l) * N + j % N : j * L + l; };
+  const uint64_t t0 = ((uint64_t)blockIdx.x * kRouteWaves + wave_id()) * TPW;
+  if (t0 >= a.tokens) return;
+  const bool live = t0 + sub < a.tokens;
+  const uint64_t t = live ? t0 + sub : t0;
+  const char* row = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
+  float x[V];
+  if (softmax && !renorm) {
+    // a lane without an element reads the row's first
+    if constexpr (UNITS) {
+      u32x4 w[V / N];
+#pragma unroll
+      for (int u = 0; u < V / N; ++u) w[u] = ld_unit<false>(row + (at(u * N) < E ? at(u * N) : 0) * T::kSize);
+#pragma unroll
+      for (int u = 0; u < V / N; ++u) {
+        float f[N];
+        unpack<T>(w[u], f);
+#pragma unroll
+        for (int c = 0; c < N; ++c) x[u * N + c] = at(u * N) < E ? f[c] + 0.0f : -inf;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = load_elem<T>(row + (at(j) < E ? at(j) : 0) * T::kSize);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = at(j) < E ? x[j] + 0.0f : -inf;
+    }
+  }
+  // the choices of this lane: one, or two where topk is above L
+  constexpr int C = L < SNAC_MAX_TOPK ? 2 : 1;
+  int32_t id[C];
+  bool have[C];
+  float dw[C], cx[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t k = l + c * L;
+    id[c] = k < K ? a.ids[t * K + k] : -1;
+    have[c] = id[c] >= 0 && (uint32_t)id[c] < E;
+    dw[c] = have[c] ? a.dweights[t * K + k] * a.r.scale : 0.0f;
+    cx[c] = have[c] ? load_logit<T>(row, (uint32_t)id[c]) : -inf;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) row_up[at(j)] = 0.0f;
+  float g[C];  // what goes to the chosen slots
+  float inv = 0.0f, dot = 0.0f, top = -inf;
+  if (softmax && !renorm) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
+    top = lanes_max<L>(top);
+    float total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      x[j] = x[j] == -inf ? 0.0f : __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
+      total += x[j];
+    }
+    total = lanes_sum<L>(total);
+    inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit masked
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t k = l + c * L;
-      id[c] = k < K ? a.ids[t * K + k] : -1;
-      have[c] = id[c] >= 0 && (uint32_t)id[c] < E;
-      dw[c] = have[c] ? a.dweights[t * K + k] * a.r.scale : 0.0f;
-      cx[c] = have[c] ? load_logit<T>(row, (uint32_t)id[c]) : -inf;
+      const float r = !have[c] || cx[c] == -inf ? 0.0f : expf(cx[c] - top) * inv;
+      dot += have[c] ? r * dw[c] : 0.0f;
+      g[c] = dw[c];
     }
+    dot = lanes_sum<L>(dot);
+  } else {
+    float m = cx[0], r[C], total = 0.0f;
+    if constexpr (C == 2) m = fmaxf(m, cx[1]);
+    if (renorm) m = lanes_max<L>(m);
+    if (!softmax) m = fminf(m, 0.0f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) up[j] = 0.0f;
-    float g[C];  // what goes to the chosen slots
-    float inv = 0.0f, dot = 0.0f, top = -inf;
-    if (softmax && !renorm) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
-      top = lanes_max<L>(top);
-      float total = 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[j] = x[j] == -inf ? 0.0f : expf(x[j] - top);
-        total += x[j];
-      }
+    for (int c = 0; c < C; ++c) {
+      r[c] = 0.0f;
+      if (have[c] && cx[c] != -inf)
+        r[c] = softmax || (renorm && m < 0.0f) ? expf(cx[c] - m) : 1.0f / (1.0f + expf(-cx[c]));
+      // the sigmoid's slope is its score times that of -x
+      g[c] = softmax ? 1.0f : 1.0f / (1.0f + expf(cx[c]));
+      if (!softmax && renorm && m < 0.0f) r[c] *= g[c];
+      total += r[c];
+    }
+    if (renorm) {
       total = lanes_sum<L>(total);
-      inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit masked
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const float r = !have[c] || cx[c] == -inf ? 0.0f : expf(cx[c] - top) * inv;
-        dot += have[c] ? r * dw[c] : 0.0f;
-        g[c] = dw[c];
+        r[c] = total == 0.0f ? 0.0f : r[c] / total;
+        dot += have[c] ? r[c] * dw[c] : 0.0f;
       }
       dot = lanes_sum<L>(dot);
-    } else {
-      float m = cx[0], r[C], total = 0.0f;
-      if constexpr (C == 2) m = fmaxf(m, cx[1]);
-      if (renorm) m = lanes_max<L>(m);
-      if (!softmax) m = fminf(m, 0.0f);
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        r[c] = 0.0f;
-        if (have[c] && cx[c] != -inf)
-          r[c] = softmax || (renorm && m < 0.0f) ? expf(cx[c] - m) : 1.0f / (1.0f + expf(-cx[c]));
-        // the sigmoid's slope is its score times that of -x
-        g[c] = softmax ? 1.0f : 1.0f / (1.0f + expf(cx[c]));
-        if (!softmax && renorm && m < 0.0f) r[c] *= g[c];
-        total += r[c];
-      }
-      if (renorm) {
-        total = lanes_sum<L>(total);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          r[c] = total == 0.0f ? 0.0f : r[c] / total;
-          dot += have[c] ? r[c] * dw[c] : 0.0f;
-        }
-        dot = lanes_sum<L>(dot);
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c) g[c] = r[c] * g[c] * (dw[c] - dot);
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (have[c]) atomicAdd(&row_up[id[c]], g[c]);
-    float d[V];
+    for (int c = 0; c < C; ++c) g[c] = r[c] * g[c] * (dw[c] - dot);
+  }
 #pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = up[j];
-    if (softmax && !renorm) {
+  for (int c = 0; c < C; ++c)
+    if (have[c]) atomicAdd(&row_up[id[c]], g[c]);
+  float d[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) d[j] = x[j] * inv * (d[j] - dot);
+  for (int j = 0; j < V; ++j) d[j] = row_up[at(j)];
+  if (softmax && !renorm) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = x[j] * inv * (d[j] - dot);
+  }
+  if (!live) return;
+  char* p = static_cast<char*>(a.dlogits) + t * a.ld_d * T::kSize;
+  if constexpr (UNITS) {
+#pragma unroll
+    for (int u = 0; u < V / N; ++u) {
+      float f[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) f[c] = d[u * N + c];
+      if (at(u * N) < E) st_unit<true>(p + at(u * N) * T::kSize, pack<T>(f));
     }
-    if (!live) continue;
-    char* p = static_cast<char*>(a.dlogits) + (t * a.ld_d + e0) * T::kSize;
-    bool done = false;
-    if constexpr (V >= N) {
-      if (whole) {
-        if (n) {
+  } else {
 #pragma unroll
-          for (int u = 0; u < V / N; ++u) {
-            float f[N];
-#pragma unroll
-            for (int c = 0; c < N; ++c) f[c] = d[u * N + c];
-            st_unit<false>(p + u * 16, pack<T>(f));
-          }
-        }
-        done = true;
-      }
-    }
-    if (!done) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if ((uint32_t)j < n) store_elem<T>(p + j * T::kSize, d[j]);
-    }
+    for (int j = 0; j < V; ++j)
+      if (at(j) < E) store_elem<T>(p + at(j) * T::kSize, d[j]);
   }
 }
 
@@ -669,12 +680,17 @@ bool route_fits(const RouteArgs& a, hipStream_t stream) {
   uint32_t ps = group_shift(a.r, V);
   if (a.r.topk > KB || a.r.topk + 1 > L || (uint64_t)a.r.groups << ps > L) return false;
   if (a.r.groups == 1) ps = __builtin_ctz(L);
-  const uint64_t per = kRouteWaves * (64 / L);
-  const uint64_t want = (a.tokens + per - 1) / per;
-  const int cus = device_cu_count();
-  const uint64_t most = (uint64_t)(cus > 0 ? cus : 1) * 16;
-  hipLaunchKernelGGL((route_kernel<T, L, V, KB, KEY>), dim3((uint32_t)(want < most ? want : most)), dim3(kRouteThreads),
-                     0, stream, a, ps, (uint32_t)(a.r.experts / a.r.groups));
+  // a wave a set of tokens; in launches that a grid holds
+  const uint64_t per = kRouteWaves * (64 / L), most = per << 24;
+  RouteArgs c = a;
+  for (uint64_t t = 0; t < a.tokens; t += most) {
+    c.tokens = a.tokens - t < most ? a.tokens - t : most;
+    c.logits = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
+    c.weights = a.weights + t * (uint64_t)a.r.topk;
+    c.ids = a.ids + t * (uint64_t)a.r.topk;
+    hipLaunchKernelGGL((route_kernel<T, L, V, KB, KEY>), dim3((uint32_t)((c.tokens + per - 1) / per)),
+                       dim3(kRouteThreads), 0, stream, c, ps, (uint32_t)(a.r.experts / a.r.groups));
+  }
   return true;
 }
 
@@ -705,8 +721,22 @@ void route_by_key(const RouteArgs& a, hipStream_t stream) {
 
 template <typename T, int L, int V>
 void route_backward_in(const RouteBackwardArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((route_backward_kernel<T, L, V>), dim3(route_grid((a.tokens + 64 / L - 1) / (64 / L))),
-                     dim3(kRouteThreads), 0, stream, a);
+  const uint64_t per = kRouteWaves * (64 / L), most = per << 24;
+  RouteBackwardArgs c = a;
+  for (uint64_t t = 0; t < a.tokens; t += most) {
+    c.tokens = a.tokens - t < most ? a.tokens - t : most;
+    c.logits = static_cast<const char*>(a.logits) + t * a.ld * T::kSize;
+    c.ids = a.ids + t * (uint64_t)a.r.topk;
+    c.dweights = a.dweights + t * (uint64_t)a.r.topk;
+    c.dlogits = static_cast<char*>(a.dlogits) + t * a.ld_d * T::kSize;
+    const dim3 grid((uint32_t)((c.tokens + per - 1) / per)), block(kRouteThreads);
+    bool units = false;
+    if constexpr (V >= (int)kUnit<T>) {
+      units = a.r.experts % kUnit<T> == 0;
+      if (units) hipLaunchKernelGGL((route_backward_kernel<T, L, V, true>), grid, block, 0, stream, c);
+    }
+    if (!units) hipLaunchKernelGGL((route_backward_kernel<T, L, V, false>), grid, block, 0, stream, c);
+  }
 }
 
 template <typename T>
@@ -715,8 +745,8 @@ void route_backward_any(const RouteBackwardArgs& a, hipStream_t stream) {
   if (e <= 16) route_backward_in<T, 16, 1>(a, stream);
   else if (e <= 64) route_backward_in<T, 16, 4>(a, stream);
   else if (e <= 128) route_backward_in<T, 16, 8>(a, stream);
-  else if (e <= 256) route_backward_in<T, 32, 8>(a, stream);
-  else if (e <= 512) route_backward_in<T, 64, 8>(a, stream);
+  else if (e <= 256) route_backward_in<T, 16, 16>(a, stream);
+  else if (e <= 512) route_backward_in<T, 32, 16>(a, stream);
   else route_backward_in<T, 64, 16>(a, stream);
 }
 
