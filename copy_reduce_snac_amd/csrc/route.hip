@@ -13,6 +13,10 @@ namespace {
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr float kLog2e = 1.44269504f;
+// Above this, several tokens a wave (fewer instructions a token), else a wave a
+// token (shorter chains).  us, several / one: 256 experts 6.3 / 5.5 at 2048
+// tokens, 6.6 / 7.9 at 4096, 11.0 / 18.8 at 16384; 64 experts 4.3 / 4.3 at
+// 1024, 4.2 / 4.8 at 2048, 7.0 / 15.7 at 16384.
 constexpr uint64_t kRouteManyTokens = 2048;
 constexpr int kMoreRounds = 3;  // choices looked at past the next one, where two are too near
 
@@ -256,7 +260,11 @@ enum : int { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 // L lanes a token, V experts a lane (in neighbouring slots; a group of
 // experts begins at a lane of its own and has 1 << ps lanes).
 //
-// Choosing is bound by instructions, not by memory, so a key is one 32-bit
+// Choosing is bound by instructions, not by memory: 32768 tokens of 256 f32
+// logits, 8 of them from 4 of 8 groups, take 15.2 us, 860 vector instructions
+// (32 of them transcendental) a wave of 4 tokens, 12.7 us of issue; the same
+// logits are read in 5.4 us.  (All keys in binary64, by a wave a token: 147.)
+// So a key is one 32-bit
 // number: the score's distance from the row's best, QB bits of it, above the
 // complement of the slot's number.  All keys of a token differ, they order as
 // the scores do down to their last bits, and the maximum over lanes is 4 to 6
@@ -402,7 +410,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     }
     next = lanes_max<L>(left);
     bool kept = mine && mine >= last;
-    const bool near = last && next && (last >> 6) - (next >> 6) <= 2 * tol;
+    bool near = last && next && (last >> 6) - (next >> 6) <= 2 * tol;
+    // logits this near the best have equal scores in binary64 at times
+    if (by_logit) near |= last && next >> 6 >= (0x7fffffffu - __float_as_uint(1e-10f)) >> (31 - QB);
     if (__any(near && live)) {
       if constexpr (KEY == kBySoftmax) {
         doubt |= near;
@@ -697,7 +707,7 @@ bool route_fits(const RouteArgs& a, hipStream_t stream) {
 // The narrowest shape that holds the experts; few tokens take a wave each.
 template <typename T, int KEY>
 void route_any(const RouteArgs& a, hipStream_t stream) {
-  if (a.tokens >= kRouteManyTokens &&
+  if (a.tokens > kRouteManyTokens &&
       (route_fits<T, 16, 1, 8, KEY>(a, stream) || route_fits<T, 16, 4, 8, KEY>(a, stream) || route_fits<T, 16, 8, 8, KEY>(a, stream) ||
        route_fits<T, 16, 16, 8, KEY>(a, stream) || route_fits<T, 32, 16, 8, KEY>(a, stream)))
     return;

@@ -199,6 +199,12 @@ def test_scores_equal_in_binary64(tokens, score):
     x[3] = 18 + g.normal(size=64) * 3
     x[4, 1:] = 1e-20 * g.random(63)
     check(np.resize(x, (6, 64)), 7, "f32", score=score)
+    for top in (1, 2):  # and groups by their largest keys, or by two
+        y = np.tile(x, (tokens // 6, 1))
+        _, _, ids = run(y, 4, "f32", score=score, groups=8, topk_groups=2, group_top=top)
+        for t in range(6):
+            want = ref.route(host(device(x, "f32"))[t], 4, score=score, groups=8, topk_groups=2, group_top=top)[1]
+            assert (ids.reshape(-1, 6, 4)[:, t] == want).all(), (top, t)
     xs, w, ids = run(np.tile(x, (tokens // 6, 1)), 7, "f32", score=score)
     assert (ids.reshape(-1, 6, 7) == ids[:6]).all()
 
