@@ -52,8 +52,10 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 // token that makes up half the text is spread over as many waves as a
 // hundred rare ones, no atomics are needed, and the order of every sum is
 // fixed by the ids alone.  The work is bound by HBM (dout once, dtable once),
-// so the workgroups that write the zeros of the rows without a token run in
-// between those that read, in the same launch.
+// and the sort before it and the joining after it by latency, so the zeros of
+// the rows without a token are written beside all of them: workgroups past a
+// launch's own write zeros to a part of the table, before the keys are sorted
+// to all of its rows, after that to those that no key names.
 
 // kUnit<T> sums of one lane -> columns first .. first + n of row `key`.
 template <typename T, typename TG, bool ACC>
@@ -97,10 +99,12 @@ __device__ __forceinline__ void put_unit(const EmbedGradArgs& a, uint32_t key, u
 // finds their part of the sorted keys (64 probes a step) and marks those that it
 // meets.
 constexpr uint32_t kZeroRows = 16;
+constexpr uint64_t kJoinZeroBytes = 32ull << 20;  // of zeros beside the joining
 
 template <typename TG>
-__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, uint32_t lo, uint32_t* met, uint32_t* ends) {
-  const uint32_t rows = a.vocab - lo < kZeroRows ? a.vocab - lo : kZeroRows;
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, uint32_t lo, uint32_t to, uint32_t* met,
+                                          uint32_t* ends) {
+  const uint32_t rows = to - lo < kZeroRows ? to - lo : kZeroRows;
   if (threadIdx.x < kZeroRows) met[threadIdx.x] = 0;
   if (wave_id() < 2) {
     // the first position whose key is not below `key`, 64 probes at a time
@@ -214,11 +218,11 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
 // The first `adds` workgroups add, the rest write zeros as those finish.
 template <typename T, typename TG, bool ACC>
 __global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const EmbedGradArgs a, uint32_t slabs,
-                                                                     uint64_t items, uint32_t adds) {
+                                                                     uint64_t items, uint32_t adds, uint32_t zero_to) {
   __shared__ uint32_t met[kZeroRows];
   __shared__ uint32_t ends[2];
   if (!ACC && blockIdx.x >= adds) {
-    zero_rows<TG>(a, (blockIdx.x - adds) * kZeroRows, met, ends);
+    zero_rows<TG>(a, a.zero_from + (blockIdx.x - adds) * kZeroRows, zero_to, met, ends);
     return;
   }
   const uint64_t it = (uint64_t)blockIdx.x * kEmbWaves + wave_id();
@@ -233,7 +237,14 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const Embed
 constexpr int kJoinLoads = 16;
 
 template <typename TG, bool ACC>
-__global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const EmbedGradArgs a, uint32_t slabs) {
+__global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const EmbedGradArgs a, uint32_t slabs, uint32_t joins,
+                                                                     uint32_t zero_from) {
+  __shared__ uint32_t met[kZeroRows];
+  __shared__ uint32_t ends[2];
+  if (!ACC && blockIdx.x >= joins) {
+    zero_rows<TG>(a, zero_from + (blockIdx.x - joins) * kZeroRows, a.vocab, met, ends);
+    return;
+  }
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wide = (a.width + 7u) & ~7u;
   const uint32_t chunk = blockIdx.x / slabs;
@@ -296,15 +307,25 @@ hipError_t embedding_grad_any(const EmbedGradArgs& a, hipStream_t stream) {
   uint32_t slabs = (a.width + 64u * kUnit<T> - 1) / (64u * kUnit<T>);
   const uint64_t items = (uint64_t)chunks * slabs;
   const uint64_t adds = (items + kEmbWaves - 1) / kEmbWaves;
-  const uint64_t zeros = ACC ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-  if (adds + zeros == 0) return hipSuccess;
+  // zeros: what is left of them, kJoinZeroBytes beside the joining and the
+  // rest here
+  const uint32_t left = ACC ? 0 : a.vocab - a.zero_from;
+  const uint64_t row_bytes = (uint64_t)a.width * TG::kSize, late = kJoinZeroBytes / row_bytes;
+  const uint32_t join_zeros = chunks < 2 ? 0 : late < left ? (uint32_t)late : left;
+  const uint32_t zero_to = a.vocab - join_zeros;
+  const uint64_t zeros = ((uint64_t)(left - join_zeros) + kZeroRows - 1) / kZeroRows;
   if (adds + zeros > 0x7fffffffull) return hipErrorInvalidValue;  // not reached within the documented limits
-  hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC>), dim3((uint32_t)(adds + zeros)), dim3(kEmbThreads), 0, stream, a,
-                     slabs, items, (uint32_t)adds);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || chunks < 2) return e;
+  if (adds + zeros) {
+    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC>), dim3((uint32_t)(adds + zeros)), dim3(kEmbThreads), 0, stream,
+                       a, slabs, items, (uint32_t)adds, zero_to);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (chunks < 2) return hipSuccess;
   slabs = (a.width + 4 * kEmbThreads - 1) / (4 * kEmbThreads);
-  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC>), dim3((chunks - 1) * slabs), dim3(kEmbThreads), 0, stream, a, slabs);
+  const uint32_t joins = (chunks - 1) * slabs;
+  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC>), dim3(joins + (join_zeros + kZeroRows - 1) / kZeroRows),
+                     dim3(kEmbThreads), 0, stream, a, slabs, joins, zero_to);
   return hipGetLastError();
 }
 

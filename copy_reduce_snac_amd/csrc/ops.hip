@@ -135,6 +135,8 @@ snac_status check_topk(int topk) {
 
 // radix digits of an embedding gradient's keys 0 .. vocab
 constexpr uint32_t kDigitBits = 10;
+// zeros written beside a counting and a placing launch, and by a workgroup
+constexpr uint64_t kHistZeroBytes = 20ull << 20, kPlaceZeroBytes = 32ull << 20, kZeroGroupBytes = 64ull << 10;
 uint32_t key_bits(uint64_t vocab) { return 64u - (uint32_t)__builtin_clzll(vocab); }
 uint32_t key_passes(uint64_t vocab) { return (key_bits(vocab) + kDigitBits - 1) / kDigitBits; }
 
@@ -380,11 +382,25 @@ snac_status snac_embedding_backward(snac_ctx* ctx, const void* dout, size_t ld_d
     a.hist_ld = sort_hist_ld(a.blocks);
     const uint32_t bits = key_bits(vocab), passes = key_passes(vocab);
     const uint32_t digit = (bits + passes - 1) / passes;  // equal digits
+    auto zeros = [&](uint64_t bytes) {
+      ZeroRows z{};
+      if (accumulate) return z;
+      const uint64_t row = width * gs, rows = bytes / row, left = vocab - g.zero_from;
+      z.p = g.dtable + (uint64_t)g.zero_from * g.ld_dtable;
+      z.ld = g.ld_dtable;
+      z.width = (uint32_t)(row / 2);
+      z.rows = (uint32_t)(rows < left ? rows : left);
+      z.per = row < kZeroGroupBytes ? (uint32_t)(kZeroGroupBytes / row) : 1;
+      g.zero_from += z.rows;
+      return z;
+    };
     for (uint32_t p = 0; p < passes; ++p) {
       a.shift = p * digit;
       a.mask = (1u << digit) - 1;
       a.bins = 1u << digit;
       a.hist = reinterpret_cast<uint32_t*>(scratch + at.hist);
+      if (a.blocks > 1) a.zero_hist = zeros(kHistZeroBytes);
+      a.zero_place = zeros(kPlaceZeroBytes);
       a.key_out = reinterpret_cast<uint32_t*>(scratch + at.keys[p & 1]);
       a.item_out = reinterpret_cast<int32_t*>(scratch + at.items[p & 1]);
       const hipError_t e = launch_sort_pass(a, false, (hipStream_t)stream);

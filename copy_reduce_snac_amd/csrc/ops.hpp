@@ -46,6 +46,15 @@ struct RouteBackwardArgs {
 };
 hipError_t launch_route_backward(const RouteBackwardArgs& a, bool bf16, hipStream_t stream);
 
+// ---------------------------------------------------------------- zeros
+// Rows that workgroups past a launch's own write zeros to: `rows` rows of
+// `width` 2-byte words, `per` of them a workgroup.
+struct ZeroRows {
+  char* p;
+  uint64_t ld;  // bytes
+  uint32_t width, rows, per;
+};
+
 // ---------------------------------------------------------------- sort
 // One stable counting-sort pass over n items: positions by bin, ascending
 // item order within a bin.
@@ -72,6 +81,9 @@ struct SortArgs {
   int32_t* counts;
   int32_t* row_of_slot;
   int32_t* slot_of_row;
+  // written beside the counting and the placing: both leave most of the GPU
+  // idle for their latency
+  ZeroRows zero_hist, zero_place;
 };
 // blocks and chunk of a pass over n items
 void sort_shape(uint32_t n, uint32_t* blocks, uint32_t* chunk);
@@ -155,6 +167,8 @@ struct EmbedGradArgs {
   uint64_t ld_dtable;  // bytes
   int32_t accumulate;
   float* partial;  // [chunks][2][width rounded up to 8]
+  // rows from here on without a token are still to be zeroed (vocab: none)
+  uint32_t zero_from;
 };
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, bool bf16, bool grad_bf16, hipStream_t stream);
 

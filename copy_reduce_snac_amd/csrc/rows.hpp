@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ops.hpp"
 #include "snac_device.hpp"
 
 namespace snac {
@@ -204,6 +205,16 @@ __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
   for (int m = 32; m; m >>= 1) x = x + __shfl_xor(x, m);
   return x;
+}
+
+// A workgroup's share of ZeroRows, `wg` counted from the first that has one.
+__device__ __forceinline__ void write_zeros(const ZeroRows& z, uint32_t wg) {
+  const u32x4 zero[4] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  constexpr uint32_t step = 64u * 4 * kUnit<BF16>;
+  const uint32_t lo = wg * z.per, hi = z.rows - lo < z.per ? z.rows : lo + z.per;
+  for (uint32_t r = lo + wave_id(); r < hi; r += blockDim.x >> 6)
+    for (uint32_t e = 0; e < z.width; e += step)
+      st_piece<BF16, 4, true>(z.p + r * z.ld + (uint64_t)e * 2, z.width - e, zero);
 }
 
 // id of item i of an id array of 4- or 8-byte elements

@@ -54,6 +54,10 @@ __device__ __forceinline__ uint32_t sort_bin(const SortArgs& a, uint32_t key) { 
 template <int FROM>
 __global__ __launch_bounds__(kRunThreads) void sort_hist_kernel(const SortArgs a) {
   __shared__ uint32_t count[kSortMaxBins];
+  if (blockIdx.x >= a.blocks) {
+    write_zeros(a.zero_hist, blockIdx.x - a.blocks);
+    return;
+  }
   for (uint32_t b = threadIdx.x; b < a.bins; b += kRunThreads) count[b] = 0;
   __syncthreads();
   const uint32_t lo = blockIdx.x * a.chunk;
@@ -95,6 +99,10 @@ __global__ __launch_bounds__(TH) void sort_place_kernel(const SortArgs a) {
   __shared__ __align__(4) uint16_t wave_count[W][BINS];
   __shared__ uint32_t base[BINS], early[BINS];
   __shared__ uint32_t scan[W];
+  if (!PLAN && blockIdx.x >= a.blocks) {
+    write_zeros(a.zero_place, blockIdx.x - a.blocks);
+    return;
+  }
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = wave_id();
   const uint32_t bits = 32u - (uint32_t)__clz((int)(a.bins - 1) | 1);
   // this wave's part of the run
@@ -225,16 +233,19 @@ uint64_t sort_hist_words(uint32_t blocks, uint32_t bins) {
 
 namespace {
 
+uint32_t zero_groups(const ZeroRows& z) { return z.rows ? (z.rows + z.per - 1) / z.per : 0; }
+
 template <bool PLAN, int FROM>
 hipError_t sort_pass(const SortArgs& a, hipStream_t stream) {
+  const dim3 place(a.blocks + zero_groups(a.zero_place));
   if (a.blocks == 1) {
-    hipLaunchKernelGGL((sort_place_kernel<PLAN, kAloneThreads, FROM>), dim3(1), dim3(kAloneThreads), 0, stream, a);
+    hipLaunchKernelGGL((sort_place_kernel<PLAN, kAloneThreads, FROM>), place, dim3(kAloneThreads), 0, stream, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((sort_hist_kernel<FROM>), dim3(a.blocks), dim3(kRunThreads), 0, stream, a);
+  hipLaunchKernelGGL((sort_hist_kernel<FROM>), dim3(a.blocks + zero_groups(a.zero_hist)), dim3(kRunThreads), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((sort_place_kernel<PLAN, kRunThreads, FROM>), dim3(a.blocks), dim3(kRunThreads), 0, stream, a);
+  hipLaunchKernelGGL((sort_place_kernel<PLAN, kRunThreads, FROM>), place, dim3(kRunThreads), 0, stream, a);
   return hipGetLastError();
 }
 
