@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 
 // ------------------------------------------------------------- gradient
 //
-// The sorted positions are cut into chunks of kEmbedChunk.  One wave takes a
+// The sorted positions are cut into chunks of C (embed_chunk).  One wave takes a
 // chunk's slab of columns (a unit a lane), adds the rows of equal tokens in
 // order and writes a run that lies inside the chunk; the sums of the runs
 // that cross its ends go to partial[chunk][0] (begun before it) and [1]
@@ -56,6 +56,13 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 // the rows without a token are written beside all of them: workgroups past a
 // launch's own write zeros to a part of the table, before the keys are sorted
 // to all of its rows, after that to those that no key names.
+//
+// 32768 tokens (10500 different ones) of 2048 bf16 into 65536 x 2048 f32, 671
+// MB, take 138 us (4.9 TB/s).  A chunk's rows are all in flight before the
+// first sum is written, since a load issued after a store waits for it: 32
+// rows at a time 164 us, 16: 173, 8: 178, 4: 182 (before the zeros moved
+// beside the other launches).  Zeros stream (150 us for 159); the sums do not,
+// whose lanes write 16 of every 32 bytes at a time (177 us for 150).
 
 // kUnit<T> sums of one lane -> columns first .. first + n of row `key`.
 template <typename T, typename TG, bool ACC>
@@ -136,20 +143,20 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, uint32_t lo, u
   }
 }
 
-// One chunk's slab of 64 units of columns, by one wave.  WHOLE: all of them
-// exist; the form without their checks is a third of the code, which the
-// unrolled loop repeats for each row.
-template <typename T, typename TG, bool ACC, bool WHOLE>
-__device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk, uint32_t slab) {
+// One chunk's slab of 64 units of columns from `col0` on, by one wave.  WHOLE:
+// all of them exist; the form without their checks is a third of the code,
+// which the unrolled loop repeats for each row.
+template <typename T, typename TG, bool ACC, bool WHOLE, uint32_t C>
+__device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk, uint32_t col0) {
   constexpr uint32_t N = kUnit<T>;
-  static_assert(kEmbedChunk + 2 <= 64, "a lane for each key of a chunk and its neighbours");
+  static_assert(C + 2 <= 64, "a lane for each key of a chunk and its neighbours");
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wide = (a.width + 7u) & ~7u;
-  const uint32_t first = (slab * 64u + lane) * N;
+  const uint32_t first = col0 + lane * N;
   const uint32_t left = first < a.width ? a.width - first : 0;
   const uint32_t n = WHOLE ? N : left < N ? left : N;
-  constexpr int kLoads = WHOLE ? kEmbedChunk : 4;  // rows of dout in flight
-  const uint32_t lo = chunk * kEmbedChunk, hi = a.n - lo < kEmbedChunk ? a.n : lo + kEmbedChunk;
+  constexpr int kLoads = WHOLE || C < 8 ? C : 8;  // rows of dout in flight
+  const uint32_t lo = chunk * C, hi = a.n - lo < C ? a.n : lo + C;
   // lane i: the key and token of position lo + i; lane 62: the key before the
   // chunk, lane 63: the key after it (`vocab`, no gradient, where there is none)
   uint32_t my_key = a.vocab, my_token = 0;
@@ -172,8 +179,8 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
       if (n) {
 #pragma unroll
         for (uint32_t c = 0; c < N; c += 4)
-          *reinterpret_cast<u32x4*>(p + c) = u32x4{__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
-                                                   __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3])};
+          st_unit<false>(reinterpret_cast<char*>(p + c), u32x4{__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
+                                                              __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3])});
       }
     } else {
       put_unit<T, TG, ACC>(a, cur, first, n, acc);
@@ -216,7 +223,7 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
 }
 
 // The first `adds` workgroups add, the rest write zeros as those finish.
-template <typename T, typename TG, bool ACC>
+template <typename T, typename TG, bool ACC, uint32_t C>
 __global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const EmbedGradArgs a, uint32_t slabs,
                                                                      uint64_t items, uint32_t adds, uint32_t zero_to) {
   __shared__ uint32_t met[kZeroRows];
@@ -228,15 +235,21 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const Embed
   const uint64_t it = (uint64_t)blockIdx.x * kEmbWaves + wave_id();
   if (it >= items) return;
   const uint32_t chunk = (uint32_t)(it / slabs), slab = (uint32_t)(it % slabs);
-  if ((slab + 1) * 64u * kUnit<T> <= a.width) add_chunk<T, TG, ACC, true>(a, chunk, slab);
-  else add_chunk<T, TG, ACC, false>(a, chunk, slab);
+  constexpr uint32_t S = 64u * kUnit<T>;
+  uint32_t col0 = slab * S;
+  // a row's last slab reaches back to be whole: the wave before it writes the
+  // same sums to the columns they share (which must not be when they are
+  // added to what is there)
+  if (!ACC && a.width >= S && col0 + S > a.width) col0 = a.width - S;
+  if (col0 + S <= a.width) add_chunk<T, TG, ACC, true, C>(a, chunk, col0);
+  else add_chunk<T, TG, ACC, false, C>(a, chunk, col0);
 }
 
 // The runs that cross chunks: the chunk that a run begins in adds up its
 // partial sums, a lane for each 4 columns, kJoinLoads rows of them in flight.
 constexpr int kJoinLoads = 16;
 
-template <typename TG, bool ACC>
+template <typename TG, bool ACC, uint32_t C>
 __global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const EmbedGradArgs a, uint32_t slabs, uint32_t joins,
                                                                      uint32_t zero_from) {
   __shared__ uint32_t met[kZeroRows];
@@ -248,14 +261,14 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const Embed
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wide = (a.width + 7u) & ~7u;
   const uint32_t chunk = blockIdx.x / slabs;
-  const uint32_t lo = chunk * kEmbedChunk, hi = lo + kEmbedChunk;  // hi < a.n: not the last chunk
+  const uint32_t lo = chunk * C, hi = lo + C;  // hi < a.n: not the last chunk
   const uint32_t key = a.keys[hi - 1], next = a.keys[hi], begin = a.keys[lo], prev = a.keys[lo ? lo - 1 : 0];
   // only where a run begins in this chunk and goes on after it
   if (key >= a.vocab || next != key || (begin == key && lo > 0 && prev == key)) return;
   // how many chunks after this one it reaches into
   uint32_t more = 0;
   while (true) {
-    const uint64_t end = ((uint64_t)chunk + 2 + more + lane) * kEmbedChunk;  // past the more + lane + 1st
+    const uint64_t end = ((uint64_t)chunk + 2 + more + lane) * C;  // past the more + lane + 1st
     const uint64_t on = __ballot(end < a.n && a.keys[end < a.n ? end : 0] == key);
     more += on == ~0ull ? 64 : (uint32_t)__ffsll((unsigned long long)~on) - 1;
     if (on != ~0ull) break;
@@ -301,9 +314,9 @@ hipError_t embedding_any(const EmbeddingArgs& a, hipStream_t stream) {
   return a.tokens < simds && a.tokens * pieces < simds ? embedding_in<T, 1>(a, stream) : embedding_in<T, 4>(a, stream);
 }
 
-template <typename T, typename TG, bool ACC>
-hipError_t embedding_grad_any(const EmbedGradArgs& a, hipStream_t stream) {
-  const uint32_t chunks = (a.n + kEmbedChunk - 1) / kEmbedChunk;
+template <typename T, typename TG, bool ACC, uint32_t C>
+hipError_t embedding_grad_in(const EmbedGradArgs& a, hipStream_t stream) {
+  const uint32_t chunks = (a.n + C - 1) / C;
   uint32_t slabs = (a.width + 64u * kUnit<T> - 1) / (64u * kUnit<T>);
   const uint64_t items = (uint64_t)chunks * slabs;
   const uint64_t adds = (items + kEmbWaves - 1) / kEmbWaves;
@@ -316,7 +329,7 @@ hipError_t embedding_grad_any(const EmbedGradArgs& a, hipStream_t stream) {
   const uint64_t zeros = ((uint64_t)(left - join_zeros) + kZeroRows - 1) / kZeroRows;
   if (adds + zeros > 0x7fffffffull) return hipErrorInvalidValue;  // not reached within the documented limits
   if (adds + zeros) {
-    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC>), dim3((uint32_t)(adds + zeros)), dim3(kEmbThreads), 0, stream,
+    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC, C>), dim3((uint32_t)(adds + zeros)), dim3(kEmbThreads), 0, stream,
                        a, slabs, items, (uint32_t)adds, zero_to);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -324,9 +337,17 @@ hipError_t embedding_grad_any(const EmbedGradArgs& a, hipStream_t stream) {
   if (chunks < 2) return hipSuccess;
   slabs = (a.width + 4 * kEmbThreads - 1) / (4 * kEmbThreads);
   const uint32_t joins = (chunks - 1) * slabs;
-  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC>), dim3(joins + (join_zeros + kZeroRows - 1) / kZeroRows),
+  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC, C>), dim3(joins + (join_zeros + kZeroRows - 1) / kZeroRows),
                      dim3(kEmbThreads), 0, stream, a, slabs, joins, zero_to);
   return hipGetLastError();
+}
+
+// Chunks of 32 positions write the fewest partial sums; with few tokens their
+// waves are few and long.  us, chunks of 8 / 32: 1000 tokens, 2000 x 777: 19 /
+// 23; 32768 x 2048 with 2048 tokens 53 / 57, 4096: 57 / 59, 8192: 76 / 70.
+template <typename T, typename TG, bool ACC>
+hipError_t embedding_grad_any(const EmbedGradArgs& a, hipStream_t stream) {
+  return embed_chunk(a.n) == 8 ? embedding_grad_in<T, TG, ACC, 8>(a, stream) : embedding_grad_in<T, TG, ACC, 32>(a, stream);
 }
 
 }  // namespace

@@ -135,8 +135,12 @@ snac_status check_topk(int topk) {
 
 // radix digits of an embedding gradient's keys 0 .. vocab
 constexpr uint32_t kDigitBits = 10;
-// zeros written beside a counting and a placing launch, and by a workgroup
-constexpr uint64_t kHistZeroBytes = 20ull << 20, kPlaceZeroBytes = 32ull << 20, kZeroGroupBytes = 64ull << 10;
+// Zeros written beside a counting and a placing launch, and by a workgroup.
+// They go to every row, also to those that get a sum later, so only where
+// there are fewer tokens than rows.  us, with these / half / a quarter of them:
+// 32768 tokens, 65536 x 2048 f32: 139 / 143 / 145 (none: 150); 4096 tokens,
+// 32768 x 4096 bf16: 60 / 68 / 71; 32768 tokens, 8192 x 2048 f32: 75 / 75 / 73.
+constexpr uint64_t kHistZeroBytes = 40ull << 20, kPlaceZeroBytes = 80ull << 20, kZeroGroupBytes = 64ull << 10;
 uint32_t key_bits(uint64_t vocab) { return 64u - (uint32_t)__builtin_clzll(vocab); }
 uint32_t key_passes(uint64_t vocab) { return (key_bits(vocab) + kDigitBits - 1) / kDigitBits; }
 
@@ -160,7 +164,8 @@ EmbedScratch embed_scratch(uint64_t tokens, uint64_t width) {
   s.hist = at;
   at += up256(sort_hist_words(blocks, 1u << kDigitBits) * 4);
   s.partial = at;
-  const uint64_t chunks = (tokens + kEmbedChunk - 1) / kEmbedChunk;
+  const uint32_t per = embed_chunk(tokens);
+  const uint64_t chunks = (tokens + per - 1) / per;
   at += chunks * 2 * ((width + 7) & ~(uint64_t)7) * 4;
   s.total = at;
   return s;
@@ -384,7 +389,7 @@ snac_status snac_embedding_backward(snac_ctx* ctx, const void* dout, size_t ld_d
     const uint32_t digit = (bits + passes - 1) / passes;  // equal digits
     auto zeros = [&](uint64_t bytes) {
       ZeroRows z{};
-      if (accumulate) return z;
+      if (accumulate || tokens >= vocab) return z;
       const uint64_t row = width * gs, rows = bytes / row, left = vocab - g.zero_from;
       z.p = g.dtable + (uint64_t)g.zero_from * g.ld_dtable;
       z.ld = g.ld_dtable;

@@ -152,8 +152,9 @@ struct EmbeddingArgs {
 };
 hipError_t launch_embedding(const EmbeddingArgs& a, bool bf16, hipStream_t stream);
 
-// Sorted positions per run of the gradient's first pass.
-constexpr uint32_t kEmbedChunk = 32;
+// Sorted positions that a wave of the gradient adds up (embedding.hip).
+constexpr uint32_t kFewTokens = 4096;
+constexpr uint32_t embed_chunk(uint64_t tokens) { return tokens <= kFewTokens ? 8 : 32; }
 struct EmbedGradArgs {
   const char* dout;
   uint64_t ld_dout;  // bytes

@@ -147,7 +147,7 @@ def test_backward(torch, handle, dtype, grad, accumulate, tokens, vocab, first, 
                   pad=first + 1 if vocab > 2 else None)
 
 
-@pytest.mark.parametrize("tokens", [31, 32, 33, 64, 65, 1000, 9000])
+@pytest.mark.parametrize("tokens", [7, 8, 9, 31, 32, 33, 65, 1000, 4096, 4097, 9000])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_backward_of_one_token(torch, handle, tokens, accumulate):
     """Every position the same token: one run over all chunks; one sort run and several."""
@@ -155,9 +155,9 @@ def test_backward_of_one_token(torch, handle, tokens, accumulate):
 
 
 @pytest.mark.parametrize("run", [1, 2, 31, 32, 33, 95])
-def test_backward_of_equal_runs(torch, handle, run):
+@pytest.mark.parametrize("tokens", [700, 5000])
+def test_backward_of_equal_runs(torch, handle, run, tokens):
     """Runs of one length, shuffled: their ends fall on, before and after the chunks' ends."""
-    tokens = 700
     ids = np.random.default_rng(run).permutation(np.arange(tokens) // run)
     backward_case(torch, handle, "bf16", "f32", "int32", tokens, tokens // run + 2, 0, 40, 0, False, ids)
 
@@ -182,6 +182,34 @@ def test_backward_by_vocabulary(torch, handle, vocab):
     again = torch.empty_like(dt)
     ops().embedding_backward(d, torch.tensor(ids, device="cuda"), again, handle)
     assert torch.equal(again, dt), "not the same bits twice"
+
+
+@pytest.mark.parametrize("width", [512, 515, 1030, 2047])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_backward_of_ragged_widths(torch, handle, width, accumulate):
+    """Widths whose last columns do not fill a wave; few tokens and many; every row and a few rows with tokens."""
+    g = np.random.default_rng(width)
+    for tokens, vocab in ((300, 40), (300, 900), (4500, 64)):
+        ids = g.integers(-3, vocab + 3, tokens)
+        backward_case(torch, handle, "bf16", "f32", "int64", tokens, vocab, 0, width, 0, accumulate, ids)
+
+
+def test_offsets_past_32_bits(torch, handle):
+    """A table and its gradient of more than 2^32 bytes: first and last rows, zeros between."""
+    vocab, width = 150000, 8192
+    ids = torch.tensor([0, vocab - 1, 131072, vocab - 1, 131071, vocab], device="cuda")
+    table = torch.zeros(vocab, width, device="cuda")  # 4.9 GB
+    rows = torch.randn(6, width, device="cuda")
+    table[ids[:5]] = rows[[0, 3, 2, 3, 4]]
+    out = torch.empty(6, width, device="cuda")
+    ops().embedding(table, ids, out)
+    assert torch.equal(out[:5], table[ids[:5]]) and (out[5] == 0).all()
+    table.fill_(7.0)
+    ops().embedding_backward(rows, ids, table, handle)
+    assert torch.equal(table[0], rows[0]) and torch.equal(table[131072], rows[2]) and torch.equal(table[131071], rows[4])
+    assert torch.equal(table[vocab - 1], rows[1] + rows[3])
+    table[[0, 131071, 131072, vocab - 1]] = 0
+    assert not bool(table.any())
 
 
 def test_gradient_against_differences(torch, handle):

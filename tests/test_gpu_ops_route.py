@@ -179,6 +179,29 @@ def test_many_tokens(dtype, score, biased, cfg):
         assert np.all(np.abs(w[t] - rw) <= 96 * U * np.abs(rw) + 1e-37), t
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_past_32_bits(dtype):
+    """Rows 2^30 elements apart, forward and backward."""
+    torch = torch_()
+    n, step = 96, 2 ** 30
+    buf = torch.zeros(2 * step + n, dtype=getattr(torch, DT[dtype]), device="cuda")
+    x = buf.as_strided((3, n), (step, 1))
+    x.copy_(torch.randn(3, n, device="cuda"))
+    near = x.contiguous()
+    got = []
+    for lx in (x, near):
+        w, ids = torch.empty(3, 5, device="cuda"), torch.empty(3, 5, dtype=torch.int32, device="cuda")
+        ops().route(lx, w, ids, score="sigmoid")
+        dx = torch.empty_like(near)
+        ops().route_backward(lx, ids, w, dx, score="softmax", renorm=False)
+        got.append((w, ids, dx))
+    ops().route_backward(near, got[1][1], got[1][0], x, score="softmax", renorm=False)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(x, got[1][2])
+    x.zero_()
+    assert not bool(buf.any())
+
+
 def test_ties_go_to_the_lowest_index():
     g = np.random.default_rng(9)
     x = g.integers(-2, 3, size=(200, 128)).astype(np.float64) / 4
