@@ -96,8 +96,22 @@ __device__ __forceinline__ double block_sum(double x, double* lds) {
   return s;
 }
 
-// Every workgroup leaves its sum in partial[]; the last one to do so adds
-// them up in their order and leaves the ticket at 0 for the next call.
+// The norm of n partial sums, added up in a fixed order by the workgroup; in
+// every thread.
+template <typename Load>
+__device__ __forceinline__ float norm_of(uint32_t n, double* lds, Load load) {
+  double sum = 0.0;
+  for (uint32_t b = threadIdx.x; b < n; b += kGradThreads) sum += load(b);
+  sum = block_sum(sum, lds);
+  if (threadIdx.x == 0) lds[0] = sum;
+  __syncthreads();
+  return (float)sqrt(lds[0]);
+}
+
+// Every workgroup leaves its sum in partial[].  JOIN: the last one to do so
+// makes the norm of them and leaves the ticket at 0 for the next call; else
+// clip_kernel does.
+template <bool JOIN>
 __global__ __launch_bounds__(kGradThreads) void norm_kernel(const GradTile* __restrict__ tiles, uint32_t ntiles, double* partial,
                                                             uint32_t* ticket, float* norm) {
   __shared__ double lds[kGradThreads / 64];
@@ -120,18 +134,21 @@ __global__ __launch_bounds__(kGradThreads) void norm_kernel(const GradTile* __re
     else acc = g1.bf16 ? part_squares<BF16>(g1, acc) : part_squares<F32>(g1, acc);
   }
   const double s = block_sum(acc, lds);
+  if constexpr (!JOIN) {
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+    return;
+  }
   if (threadIdx.x == 0) {
     __hip_atomic_store(&partial[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
-  double sum = 0.0;
-  for (uint32_t b = threadIdx.x; b < gridDim.x; b += kGradThreads)
-    sum += __hip_atomic_load(&partial[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  sum = block_sum(sum, lds);
+  const float total = norm_of(gridDim.x, lds, [&](uint32_t b) {
+    return __hip_atomic_load(&partial[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  });
   if (threadIdx.x == 0) {
-    *norm = (float)sqrt(sum);
+    *norm = total;
     __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
@@ -164,10 +181,21 @@ __device__ __forceinline__ void tile_scale(const GradTile& g, float factor) {
   if (e < g.n) st_one<T>(g.dst + e * T::kSize, ld_one<T>(g.src + e * T::kSize) * factor);
 }
 
+// JOIN: the norm is that of `parts` partial sums, which every workgroup adds up
+// for itself and the first one writes to `norm`.
+template <bool JOIN>
 __global__ __launch_bounds__(kGradThreads) void clip_kernel(const GradTile* __restrict__ tiles, uint32_t ntiles,
-                                                            const float* __restrict__ norm, const PoolArg pa,
-                                                            float max_norm) {
-  float factor = max_norm / (*norm + 1e-6f);
+                                                            const double* __restrict__ partial, uint32_t parts, float* norm,
+                                                            const PoolArg pa, float max_norm) {
+  float total;
+  if constexpr (JOIN) {
+    __shared__ double lds[kGradThreads / 64];
+    total = norm_of(parts, lds, [&](uint32_t b) { return partial[b]; });
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  } else {
+    total = *norm;
+  }
+  float factor = max_norm / (total + 1e-6f);
   if (factor > 1.0f) factor = 1.0f;  // a NaN stays
   __shared__ unsigned long long xchg[2];
   const TilePool pool{(global_u64*)pa.next, (global_u64*)(pa.next + (uint64_t)pa.counters * kFlagStride), xchg,
@@ -187,6 +215,13 @@ uint32_t grad_grid(uint32_t ntiles, uint32_t per_cu) {
   return ntiles < most ? ntiles : most;
 }
 
+uint32_t norm_grid(uint32_t ntiles) { return grad_grid((ntiles + 1) / 2, 1); }
+
+// counters where there are rounds left for them after the grid-stride ones
+PoolArg clip_pool(uint32_t ntiles, uint32_t grid, unsigned long long* pool) {
+  return ntiles / grid >= 16 ? PoolArg{pool, 8, kGradCounters} : PoolArg{nullptr, 0, 1};
+}
+
 }  // namespace
 
 hipError_t launch_grad_norm(const GradTile* tiles, uint32_t ntiles, double* partial, uint32_t* ticket, float* norm,
@@ -194,8 +229,8 @@ hipError_t launch_grad_norm(const GradTile* tiles, uint32_t ntiles, double* part
   if (ntiles == 0)
     hipLaunchKernelGGL(zero_norm_kernel, dim3(1), dim3(1), 0, stream, norm);
   else
-    hipLaunchKernelGGL(norm_kernel, dim3(grad_grid((ntiles + 1) / 2, 1)), dim3(kGradThreads), 0, stream, tiles, ntiles, partial,
-                       ticket, norm);
+    hipLaunchKernelGGL((norm_kernel<true>), dim3(norm_grid(ntiles)), dim3(kGradThreads), 0, stream, tiles, ntiles,
+                       partial, ticket, norm);
   return hipGetLastError();
 }
 
@@ -203,9 +238,21 @@ hipError_t launch_clip(const GradTile* tiles, uint32_t ntiles, const float* norm
                        unsigned long long* pool, hipStream_t stream) {
   if (ntiles == 0) return hipSuccess;
   const uint32_t grid = grad_grid(ntiles, 2);
-  // counters where there are rounds left for them after the grid-stride ones
-  const PoolArg pa = ntiles / grid >= 16 ? PoolArg{pool, 8, kGradCounters} : PoolArg{nullptr, 0, 1};
-  hipLaunchKernelGGL(clip_kernel, dim3(grid), dim3(kGradThreads), 0, stream, tiles, ntiles, norm, pa, max_norm);
+  hipLaunchKernelGGL((clip_kernel<false>), dim3(grid), dim3(kGradThreads), 0, stream, tiles, ntiles, nullptr, 0,
+                     const_cast<float*>(norm), clip_pool(ntiles, grid, pool), max_norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_and_clip(const GradTile* tiles, uint32_t ntiles, double* partial, float* norm, float max_norm,
+                                unsigned long long* pool, hipStream_t stream) {
+  if (ntiles == 0) return launch_grad_norm(tiles, 0, partial, nullptr, norm, stream);
+  const uint32_t parts = norm_grid(ntiles), grid = grad_grid(ntiles, 2);
+  hipLaunchKernelGGL((norm_kernel<false>), dim3(parts), dim3(kGradThreads), 0, stream, tiles, ntiles, partial, nullptr,
+                     nullptr);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((clip_kernel<true>), dim3(grid), dim3(kGradThreads), 0, stream, tiles, ntiles, partial, parts, norm,
+                     clip_pool(ntiles, grid, pool), max_norm);
   return hipGetLastError();
 }
 

@@ -538,8 +538,10 @@ snac_status snac_clip_grads(snac_grads* grads, const float* norm, float max_norm
 
 snac_status snac_clip_grad_norm(snac_grads* grads, float max_norm, float* norm, snac_stream stream) {
   TRY(check_max_norm(max_norm));
-  TRY(snac_grad_norm(grads, norm, stream));
-  return snac_clip_grads(grads, norm, max_norm, stream);
+  TRY(check_grads(grads, norm));
+  const hipError_t e = launch_norm_and_clip(grads->tiles, grads->ntiles, grads->partial, norm, max_norm, grads->pool,
+                                            (hipStream_t)stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "snac_clip_grad_norm launch");
 }
 
 }  // extern "C"

@@ -191,5 +191,8 @@ hipError_t launch_grad_norm(const GradTile* tiles, uint32_t ntiles, double* part
 constexpr uint32_t kGradCounters = 4;
 hipError_t launch_clip(const GradTile* tiles, uint32_t ntiles, const float* norm, float max_norm,
                        unsigned long long* pool, hipStream_t stream);
+// both, the norm made of the partial sums by the second launch
+hipError_t launch_norm_and_clip(const GradTile* tiles, uint32_t ntiles, double* partial, float* norm, float max_norm,
+                                unsigned long long* pool, hipStream_t stream);
 
 }  // namespace snac

@@ -167,6 +167,21 @@ def test_again_and_again(torch):
     assert (got[:20] == got[0]).all() and (got[20:] == got[20]).all() and got[0] != got[20]
 
 
+def test_in_one_call_and_in_two(torch):
+    """snac_clip_grad_norm is snac_grad_norm, then snac_clip_grads: the same bits."""
+    g = np.random.default_rng(7)
+    for spec in LISTS:
+        _, ts = tensors(torch, spec, g)
+        outs = [[torch.empty_like(t) for t in ts] for _ in range(2)]
+        norm = torch.empty(2, device="cuda")
+        ops().clip_grad_norm(ops().GradList(ts, outs[0]), 0.5, norm[:1])
+        two = ops().GradList(ts, outs[1])
+        ops().grad_norm(two, norm[1:])
+        ops().clip_grads(two, norm[1:], 0.5)
+        assert norm[0] == norm[1]
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 def test_max_norm_of_zero(torch):
     x = torch.ones(100, device="cuda")
     norm = torch.empty(1, device="cuda")
