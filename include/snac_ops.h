@@ -63,11 +63,11 @@ typedef enum snac_score { SNAC_SCORE_SOFTMAX = 0, SNAC_SCORE_SIGMOID = 1 } snac_
  * Keys and worths are ordered as in binary64, so logits one step apart in
  * their own type fall on their right sides; equal ones by the lower index.
  * A masked expert (logit or key of -infinity) is never chosen, nor is a group
- * whose worth is -infinity; where fewer than topk are left the row ends in
- * id -1 with weight 0, and where their scores sum to 0 the weights are 0.
- * The sum of renormalised sigmoid scores does not underflow: very low logits
- * keep their ratios.  NaN orders above everything, and spreads by the
- * formulas (softmax: over the whole row).
+ * whose worth is -infinity (one of fewer than group_top unmasked experts
+ * among them); where fewer than topk are left the row ends in id -1 with
+ * weight 0.  Renormalised scores do not underflow: very low logits keep their
+ * ratios.  NaN orders above everything, and spreads by the formulas (softmax:
+ * over the whole row, as +infinity does).
  */
 typedef struct snac_router {
   int32_t experts;     /* 1 .. SNAC_MAX_EXPERTS, a multiple of groups */
@@ -92,8 +92,9 @@ snac_status snac_route(const snac_router* router, const void* logits, size_t ld,
 /*
  * snac_route_backward -- dlogits[tokens][experts] (row stride ld_d, `dtype`,
  * every element written) from dweights[tokens][topk] for the ids that
- * snac_route chose.  Of the router, experts, topk, score, renorm and scale
- * are used.  An id outside 0 .. experts - 1 has no part in it.
+ * snac_route chose (a row's ids differ from each other).  Of the router,
+ * experts, topk, score, renorm and scale are used.  An id outside
+ * 0 .. experts - 1 has no part in it.
  */
 snac_status snac_route_backward(const snac_router* router, const void* logits, size_t ld, const int32_t* ids,
                                 const float* dweights, size_t tokens, snac_dtype dtype, void* dlogits, size_t ld_d,
