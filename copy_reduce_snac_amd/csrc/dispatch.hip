@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kPieceUnits = 4;  // of combine_backward, and of the others' large calls
+constexpr int kPieceUnits = 4;  // of combine_backward
 
 template <typename T, int U>
 constexpr uint32_t kPieceElems = 64u * U * kUnit<T>;
@@ -124,14 +124,21 @@ uint32_t row_grid(uint64_t items) {
   return (uint32_t)(want < (1u << 22) ? want : 1u << 22);
 }
 
-// Pieces of a row for `tokens` rows of `width` elements: of kPieceUnits units,
-// or of one where those would leave SIMDs without a wave (4 a CU): 64 tokens,
-// 8 rows of 16 KiB each, took 8.3 us with one and 10 with four.
+// Units a lane of the pieces that `tokens` rows of `width` elements are cut
+// into.  Four read the most at a time; where they would leave SIMDs without a
+// wave (4 a CU) one, and with few waves a SIMD (64 a CU) two, since a wave
+// walks its token's slots one after another.  us, pieces of 1 / 2 / 4 units:
+//   combine   64 tokens of 8 rows of 16 KiB 8.3 / - / 10; 629 of 6 rows of
+//             6.4 KiB 14.5 / 14.1 / 19.9; 2600 of 6 rows of 4 KiB 18.2 / 15.3 /
+//             15.6; 9000 48.9 / 45.2 / 44.6; 16384 of 8 133 / 103 / 101
+//   dispatch  629 15.4 / 15.7 / 16.1; 9000 50.6 / 52.2 / 54.2 (never four)
 template <typename T>
-bool small_pieces(uint64_t tokens, uint32_t width) {
+int piece_units(uint64_t tokens, uint32_t width, int most) {
   const int cus = device_cu_count();
-  const uint32_t pieces = (width + kPieceElems<T, kPieceUnits> - 1) / kPieceElems<T, kPieceUnits>;
-  return tokens < (uint64_t)(cus > 0 ? cus : 1) * 4 && tokens * pieces < (uint64_t)(cus > 0 ? cus : 1) * 4;
+  const uint64_t cu = (uint64_t)(cus > 0 ? cus : 1);
+  const uint32_t pieces = (width + kPieceElems<T, 4> - 1) / kPieceElems<T, 4>;
+  if (tokens >= cu * 64) return most;
+  return tokens * pieces < cu * 4 ? 1 : tokens * pieces < cu * 64 ? 2 : most;
 }
 
 template <typename T, int U>
@@ -144,7 +151,7 @@ hipError_t dispatch_in(const DispatchArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t dispatch_any(const DispatchArgs& a, hipStream_t stream) {
-  return small_pieces<T>(a.tokens, a.width) ? dispatch_in<T, 1>(a, stream) : dispatch_in<T, kPieceUnits>(a, stream);
+  return piece_units<T>(a.tokens, a.width, 2) == 1 ? dispatch_in<T, 1>(a, stream) : dispatch_in<T, 2>(a, stream);
 }
 
 template <typename T, int U>
@@ -157,7 +164,11 @@ hipError_t combine_in(const CombineArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t combine_any(const CombineArgs& a, hipStream_t stream) {
-  return small_pieces<T>(a.tokens, a.width) ? combine_in<T, 1>(a, stream) : combine_in<T, kPieceUnits>(a, stream);
+  switch (piece_units<T>(a.tokens, a.width, 4)) {
+    case 1: return combine_in<T, 1>(a, stream);
+    case 2: return combine_in<T, 2>(a, stream);
+    default: return combine_in<T, 4>(a, stream);
+  }
 }
 
 template <typename T>

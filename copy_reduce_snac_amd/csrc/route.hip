@@ -328,8 +328,27 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
   }
   top = lanes_max<L>(top);
   doubt |= top == inf;
+  // in binary64: softmax's sum over the row (read again: doubts are rare), and
+  // a score with its bias
+  double sum64 = 1.0;
+  auto make_sum64 = [&]() {
+    if constexpr (KEY == kBySoftmax) {
+      float y[V];
+      load_elems<T, V>(row, e0, n, whole, full, -inf, y);
+      sum64 = 0.0;
+#pragma unroll 1
+      for (int j = 0; j < V; ++j) {
+        float v = y[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) v = i == j ? y[i] + 0.0f : v;
+        sum64 += v == -inf ? 0.0 : exp((double)v - (double)top);
+      }
+#pragma unroll
+      for (int m = 1; m < L; m *= 2) sum64 += __shfl_xor(sum64, m, L);
+    }
+  };
   auto score64 = [&](float x, float b) {
-    const double s = softmax ? exp((double)x - (double)top) : 1.0 / (1.0 + exp(-(double)x));
+    const double s = softmax ? exp((double)x - (double)top) / sum64 : 1.0 / (1.0 + exp(-(double)x));
     return by_logit ? s : s + (double)b;
   };
   float total = 0.0f;  // softmax: sum of exp(x - top)
@@ -414,34 +433,31 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     // logits this near the best have equal scores in binary64 at times
     if (by_logit) near |= last && next >> 6 >= (0x7fffffffu - __float_as_uint(1e-10f)) >> (31 - QB);
     if (__any(near && live)) {
-      if constexpr (KEY == kBySoftmax) {
-        doubt |= near;
-      } else {
-        // by the worths in binary64, every lane its own group's; the keys
-        // that they sum have to be clear of the next one
-        uint32_t third = 0;
+      make_sum64();
+      // by the worths in binary64, every lane its own group's; the keys
+      // that they sum have to be clear of the next one
+      uint32_t third = 0;
 #pragma unroll
-        for (int j = V > 2 ? 2 : V - 1; j >= 0; --j) third = key[j] != m0 && (!two || key[j] != m1) ? key[j] + 0 : third;
-        for (uint32_t d = 1; d < 1u << ps; d *= 2) {
-          const uint32_t o = __shfl_xor(third, (int)d, L);
-          third = o > third ? o : third;
-        }
-        const int away = (int)(mine >> 6) - (int)(last >> 6);
-        doubt |= near && mine && third && (uint32_t)abs(away) <= 4 * tol &&
-                 ((two ? m1 : m0) >> IB) - (third >> IB) <= tol;
-        uint64_t w64 = 0;
-        if (mine) {
-          const Choice c0 = chosen(row, m0), c1 = chosen(row, two ? m1 : m0);
-          const double s0 = score64(c0.x, c0.b), s1 = score64(c1.x, c1.b);
-          w64 = order64(two ? s0 + s1 : s0);
-        }
-        uint32_t before = 0;
-        for (uint32_t o = 0; o < G; ++o) {
-          const uint64_t v = __shfl((unsigned long long)w64, (int)(o << ps), L);
-          before += v > w64 || (v == w64 && o < g);
-        }
-        kept = near ? mine && before < (uint32_t)a.r.topk_groups : kept;
+      for (int j = V > 2 ? 2 : V - 1; j >= 0; --j) third = key[j] != m0 && (!two || key[j] != m1) ? key[j] + 0 : third;
+      for (uint32_t d = 1; d < 1u << ps; d *= 2) {
+        const uint32_t o = __shfl_xor(third, (int)d, L);
+        third = o > third ? o : third;
       }
+      const int away = (int)(mine >> 6) - (int)(last >> 6);
+      doubt |= near && mine && third && (uint32_t)abs(away) <= 4 * tol &&
+               ((two ? m1 : m0) >> IB) - (third >> IB) <= tol;
+      uint64_t w64 = 0;
+      if (mine) {
+        const Choice c0 = chosen(row, m0), c1 = chosen(row, two ? m1 : m0);
+        const double s0 = score64(c0.x, c0.b), s1 = score64(c1.x, c1.b);
+        w64 = order64(two ? s0 + s1 : s0);
+      }
+      uint32_t before = 0;
+      for (uint32_t o = 0; o < G; ++o) {
+        const uint64_t v = __shfl((unsigned long long)w64, (int)(o << ps), L);
+        before += v > w64 || (v == w64 && o < g);
+      }
+      kept = near ? mine && before < (uint32_t)a.r.topk_groups : kept;
     }
     doubt |= kept && cut;
     if (!kept) {
@@ -485,28 +501,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     }
   }
   if (__any(near && live)) {
-    if constexpr (KEY == kBySoftmax) {
-      doubt |= near;
-    } else {
-      // by the binary64 scores of the choices and of kMoreRounds after
-      // them, the last of which has to be clear of the topk-th
+    make_sum64();
+    // by the binary64 scores of the choices and of kMoreRounds after
+    // them, the last of which has to be clear of the topk-th
 #pragma unroll
-      for (int r = 1; r <= kMoreRounds; ++r) round(K + r, kMoreRounds - r);
-      const uint32_t end = __shfl(won, (int)(K + kMoreRounds), L);
-      doubt |= l + 1 == K && end && q - (end >> IB) <= tol;
-      c = chosen(row, won);
-      const uint64_t k64 = won ? order64(score64(c.x, c.b)) : 0;
-      uint32_t rank = 0;
-      for (uint32_t o = 0; o <= K + kMoreRounds; ++o) {
-        const uint64_t v = __shfl((unsigned long long)k64, (int)o, L);
-        const int32_t v_id = __shfl(c.id, (int)o, L);
-        rank += v > k64 || (v == k64 && v_id < c.id);
-      }
-      // to the lane of its rank (the lanes that nothing is sent to get 0)
-      const uint32_t to = won ? rank : L - 1;
-      won = (uint32_t)__builtin_amdgcn_ds_permute((int)((sub * L + to) * 4), (int)won);
-      c = chosen(row, won);
+    for (int r = 1; r <= kMoreRounds; ++r) round(K + r, kMoreRounds - r);
+    const uint32_t end = __shfl(won, (int)(K + kMoreRounds), L);
+    doubt |= l + 1 == K && end && q - (end >> IB) <= tol;
+    c = chosen(row, won);
+    const uint64_t k64 = won ? order64(score64(c.x, c.b)) : 0;
+    uint32_t rank = 0;
+    for (uint32_t o = 0; o <= K + kMoreRounds; ++o) {
+      const uint64_t v = __shfl((unsigned long long)k64, (int)o, L);
+      const int32_t v_id = __shfl(c.id, (int)o, L);
+      rank += v > k64 || (v == k64 && v_id < c.id);
     }
+    // to the lane of its rank (the lanes that nothing is sent to get 0)
+    const uint32_t to = won ? rank : L - 1;
+    won = (uint32_t)__builtin_amdgcn_ds_permute((int)((sub * L + to) * 4), (int)won);
+    c = chosen(row, won);
   }
   const uint64_t again = __ballot(doubt && live);
   const float cx = c.x;
@@ -688,7 +701,7 @@ uint32_t group_shift(const snac_router& r, uint32_t V) {
 template <typename T, int L, int V, int KB, int KEY>
 bool route_fits(const RouteArgs& a, hipStream_t stream) {
   uint32_t ps = group_shift(a.r, V);
-  if (a.r.topk > KB || a.r.topk + 1 > L || (uint64_t)a.r.groups << ps > L) return false;
+  if (a.r.topk > KB || a.r.topk + kMoreRounds + 1 > L || (uint64_t)a.r.groups << ps > L) return false;
   if (a.r.groups == 1) ps = __builtin_ctz(L);
   // a wave a set of tokens; in launches that a grid holds
   const uint64_t per = kRouteWaves * (64 / L), most = per << 24;
@@ -709,7 +722,9 @@ template <typename T, int KEY>
 void route_any(const RouteArgs& a, hipStream_t stream) {
   if (a.tokens > kRouteManyTokens &&
       (route_fits<T, 16, 1, 8, KEY>(a, stream) || route_fits<T, 16, 4, 8, KEY>(a, stream) || route_fits<T, 16, 8, 8, KEY>(a, stream) ||
-       route_fits<T, 16, 16, 8, KEY>(a, stream) || route_fits<T, 32, 16, 8, KEY>(a, stream)))
+       route_fits<T, 16, 16, 8, KEY>(a, stream) || route_fits<T, 32, 16, 8, KEY>(a, stream) ||
+       route_fits<T, 16, 4, 12, KEY>(a, stream) || route_fits<T, 16, 16, 12, KEY>(a, stream) ||
+       route_fits<T, 32, 16, 12, KEY>(a, stream)))
     return;
   if (route_fits<T, 64, 1, 8, KEY>(a, stream) || route_fits<T, 64, 4, 8, KEY>(a, stream) || route_fits<T, 64, 16, 8, KEY>(a, stream))
     return;

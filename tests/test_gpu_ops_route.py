@@ -142,7 +142,8 @@ def test_keys_one_step_apart(score, groups, copies):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("score,biased", [("softmax", False), ("softmax", True), ("sigmoid", True)])
 @pytest.mark.parametrize("cfg", [c for c in CONFIGS if c["topk"] <= 8] + [
-    dict(n=10, topk=8), dict(n=500, topk=8, groups=5, topk_groups=3), dict(n=96, topk=5, groups=48, topk_groups=7),
+    dict(n=10, topk=8), dict(n=16, topk=12), dict(n=60, topk=9), dict(n=292, topk=10, groups=4, topk_groups=2),
+    dict(n=256, topk=12, renorm=False), dict(n=500, topk=8, groups=5, topk_groups=3), dict(n=96, topk=5, groups=48, topk_groups=7),
     dict(n=1020, topk=7, groups=3, topk_groups=2), dict(n=900, topk=3, groups=30, topk_groups=4)],
     ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
 def test_many_tokens(dtype, score, biased, cfg):
