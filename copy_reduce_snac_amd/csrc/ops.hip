@@ -241,7 +241,7 @@ snac_status snac_dispatch_plan(snac_ctx* ctx, const void* ids, int id_bytes, siz
   a.counts = counts;
   a.row_of_slot = row_of_slot;
   a.slot_of_row = slot_of_row;
-  const hipError_t e = launch_sort_pass(a, true, (hipStream_t)stream);
+  const hipError_t e = launch_plan(a, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_dispatch_plan launch");
 }
 
@@ -399,22 +399,33 @@ snac_status snac_embedding_backward(snac_ctx* ctx, const void* dout, size_t ld_d
       g.zero_from += z.rows;
       return z;
     };
-    for (uint32_t p = 0; p < passes; ++p) {
-      a.shift = p * digit;
-      a.mask = (1u << digit) - 1;
-      a.bins = 1u << digit;
-      a.hist = reinterpret_cast<uint32_t*>(scratch + at.hist);
-      if (a.blocks > 1) a.zero_hist = zeros(kHistZeroBytes);
-      a.zero_place = zeros(kPlaceZeroBytes);
-      a.key_out = reinterpret_cast<uint32_t*>(scratch + at.keys[p & 1]);
-      a.item_out = reinterpret_cast<int32_t*>(scratch + at.items[p & 1]);
-      const hipError_t e = launch_sort_pass(a, false, (hipStream_t)stream);
-      if (e != hipSuccess) return hip_fail(e, "snac_embedding_backward sort launch");
-      a.key_in = a.key_out;
-      a.item_in = a.item_out;
+    SortPasses r{passes, digit, {}, {}};
+    for (int i = 0; i < 2; ++i) {
+      r.keys[i] = reinterpret_cast<uint32_t*>(scratch + at.keys[i]);
+      r.items[i] = reinterpret_cast<int32_t*>(scratch + at.items[i]);
     }
-    g.keys = a.key_in;
-    g.tokens = a.item_in;
+    a.mask = (1u << digit) - 1;
+    a.bins = 1u << digit;
+    a.hist = reinterpret_cast<uint32_t*>(scratch + at.hist);
+    if (a.blocks == 1) {
+      a.zero_place = zeros(kPlaceZeroBytes);
+      const hipError_t e = launch_radix_alone(a, r, (hipStream_t)stream);
+      if (e != hipSuccess) return hip_fail(e, "snac_embedding_backward sort launch");
+    } else {
+      for (uint32_t p = 0; p < passes; ++p) {
+        a.shift = p * digit;
+        a.zero_hist = zeros(kHistZeroBytes);
+        a.zero_place = zeros(kPlaceZeroBytes);
+        a.key_out = r.keys[p & 1];
+        a.item_out = r.items[p & 1];
+        const hipError_t e = launch_radix_pass(a, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "snac_embedding_backward sort launch");
+        a.key_in = a.key_out;
+        a.item_in = a.item_out;
+      }
+    }
+    g.keys = r.keys[(passes - 1) & 1];
+    g.tokens = r.items[(passes - 1) & 1];
   }
   const hipError_t e = launch_embedding_grad(g, dtype == SNAC_BF16, grad_dtype == SNAC_BF16, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_embedding_backward launch");

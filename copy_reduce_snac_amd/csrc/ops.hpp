@@ -89,7 +89,15 @@ struct SortArgs {
 void sort_shape(uint32_t n, uint32_t* blocks, uint32_t* chunk);
 constexpr uint32_t sort_hist_ld(uint32_t blocks) { return (blocks + 3) & ~3u; }
 uint64_t sort_hist_words(uint32_t blocks, uint32_t bins);  // of one pass
-hipError_t launch_sort_pass(const SortArgs& a, bool plan, hipStream_t stream);
+// The passes of a radix sort of one run.
+struct SortPasses {
+  uint32_t passes, digit;  // bits a pass
+  uint32_t* keys[2];
+  int32_t* items[2];
+};
+hipError_t launch_plan(const SortArgs& a, hipStream_t stream);
+hipError_t launch_radix_pass(const SortArgs& a, hipStream_t stream);  // several runs
+hipError_t launch_radix_alone(const SortArgs& a, const SortPasses& p, hipStream_t stream);
 
 // ------------------------------------------------- dispatch and combine
 struct DispatchArgs {
@@ -154,7 +162,7 @@ hipError_t launch_embedding(const EmbeddingArgs& a, bool bf16, hipStream_t strea
 
 // Sorted positions that a wave of the gradient adds up (embedding.hip).
 constexpr uint32_t kFewTokens = 4096;
-constexpr uint32_t embed_chunk(uint64_t tokens) { return tokens <= kFewTokens ? 8 : 32; }
+constexpr uint32_t embed_chunk(uint64_t tokens) { return tokens > 32 && tokens <= kFewTokens ? 8 : 32; }
 struct EmbedGradArgs {
   const char* dout;
   uint64_t ld_dout;  // bytes

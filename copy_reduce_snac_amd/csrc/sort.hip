@@ -3,7 +3,7 @@
 // tokens.
 //
 // The items are cut into `blocks` runs.  With one run a single workgroup
-// counts and places them; otherwise sort_hist_kernel counts every run's bins
+// counts and places them (all passes of a radix sort in one launch); otherwise sort_hist_kernel counts every run's bins
 // and sort_place_kernel places: item i goes to
 //     (items of lower bins) + (items of its bin in earlier runs)
 //       + (items of its bin before it in its run).
@@ -92,17 +92,23 @@ __device__ __forceinline__ uint32_t place_in_wave(uint16_t* count, uint32_t bin,
   return place;
 }
 
+constexpr uint32_t kSortBins = kSortMaxBins + 1;  // an even number
+template <int TH>
+struct SortLds {
+  __align__(4) uint16_t wave_count[TH / 64][kSortBins];
+  uint32_t base[kSortBins], early[kSortBins];
+  uint32_t scan[TH / 64];
+};
+
+// One pass over this workgroup's run.
 template <bool PLAN, int TH, int FROM>
-__global__ __launch_bounds__(TH) void sort_place_kernel(const SortArgs a) {
+__device__ __forceinline__ void place_run(const SortArgs& a, SortLds<TH>& lds) {
   constexpr uint32_t W = TH / 64;
-  constexpr uint32_t BINS = kSortMaxBins + 1;  // an even number
-  __shared__ __align__(4) uint16_t wave_count[W][BINS];
-  __shared__ uint32_t base[BINS], early[BINS];
-  __shared__ uint32_t scan[W];
-  if (!PLAN && blockIdx.x >= a.blocks) {
-    write_zeros(a.zero_place, blockIdx.x - a.blocks);
-    return;
-  }
+  constexpr uint32_t BINS = kSortBins;
+  auto& wave_count = lds.wave_count;
+  auto& base = lds.base;
+  auto& early = lds.early;
+  auto& scan = lds.scan;
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = wave_id();
   const uint32_t bits = 32u - (uint32_t)__clz((int)(a.bins - 1) | 1);
   // this wave's part of the run
@@ -210,6 +216,40 @@ __global__ __launch_bounds__(TH) void sort_place_kernel(const SortArgs a) {
   }
 }
 
+template <bool PLAN, int TH, int FROM>
+__global__ __launch_bounds__(TH) void sort_place_kernel(const SortArgs a) {
+  __shared__ SortLds<TH> lds;
+  if (!PLAN && blockIdx.x >= a.blocks) {
+    write_zeros(a.zero_place, blockIdx.x - a.blocks);
+    return;
+  }
+  place_run<PLAN, TH, FROM>(a, lds);
+}
+
+// All passes of a radix sort of one run, by one workgroup: `digit` bits a
+// pass, the keys and items of the passes in out[0] and out[1] by turns.
+template <int FROM>
+__global__ __launch_bounds__(kAloneThreads) void sort_alone_kernel(const SortArgs a, const SortPasses p) {
+  __shared__ SortLds<kAloneThreads> lds;
+  if (blockIdx.x >= 1) {
+    write_zeros(a.zero_place, blockIdx.x - 1);
+    return;
+  }
+  SortArgs b = a;
+  b.key_out = p.keys[0];
+  b.item_out = p.items[0];
+  place_run<false, kAloneThreads, FROM>(b, lds);
+  for (uint32_t i = 1; i < p.passes; ++i) {
+    __syncthreads();  // what was placed is seen by all, and the counters are free
+    b.shift = i * p.digit;
+    b.key_in = p.keys[(i - 1) & 1];
+    b.item_in = p.items[(i - 1) & 1];
+    b.key_out = p.keys[i & 1];
+    b.item_out = p.items[i & 1];
+    place_run<false, kAloneThreads, kFromKeys>(b, lds);
+  }
+}
+
 }  // namespace
 
 // One run up to 8192 items (one launch a pass); else runs of 2048 items or,
@@ -237,11 +277,13 @@ uint32_t zero_groups(const ZeroRows& z) { return z.rows ? (z.rows + z.per - 1) /
 
 template <bool PLAN, int FROM>
 hipError_t sort_pass(const SortArgs& a, hipStream_t stream) {
-  const dim3 place(a.blocks + zero_groups(a.zero_place));
-  if (a.blocks == 1) {
-    hipLaunchKernelGGL((sort_place_kernel<PLAN, kAloneThreads, FROM>), place, dim3(kAloneThreads), 0, stream, a);
-    return hipGetLastError();
+  if constexpr (PLAN) {
+    if (a.blocks == 1) {
+      hipLaunchKernelGGL((sort_place_kernel<true, kAloneThreads, FROM>), dim3(1), dim3(kAloneThreads), 0, stream, a);
+      return hipGetLastError();
+    }
   }
+  const dim3 place(a.blocks + zero_groups(a.zero_place));
   hipLaunchKernelGGL((sort_hist_kernel<FROM>), dim3(a.blocks + zero_groups(a.zero_hist)), dim3(kRunThreads), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -251,10 +293,20 @@ hipError_t sort_pass(const SortArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_sort_pass(const SortArgs& a, bool plan, hipStream_t stream) {
-  if (plan) return a.id_bytes == 8 ? sort_pass<true, kFromIds8>(a, stream) : sort_pass<true, kFromIds4>(a, stream);
+hipError_t launch_plan(const SortArgs& a, hipStream_t stream) {
+  return a.id_bytes == 8 ? sort_pass<true, kFromIds8>(a, stream) : sort_pass<true, kFromIds4>(a, stream);
+}
+
+hipError_t launch_radix_pass(const SortArgs& a, hipStream_t stream) {
   if (a.key_in) return sort_pass<false, kFromKeys>(a, stream);
   return a.id_bytes == 8 ? sort_pass<false, kFromIds8>(a, stream) : sort_pass<false, kFromIds4>(a, stream);
+}
+
+hipError_t launch_radix_alone(const SortArgs& a, const SortPasses& p, hipStream_t stream) {
+  const dim3 grid(1 + zero_groups(a.zero_place)), block(kAloneThreads);
+  if (a.id_bytes == 8) hipLaunchKernelGGL((sort_alone_kernel<kFromIds8>), grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL((sort_alone_kernel<kFromIds4>), grid, block, 0, stream, a, p);
+  return hipGetLastError();
 }
 
 }  // namespace snac
