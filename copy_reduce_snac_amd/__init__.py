@@ -219,9 +219,10 @@ def _ptr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
-    raise TypeError(f"cannot take a device pointer from {type(x).__name__}")
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        raise TypeError(f"cannot take a device pointer from {type(x).__name__}") from None
 
 
 def _stream(s) -> int:

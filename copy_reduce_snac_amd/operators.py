@@ -20,15 +20,15 @@ _FLOAT = {torch.bfloat16: "bf16", torch.float32: "f32"}
 _ID = {torch.int32: 4, torch.int64: 8}
 
 
-# torch's current stream as a hipStream_t: torch.cuda.current_stream() makes a
-# Stream object for it, which takes longer (2.5 us) than a call's other checks
+# torch's current stream of a device as a hipStream_t: torch.cuda.current_stream()
+# makes a Stream object for it, which takes longer (2.5 us) than a call's other checks
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, device: int):
     if stream is not None:
         return stream
-    return _raw_stream(torch.cuda.current_device()) if _raw_stream else torch.cuda.current_stream()
+    return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device)
 
 
 def _float(t, what: str) -> str:
@@ -45,11 +45,15 @@ def _ids(t, what: str) -> int:
     return size
 
 
-def _device(what: str, *ts) -> None:
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    for t in ts:
-        if t is not None and t.get_device() != here:
+def _device(what: str, first, *others) -> int:
+    """The tensors' device, which has to be the current one."""
+    device = first.get_device()
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError(f"{what}: every tensor must be on the current device, not on {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"{what}: every tensor must be on the current device, not on {t.device}")
+    return device
 
 
 def _matrix(t, what: str) -> int:
@@ -98,9 +102,9 @@ def route(logits, weights, ids, *, bias=None, score: str = "softmax", groups: in
     _packed(weights, (t, k), torch.float32, "route: weights")
     if bias is not None:
         _packed(bias, (e,), torch.float32, "route: bias")
-    _device("route", logits, weights, ids, bias)
+    on = _device("route", logits, weights, ids, bias)
     snac_route(router(e, k, score, groups, topk_groups, group_top, renorm, scale), logits, ld, bias, t, dt, weights,
-               ids, _stream(stream))
+               ids, _stream(stream, on))
 
 
 def route_backward(logits, ids, dweights, dlogits, *, score: str = "softmax", renorm: bool = True, scale: float = 1.0,
@@ -116,9 +120,9 @@ def route_backward(logits, ids, dweights, dlogits, *, score: str = "softmax", re
     k = ids.shape[1]
     _packed(ids, (t, k), torch.int32, "route_backward: ids")
     _packed(dweights, (t, k), torch.float32, "route_backward: dweights")
-    _device("route_backward", logits, ids, dweights, dlogits)
+    on = _device("route_backward", logits, ids, dweights, dlogits)
     snac_route_backward(router(e, k, score, 1, 1, 1, renorm, scale), logits, ld, ids, dweights, t, dt, dlogits, ld_d,
-                        _stream(stream))
+                        _stream(stream, on))
 
 
 def dispatch_plan(ids, counts, row_of_slot, slot_of_row, handle, stream=None) -> None:
@@ -135,8 +139,8 @@ def dispatch_plan(ids, counts, row_of_slot, slot_of_row, handle, stream=None) ->
     _packed(counts, counts.shape, torch.int32, "dispatch_plan: counts")
     _packed(row_of_slot, ids.shape, torch.int32, "dispatch_plan: row_of_slot")
     _packed(slot_of_row, (n,), torch.int32, "dispatch_plan: slot_of_row")
-    _device("dispatch_plan", ids, counts, row_of_slot, slot_of_row)
-    snac_dispatch_plan(handle, ids, size, n, counts.shape[0], counts, row_of_slot, slot_of_row, _stream(stream))
+    on = _device("dispatch_plan", ids, counts, row_of_slot, slot_of_row)
+    snac_dispatch_plan(handle, ids, size, n, counts.shape[0], counts, row_of_slot, slot_of_row, _stream(stream, on))
 
 
 def _slots(row_of_slot, tokens: int, what: str) -> int:
@@ -157,8 +161,8 @@ def dispatch(x, row_of_slot, out, stream=None) -> None:
     k = _slots(row_of_slot, t, "dispatch")
     if out.shape[1] != w:
         raise ValueError("dispatch: x and out must have rows of the same width")
-    _device("dispatch", x, row_of_slot, out)
-    snac_dispatch(x, ld_x, row_of_slot, t, k, w, dt, out, ld_out, out.shape[0], _stream(stream))
+    on = _device("dispatch", x, row_of_slot, out)
+    snac_dispatch(x, ld_x, row_of_slot, t, k, w, dt, out, ld_out, out.shape[0], _stream(stream, on))
 
 
 def combine(y, row_of_slot, weights, out, stream=None) -> None:
@@ -173,8 +177,8 @@ def combine(y, row_of_slot, weights, out, stream=None) -> None:
         raise ValueError("combine: y and out must have rows of the same width")
     if weights is not None:
         _packed(weights, (t, k), torch.float32, "combine: weights")
-    _device("combine", y, row_of_slot, weights, out)
-    snac_combine(y, ld_y, y.shape[0], row_of_slot, weights, t, k, w, dt, out, ld_out, _stream(stream))
+    on = _device("combine", y, row_of_slot, weights, out)
+    snac_combine(y, ld_y, y.shape[0], row_of_slot, weights, t, k, w, dt, out, ld_out, _stream(stream, on))
 
 
 def combine_backward(dout, y, row_of_slot, weights, dy, dweights, stream=None) -> None:
@@ -190,9 +194,9 @@ def combine_backward(dout, y, row_of_slot, weights, dy, dweights, stream=None) -
         raise ValueError("combine_backward: rows of different widths, or dy without the shape of y")
     _packed(weights, (t, k), torch.float32, "combine_backward: weights")
     _packed(dweights, (t, k), torch.float32, "combine_backward: dweights")
-    _device("combine_backward", dout, y, row_of_slot, weights, dy, dweights)
+    on = _device("combine_backward", dout, y, row_of_slot, weights, dy, dweights)
     snac_combine_backward(dout, ld_g, y, ld_y, y.shape[0], row_of_slot, weights, t, k, w, dt, dy, ld_dy, dweights,
-                          _stream(stream))
+                          _stream(stream, on))
 
 
 def embedding(table, ids, out, *, first: int = 0, scale: float = 1.0, stream=None) -> None:
@@ -205,8 +209,8 @@ def embedding(table, ids, out, *, first: int = 0, scale: float = 1.0, stream=Non
     v, w = table.shape
     n, flat = _tokens(ids, out, w, "embedding", "out")
     size = _ids(ids, "embedding: ids")
-    _device("embedding", table, ids, out)
-    snac_embedding(table, ld, v, first, ids, size, n, w, scale, dt, out, flat, _stream(stream))
+    on = _device("embedding", table, ids, out)
+    snac_embedding(table, ld, v, first, ids, size, n, w, scale, dt, out, flat, _stream(stream, on))
 
 
 def _tokens(ids, rows, width: int, what: str, name: str):
@@ -235,18 +239,19 @@ def embedding_backward(dout, ids, dtable, handle, *, first: int = 0, pad: int | 
     v, w = dtable.shape
     n, ld = _tokens(ids, dout, w, "embedding_backward", "dout")
     size = _ids(ids, "embedding_backward: ids")
-    _device("embedding_backward", dout, ids, dtable)
+    on = _device("embedding_backward", dout, ids, dtable)
     # an id just below the shard is in no row of it
     pad_id = first - 1 if pad is None else pad
     snac_embedding_backward(handle, dout, ld, dt, ids, size, n, first, v, pad_id, w, scale, dtable, ld_t, gt,
-                            int(accumulate), _stream(stream))
+                            int(accumulate), _stream(stream, on))
 
 
 class GradList:
     """A fixed list of gradient tensors (bfloat16 and float32, contiguous, any
     shapes) for the norm and clipping; ``outs`` receives the clipped ones, by
     default the tensors themselves.  It keeps the tensors alive and reads them
-    where they lie at each call.  ``close()`` frees it."""
+    where they lie at each call.  ``close()``, or its end of life, waits for the
+    stream and frees it: not while a graph is captured."""
 
     def __init__(self, grads, outs=None, stream=None):
         self._h = None
@@ -255,8 +260,7 @@ class GradList:
         every = self.grads + (self.outs or [])
         if self.outs is not None and len(self.outs) != len(self.grads):
             raise ValueError(f"GradList: {len(self.grads)} tensors but {len(self.outs)} outputs")
-        if every:
-            _device("GradList", *every)
+        self.device = _device("GradList", *every) if every else torch.cuda.current_device()
         for t in every:
             if not t.is_contiguous():
                 raise ValueError("GradList: tensors must be contiguous")
@@ -265,7 +269,8 @@ class GradList:
             _pair(g, o, "GradList: a tensor and its output")
             if g.numel() != o.numel():
                 raise ValueError("GradList: a tensor and its output differ in length")
-        self._h = snac_grads_init(self.grads, self.outs, [t.numel() for t in self.grads], types, _stream(stream))
+        self._h = snac_grads_init(self.grads, self.outs, [t.numel() for t in self.grads], types,
+                                  _stream(stream, self.device))
 
     @property
     def handle(self):
@@ -276,7 +281,7 @@ class GradList:
     def close(self, stream=None) -> None:
         h, self._h = self._h, None
         if h is not None:
-            snac_grads_finalize(h, _stream(stream))
+            snac_grads_finalize(h, _stream(stream, self.device))
 
     def __del__(self):
         try:
@@ -285,25 +290,25 @@ class GradList:
             pass
 
 
-def _scalar(norm, what: str) -> None:
+def _scalar(norm, what: str) -> int:
     if norm.numel() != 1 or norm.dtype != torch.float32:
         raise ValueError(f"{what}: norm must be one float32")
-    _device(what, norm)
+    return _device(what, norm)
 
 
 def grad_norm(grads: GradList, norm, stream=None) -> None:
     """norm[0] = the 2-norm of all elements of the list."""
-    _scalar(norm, "grad_norm")
-    snac_grad_norm(grads.handle, norm, _stream(stream))
+    on = _scalar(norm, "grad_norm")
+    snac_grad_norm(grads.handle, norm, _stream(stream, on))
 
 
 def clip_grads(grads: GradList, norm, max_norm: float, stream=None) -> None:
     """The list's outputs = its tensors * min(1, max_norm / (norm + 1e-6))."""
-    _scalar(norm, "clip_grads")
-    snac_clip_grads(grads.handle, norm, max_norm, _stream(stream))
+    on = _scalar(norm, "clip_grads")
+    snac_clip_grads(grads.handle, norm, max_norm, _stream(stream, on))
 
 
 def clip_grad_norm(grads: GradList, max_norm: float, norm, stream=None) -> None:
     """``grad_norm`` into ``norm``, then ``clip_grads`` by it."""
-    _scalar(norm, "clip_grad_norm")
-    snac_clip_grad_norm(grads.handle, max_norm, norm, _stream(stream))
+    on = _scalar(norm, "clip_grad_norm")
+    snac_clip_grad_norm(grads.handle, max_norm, norm, _stream(stream, on))
