@@ -264,16 +264,19 @@ enum : int { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 // logits, 8 of them from 4 of 8 groups, take 15.2 us, 860 vector instructions
 // (32 of them transcendental) a wave of 4 tokens, 12.7 us of issue; the same
 // logits are read in 5.4 us.  (All keys in binary64, by a wave a token: 147.)
-// So a key is one 32-bit
-// number: the score's distance from the row's best, QB bits of it, above the
-// complement of the slot's number.  All keys of a token differ, they order as
-// the scores do down to their last bits, and the maximum over lanes is 4 to 6
-// instructions.  A lane sorts its V keys once; a round takes the largest
-// head over the lanes and shifts that lane's keys down.  What QB bits and
-// binary32 scores cannot tell apart is seen by comparing every choice with
-// the next one (one round more than topk): where they come as near as `tol`
-// steps without being equal in logit and bias, or are not finite, the token
-// is done again by route_exact.
+// So a key is one 32-bit number: the score's distance from the row's best, QB
+// bits of it, above the complement of the slot's number.  All keys of a token
+// differ, they order as the scores do down to their last bits, and the maximum
+// over lanes is 4 to 6 instructions.  A lane sorts its V keys once; a round
+// takes the largest head over the lanes and shifts that lane's keys down.
+//
+// What QB bits and binary32 scores cannot tell apart is seen by comparing every
+// choice with the next one (one round more than topk), and the last group that
+// stays with the first that does not.  Where two come as near as `tol` steps
+// without being equal in logit and bias, the choices and kMoreRounds after them
+// (or the groups, by their two largest keys) are ordered by their binary64
+// scores; a token that this does not settle, or that is not finite, is done
+// again by route_exact.
 //   no bias (keys order as the logits): the distance as a floating number of
 //     QB bits.  Distance and cut keep the order, so only equal codes of
 //     different logits are in doubt.
