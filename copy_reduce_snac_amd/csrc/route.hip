@@ -554,10 +554,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
 // unit u of lane l being the row's unit u L + l, for rows of whole units; else
 // by elements, j L + l.  Either way neighbouring lanes touch neighbouring
 // memory (32768 x 128 f32: 8.5 us; with a lane's 8 logits side by side, in two
-// units of every other 16 bytes, 10.1; 32 lanes of 4 logits 9.3).  The chosen experts' terms come to their lanes
-// by way of LDS: lane k < topk works choice k out and adds it to the row's
-// slot.  Bound by HBM: the row is read once (not at all where only the chosen
-// logits matter) and written once.
+// units of every other 16 bytes, 10.1; 32 lanes of 4 logits 9.3).  The chosen
+// experts' terms come to their lanes by way of LDS: lane k < topk works choice
+// k out and adds it to the row's slot.  Bound by HBM: the row is read once (not
+// at all where only the chosen logits matter) and written once.
 template <typename T, int L, int V, bool UNITS>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const RouteBackwardArgs a) {
   constexpr uint32_t TPW = 64 / L;
@@ -706,8 +706,8 @@ bool route_fits(const RouteArgs& a, hipStream_t stream) {
   uint32_t ps = group_shift(a.r, V);
   if (a.r.topk > KB || a.r.topk + kMoreRounds + 1 > L || (uint64_t)a.r.groups << ps > L) return false;
   if (a.r.groups == 1) ps = __builtin_ctz(L);
-  // a wave a set of tokens; in launches that a grid holds
-  const uint64_t per = kRouteWaves * (64 / L), most = per << 24;
+  // a wave a set of tokens; in launches of fewer than 2^32 threads
+  const uint64_t per = kRouteWaves * (64 / L), most = per << 23;
   RouteArgs c = a;
   for (uint64_t t = 0; t < a.tokens; t += most) {
     c.tokens = a.tokens - t < most ? a.tokens - t : most;
@@ -749,7 +749,7 @@ void route_by_key(const RouteArgs& a, hipStream_t stream) {
 
 template <typename T, int L, int V>
 void route_backward_in(const RouteBackwardArgs& a, hipStream_t stream) {
-  const uint64_t per = kRouteWaves * (64 / L), most = per << 24;
+  const uint64_t per = kRouteWaves * (64 / L), most = per << 23;
   RouteBackwardArgs c = a;
   for (uint64_t t = 0; t < a.tokens; t += most) {
     c.tokens = a.tokens - t < most ? a.tokens - t : most;

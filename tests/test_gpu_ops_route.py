@@ -203,6 +203,27 @@ def test_rows_past_32_bits(dtype):
     assert not bool(buf.any())
 
 
+def test_more_tokens_than_a_launch_holds():
+    """2^28 tokens and some are 2^32 threads and some: the same as calls of 2^26 tokens."""
+    torch = torch_()
+    n, part = 2 ** 28 + 77, 2 ** 26
+    x = torch.empty(n, 16, dtype=torch.bfloat16, device="cuda").normal_()
+    w, ids = torch.empty(n, 1, device="cuda"), torch.empty(n, 1, dtype=torch.int32, device="cuda")
+    dx = torch.empty_like(x)
+    ops().route(x, w, ids, renorm=False)
+    ops().route_backward(x, ids, w, dx, renorm=False)
+    for lo in range(0, n, part):
+        px = x[lo:lo + part]
+        pw, pids, pdx = torch.full_like(w[:len(px)], -1), torch.full_like(ids[:len(px)], -1), torch.empty_like(px)
+        ops().route(px, pw, pids, renorm=False)
+        ops().route_backward(px, pids, pw, pdx, renorm=False)
+        # the last part is small enough for another shape, whose softmax adds up in another order
+        same = len(px) == part
+        assert torch.equal(ids[lo:lo + part], pids), lo
+        assert torch.equal(w[lo:lo + part], pw) if same else torch.allclose(w[lo:lo + part], pw, rtol=192 * U, atol=0), lo
+        assert torch.equal(dx[lo:lo + part], pdx) if same else bool(dx[lo:].isfinite().all()), lo
+
+
 def test_ties_go_to_the_lowest_index():
     g = np.random.default_rng(9)
     x = g.integers(-2, 3, size=(200, 128)).astype(np.float64) / 4
