@@ -13,8 +13,8 @@ constexpr int kEmbWaves = kEmbThreads / 64;
 template <typename T, int U>
 constexpr uint32_t kEmbElems = 64u * U * kUnit<T>;
 
-// One wave a piece (U units a lane) of one token's row.  32768 rows of 4 KiB: 31 us (38 with
-// stores that stay in the caches).
+// One wave a piece (U units a lane) of one token's row.  32768 rows of 4 KiB:
+// 31 us (38 with stores that stay in the caches).
 template <typename T, int U>
 __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingArgs a, uint32_t pieces, uint64_t items) {
   constexpr uint32_t N = kUnit<T>;
@@ -44,8 +44,8 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 
 // ------------------------------------------------------------- gradient
 //
-// The sorted positions are cut into chunks of C (embed_chunk).  One wave takes a
-// chunk's slab of columns (a unit a lane), adds the rows of equal tokens in
+// The sorted positions are cut into chunks of C (embed_chunk).  One wave takes
+// a chunk's slab of columns (a unit a lane), adds the rows of equal tokens in
 // order and writes a run that lies inside the chunk; the sums of the runs
 // that cross its ends go to partial[chunk][0] (begun before it) and [1]
 // (begun in it), and embedding_join_kernel adds those up in order.  So a
@@ -326,13 +326,19 @@ hipError_t embedding_grad_in(const EmbedGradArgs& a, hipStream_t stream) {
   const uint64_t row_bytes = (uint64_t)a.width * TG::kSize, late = kJoinZeroBytes / row_bytes;
   const uint32_t join_zeros = chunks < 2 ? 0 : late < left ? (uint32_t)late : left;
   const uint32_t zero_to = a.vocab - join_zeros;
-  const uint64_t zeros = ((uint64_t)(left - join_zeros) + kZeroRows - 1) / kZeroRows;
-  if (adds + zeros > 0x7fffffffull) return hipErrorInvalidValue;  // not reached within the documented limits
-  if (adds + zeros) {
-    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC, C>), dim3((uint32_t)(adds + zeros)), dim3(kEmbThreads), 0, stream,
-                       a, slabs, items, (uint32_t)adds, zero_to);
+  uint64_t zeros = ((uint64_t)(left - join_zeros) + kZeroRows - 1) / kZeroRows;
+  // a launch has fewer than 2^32 threads; more rows than that take further ones
+  constexpr uint64_t kMostGroups = (1ull << 32) / kEmbThreads - 1;
+  if (adds > kMostGroups) return hipErrorInvalidValue;  // dout would be larger than the memory
+  EmbedGradArgs c = a;
+  for (uint64_t add = adds; add + zeros; add = 0) {
+    const uint64_t room = kMostGroups - add, now = zeros < room ? zeros : room;
+    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC, C>), dim3((uint32_t)(add + now)), dim3(kEmbThreads), 0, stream,
+                       c, slabs, items, (uint32_t)add, zero_to);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    c.zero_from += (uint32_t)now * kZeroRows;
+    zeros -= now;
   }
   if (chunks < 2) return hipSuccess;
   slabs = (a.width + 4 * kEmbThreads - 1) / (4 * kEmbThreads);

@@ -3,18 +3,19 @@
 // tokens.
 //
 // The items are cut into `blocks` runs.  With one run a single workgroup
-// counts and places them (all passes of a radix sort in one launch); otherwise sort_hist_kernel counts every run's bins
-// and sort_place_kernel places: item i goes to
+// counts and places them (all passes of a radix sort in one launch); otherwise
+// sort_hist_kernel counts every run's bins and sort_place_kernel places: item i
+// goes to
 //     (items of lower bins) + (items of its bin in earlier runs)
 //       + (items of its bin before it in its run).
 // Every workgroup works the first two out for itself from the counts of all
 // runs (they stay in L2), which costs less than a launch of its own.  In a
 // run each wave owns a contiguous part and its own 16-bit counters, and a
 // lane's rank among equal bins of its wave comes from ballots over the bin's
-// bits, so that the order needs no atomics and is the same every time.  (Counting a radix
-// pass's bins with integer atomics while the pass before it places took 19 us
-// more than a launch of sort_hist_kernel, 4.8 us: frequent tokens make them
-// meet.)
+// bits, so that the order needs no atomics and is the same every time.
+// (Counting a radix pass's bins with integer atomics while the pass before it
+// places took 19 us more than a launch of sort_hist_kernel, 4.8 us: frequent
+// tokens make them meet.)
 //
 // The passes are bound by latency, launches and first loads: 131072 slots of
 // 256 experts take 4.8 us (counting) and 8.3 us (placing) in 64 runs of 2048;
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(kAloneThreads) void sort_alone_kernel(const SortArg
 
 }  // namespace
 
-// One run up to 8192 items (one launch a pass); else runs of 2048 items or,
+// One run up to 8192 items (one launch); else runs of 2048 items or,
 // past 256 of them, of as many more as keep to that, while a run's items fit
 // the 16-bit counters.
 void sort_shape(uint32_t n, uint32_t* blocks, uint32_t* chunk) {

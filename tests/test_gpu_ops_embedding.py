@@ -212,6 +212,22 @@ def test_offsets_past_32_bits(torch, handle):
     assert not bool(table.any())
 
 
+@pytest.mark.parametrize("tokens", [0, 3, 9000])
+def test_more_rows_than_a_launch_holds(torch, handle, tokens):
+    """Zeros of 2^28 rows and some are 2^32 threads and some."""
+    vocab = 2 ** 28 + 2 ** 24 + 5
+    g = torch.Generator().manual_seed(tokens)
+    ids = torch.randint(0, vocab, (tokens,), generator=g)
+    ids[:3] = torch.tensor([vocab - 1, 2 ** 28, 0])[:tokens]
+    ids = ids.cuda()
+    table = torch.full((vocab, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    ops().embedding_backward(torch.ones(tokens, 1, device="cuda"), ids, table, handle)
+    named, times = ids.unique(return_counts=True)
+    assert torch.equal(table[named, 0].float(), times.float())
+    table[named] = 0
+    assert not bool(table.any())
+
+
 def test_gradient_against_differences(torch, handle):
     """The lookup is linear in the table, so a difference of its outputs at two tables is exact but for rounding: each
     output is off by 2 half steps, over tokens of them, and the step divides it."""
