@@ -399,33 +399,32 @@ snac_status snac_embedding_backward(snac_ctx* ctx, const void* dout, size_t ld_d
       g.zero_from += z.rows;
       return z;
     };
-    SortPasses r{passes, digit, {}, {}};
-    for (int i = 0; i < 2; ++i) {
-      r.keys[i] = reinterpret_cast<uint32_t*>(scratch + at.keys[i]);
-      r.items[i] = reinterpret_cast<int32_t*>(scratch + at.items[i]);
-    }
+    uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(scratch + at.keys[0]), reinterpret_cast<uint32_t*>(scratch + at.keys[1])};
+    int32_t* const items[2] = {reinterpret_cast<int32_t*>(scratch + at.items[0]), reinterpret_cast<int32_t*>(scratch + at.items[1])};
     a.mask = (1u << digit) - 1;
     a.bins = 1u << digit;
     a.hist = reinterpret_cast<uint32_t*>(scratch + at.hist);
     if (a.blocks == 1) {
       a.zero_place = zeros(kPlaceZeroBytes);
-      const hipError_t e = launch_radix_alone(a, r, (hipStream_t)stream);
+      a.key_out = keys[0];
+      a.item_out = items[0];
+      const hipError_t e = launch_radix_alone(a, passes, digit, (hipStream_t)stream);
       if (e != hipSuccess) return hip_fail(e, "snac_embedding_backward sort launch");
     } else {
       for (uint32_t p = 0; p < passes; ++p) {
         a.shift = p * digit;
         a.zero_hist = zeros(kHistZeroBytes);
         a.zero_place = zeros(kPlaceZeroBytes);
-        a.key_out = r.keys[p & 1];
-        a.item_out = r.items[p & 1];
+        a.key_out = keys[p & 1];
+        a.item_out = items[p & 1];
         const hipError_t e = launch_radix_pass(a, (hipStream_t)stream);
         if (e != hipSuccess) return hip_fail(e, "snac_embedding_backward sort launch");
         a.key_in = a.key_out;
         a.item_in = a.item_out;
       }
     }
-    g.keys = r.keys[(passes - 1) & 1];
-    g.tokens = r.items[(passes - 1) & 1];
+    g.keys = a.key_out;
+    g.tokens = a.item_out;
   }
   const hipError_t e = launch_embedding_grad(g, dtype == SNAC_BF16, grad_dtype == SNAC_BF16, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_embedding_backward launch");

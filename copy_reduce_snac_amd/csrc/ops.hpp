@@ -85,19 +85,17 @@ struct SortArgs {
   // idle for their latency
   ZeroRows zero_hist, zero_place;
 };
+// Most items that one workgroup sorts alone; a radix sort of so many is one
+// launch.
+constexpr uint32_t kSortAlone = 8192;
 // blocks and chunk of a pass over n items
 void sort_shape(uint32_t n, uint32_t* blocks, uint32_t* chunk);
 constexpr uint32_t sort_hist_ld(uint32_t blocks) { return (blocks + 3) & ~3u; }
 uint64_t sort_hist_words(uint32_t blocks, uint32_t bins);  // of one pass
-// The passes of a radix sort of one run.
-struct SortPasses {
-  uint32_t passes, digit;  // bits a pass
-  uint32_t* keys[2];
-  int32_t* items[2];
-};
 hipError_t launch_plan(const SortArgs& a, hipStream_t stream);
 hipError_t launch_radix_pass(const SortArgs& a, hipStream_t stream);  // several runs
-hipError_t launch_radix_alone(const SortArgs& a, const SortPasses& p, hipStream_t stream);
+// one run: all passes of `digit` bits each
+hipError_t launch_radix_alone(const SortArgs& a, uint32_t passes, uint32_t digit, hipStream_t stream);
 
 // ------------------------------------------------- dispatch and combine
 struct DispatchArgs {
