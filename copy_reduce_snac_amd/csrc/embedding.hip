@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 // to all of its rows, after that to those that no key names.
 //
 // 32768 tokens (10500 different ones) of 2048 bf16 into 65536 x 2048 f32, 671
-// MB, take 138 us (4.9 TB/s).  A chunk's rows are all in flight before the
+// MB, take 134 us (5.0 TB/s).  A chunk's rows are all in flight before the
 // first sum is written, since a load issued after a store waits for it: 32
 // rows at a time 164 us, 16: 173, 8: 178, 4: 182 (before the zeros moved
 // beside the other launches).  Zeros stream (150 us for 159); the sums do not,
@@ -102,45 +102,58 @@ __device__ __forceinline__ void put_unit(const EmbedGradArgs& a, uint32_t key, u
   }
 }
 
-// Zeros for the rows that no token names: a workgroup takes kZeroRows rows,
-// finds their part of the sorted keys (64 probes a step) and marks those that it
-// meets.
-constexpr uint32_t kZeroRows = 16;
+// Zeros for the rows that no token names, kZeroBytes of them a workgroup where
+// they are that long: `per` rows, or `cols` columns of one.  It finds its
+// rows' part of the sorted keys and marks those that it meets.  Small groups
+// keep what is written at a time close together; the search, of kProbes keys
+// a step, must not read more lines than they write.  us, 16384 tokens into
+// 131072 x 4096 f32: groups of 12 / 16 / 32 KiB 628 / 369 / 426, of 16 rows
+// 418; 8 / 16 / 32 / 48 / 256 keys a step 418 / 392 / 369 / 367 / 447.
+constexpr uint32_t kZeroRows = 16;  // at most
+constexpr uint32_t kZeroBytes = 16384;
+constexpr uint32_t kProbes = 48;
 constexpr uint64_t kJoinZeroBytes = 32ull << 20;  // of zeros beside the joining
+struct ZeroShape {
+  uint32_t per, cols, slabs;  // slabs: of cols columns in a row
+  __host__ __device__ uint64_t groups(uint64_t rows) const { return (rows + per - 1) / per * slabs; }
+};
 
 template <typename TG>
-__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, uint32_t lo, uint32_t to, uint32_t* met,
-                                          uint32_t* ends) {
-  const uint32_t rows = to - lo < kZeroRows ? to - lo : kZeroRows;
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, uint32_t wg, uint32_t from, uint32_t to, const ZeroShape z,
+                                          uint32_t* met, uint32_t* start) {
+  uint32_t set = wg, col = 0;
+  if (z.slabs > 1) set = wg / z.slabs, col = (wg - set * z.slabs) * z.cols;
+  const uint32_t lo = from + set * z.per, rows = to - lo < z.per ? to - lo : z.per;
+  const uint32_t cols = a.width - col < z.cols ? a.width - col : z.cols;
   if (threadIdx.x < kZeroRows) met[threadIdx.x] = 0;
-  if (wave_id() < 2) {
-    // the first position whose key is not below `key`, 64 probes at a time
-    const uint32_t key = lo + (wave_id() ? rows : 0), lane = threadIdx.x & 63u;
+  if (wave_id() == 0) {
+    // the first position whose key is not below lo, kProbes at a time
+    const uint32_t lane = threadIdx.x & 63u;
     uint32_t b = 0, e = a.n;
     while (b < e) {
-      const uint32_t step = (e - b + 63) / 64;
-      const uint32_t at = b + lane * step;  // lanes whose probe lies past the end answer no
-      const uint32_t below = (uint32_t)__popcll(__ballot(at < e && a.keys[at < e ? at : b] < key));
+      const uint32_t step = (e - b + kProbes - 1) / kProbes;
+      const uint32_t at = b + lane * step;  // a probe past the end answers no
+      const bool probe = lane < kProbes && at < e;
+      const uint32_t below = (uint32_t)__popcll(__ballot(probe && a.keys[probe ? at : b] < lo));
       // probes 0 .. below - 1 are below: the answer lies after the last of them
       if (below == 0) {
         e = b;
       } else {
-        e = below < 64 && b + below * step < e ? b + below * step : e;
+        e = below < kProbes && b + below * step < e ? b + below * step : e;
         b += (below - 1) * step + 1;
       }
     }
-    if (lane == 0) ends[wave_id()] = b;
+    if (lane == 0) *start = b;
   }
   __syncthreads();
-  for (uint32_t i = ends[0] + threadIdx.x; i < ends[1]; i += kEmbThreads) met[a.keys[i] - lo] = 1;
-  __syncthreads();
-  const u32x4 zero[4] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
-  constexpr uint32_t step = 64u * 4 * kUnit<TG>;
-  for (uint32_t r = wave_id(); r < rows; r += kEmbWaves) {
-    if (met[r]) continue;
-    char* row = a.dtable + (uint64_t)(lo + r) * a.ld_dtable;
-    for (uint32_t e = 0; e < a.width; e += step) st_piece<TG, 4, true>(row + (uint64_t)e * TG::kSize, a.width - e, zero);
+  for (uint32_t i = *start + threadIdx.x; i < a.n; i += kEmbThreads) {
+    const uint32_t r = a.keys[i] - lo;
+    if (r >= rows) break;
+    met[r] = 1;
   }
+  __syncthreads();
+  put_zeros<TG>(a.dtable + (uint64_t)lo * a.ld_dtable + (uint64_t)col * TG::kSize, a.ld_dtable, cols, rows,
+                [&](uint32_t r) { return met[r] != 0; });
 }
 
 // One chunk's slab of 64 units of columns from `col0` on, by one wave.  WHOLE:
@@ -225,11 +238,12 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
 // The first `adds` workgroups add, the rest write zeros as those finish.
 template <typename T, typename TG, bool ACC, uint32_t C>
 __global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const EmbedGradArgs a, uint32_t slabs,
-                                                                     uint64_t items, uint32_t adds, uint32_t zero_to) {
+                                                                     uint64_t items, uint32_t adds, uint32_t zero_to,
+                                                                     const ZeroShape z) {
   __shared__ uint32_t met[kZeroRows];
-  __shared__ uint32_t ends[2];
+  __shared__ uint32_t start;
   if (!ACC && blockIdx.x >= adds) {
-    zero_rows<TG>(a, a.zero_from + (blockIdx.x - adds) * kZeroRows, zero_to, met, ends);
+    zero_rows<TG>(a, blockIdx.x - adds, a.zero_from, zero_to, z, met, &start);
     return;
   }
   const uint64_t it = (uint64_t)blockIdx.x * kEmbWaves + wave_id();
@@ -251,11 +265,11 @@ constexpr int kJoinLoads = 16;
 
 template <typename TG, bool ACC, uint32_t C>
 __global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const EmbedGradArgs a, uint32_t slabs, uint32_t joins,
-                                                                     uint32_t zero_from) {
+                                                                     uint32_t zero_from, const ZeroShape z) {
   __shared__ uint32_t met[kZeroRows];
-  __shared__ uint32_t ends[2];
+  __shared__ uint32_t start;
   if (!ACC && blockIdx.x >= joins) {
-    zero_rows<TG>(a, zero_from + (blockIdx.x - joins) * kZeroRows, a.vocab, met, ends);
+    zero_rows<TG>(a, blockIdx.x - joins, zero_from, a.vocab, z, met, &start);
     return;
   }
   const uint32_t lane = threadIdx.x & 63u;
@@ -326,25 +340,29 @@ hipError_t embedding_grad_in(const EmbedGradArgs& a, hipStream_t stream) {
   const uint64_t row_bytes = (uint64_t)a.width * TG::kSize, late = kJoinZeroBytes / row_bytes;
   const uint32_t join_zeros = chunks < 2 ? 0 : late < left ? (uint32_t)late : left;
   const uint32_t zero_to = a.vocab - join_zeros;
-  uint64_t zeros = ((uint64_t)(left - join_zeros) + kZeroRows - 1) / kZeroRows;
+  constexpr uint32_t kCols = kZeroBytes / TG::kSize;
+  const uint32_t fit = a.width > kCols / kZeroRows ? kCols / a.width : kZeroRows;
+  const ZeroShape z{fit ? fit : 1, kCols, (a.width + kCols - 1) / kCols};
+  uint32_t rows = left - join_zeros;
   // a launch has fewer than 2^32 threads; more rows than that take further ones
   constexpr uint64_t kMostGroups = (1ull << 32) / kEmbThreads - 1;
   if (adds > kMostGroups) return hipErrorInvalidValue;  // dout would be larger than the memory
   EmbedGradArgs c = a;
-  for (uint64_t add = adds; add + zeros; add = 0) {
-    const uint64_t room = kMostGroups - add, now = zeros < room ? zeros : room;
-    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC, C>), dim3((uint32_t)(add + now)), dim3(kEmbThreads), 0, stream,
-                       c, slabs, items, (uint32_t)add, zero_to);
+  for (uint64_t add = adds; add || rows; add = 0) {
+    const uint64_t most = (kMostGroups - add) / z.slabs * z.per;  // rows
+    const uint32_t now = rows < most ? rows : (uint32_t)most;
+    hipLaunchKernelGGL((embedding_grad_kernel<T, TG, ACC, C>), dim3((uint32_t)(add + z.groups(now))), dim3(kEmbThreads), 0,
+                       stream, c, slabs, items, (uint32_t)add, zero_to, z);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    c.zero_from += (uint32_t)now * kZeroRows;
-    zeros -= now;
+    c.zero_from += now;
+    rows -= now;
   }
   if (chunks < 2) return hipSuccess;
   slabs = (a.width + 4 * kEmbThreads - 1) / (4 * kEmbThreads);
   const uint32_t joins = (chunks - 1) * slabs;
-  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC, C>), dim3(joins + (join_zeros + kZeroRows - 1) / kZeroRows),
-                     dim3(kEmbThreads), 0, stream, a, slabs, joins, zero_to);
+  hipLaunchKernelGGL((embedding_join_kernel<TG, ACC, C>), dim3(joins + (uint32_t)z.groups(join_zeros)),
+                     dim3(kEmbThreads), 0, stream, a, slabs, joins, zero_to, z);
   return hipGetLastError();
 }
 

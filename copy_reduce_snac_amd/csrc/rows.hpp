@@ -207,14 +207,23 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
+// Zeros to `rows` rows of `width` elements from `p` on, but those that `skip`
+// names, by the whole workgroup: a wave a piece, in the order of the addresses.
+template <typename T, typename Skip>
+__device__ __forceinline__ void put_zeros(char* p, uint64_t ld, uint32_t width, uint32_t rows, Skip skip) {
+  const u32x4 zero[4] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  constexpr uint32_t step = 64u * 4 * kUnit<T>;
+  const uint32_t pieces = (width + step - 1) / step;
+  for (uint32_t i = wave_id(); i < rows * pieces; i += blockDim.x >> 6) {
+    const uint32_t r = i / pieces, e = (i - r * pieces) * step;
+    if (!skip(r)) st_piece<T, 4, true>(p + r * ld + (uint64_t)e * T::kSize, width - e, zero);
+  }
+}
+
 // A workgroup's share of ZeroRows, `wg` counted from the first that has one.
 __device__ __forceinline__ void write_zeros(const ZeroRows& z, uint32_t wg) {
-  const u32x4 zero[4] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
-  constexpr uint32_t step = 64u * 4 * kUnit<BF16>;
-  const uint32_t lo = wg * z.per, hi = z.rows - lo < z.per ? z.rows : lo + z.per;
-  for (uint32_t r = lo + wave_id(); r < hi; r += blockDim.x >> 6)
-    for (uint32_t e = 0; e < z.width; e += step)
-      st_piece<BF16, 4, true>(z.p + r * z.ld + (uint64_t)e * 2, z.width - e, zero);
+  const uint32_t lo = wg * z.per, rows = z.rows - lo < z.per ? z.rows - lo : z.per;
+  put_zeros<BF16>(z.p + lo * z.ld, z.ld, z.width, rows, [](uint32_t) { return false; });
 }
 
 // id of item i of an id array of 4- or 8-byte elements

@@ -194,6 +194,23 @@ def test_backward_of_ragged_widths(torch, handle, width, accumulate):
         backward_case(torch, handle, "bf16", "f32", "int64", tokens, vocab, 0, width, 0, accumulate, ids)
 
 
+@pytest.mark.parametrize("dtype,grad,width", [("bf16", "f32", 4095), ("bf16", "f32", 4097), ("bf16", "bf16", 8200),
+                                              ("f32", "f32", 12289), ("f32", "bf16", 16385)])
+@pytest.mark.parametrize("tokens", [5, 200, 9000])
+def test_backward_of_wide_rows(torch, handle, dtype, grad, width, tokens):
+    """Rows whose zeros are more than one workgroup's; a few rows without a token, and most."""
+    vocab = 9300 if tokens == 9000 else 230
+    g = np.random.default_rng(width + tokens)
+    ids = g.integers(0, vocab, tokens)
+    d = torch.ones(tokens, width, dtype=getattr(torch, DT[dtype]), device="cuda")
+    dt = torch.full((vocab, width + 3), 77.0, dtype=getattr(torch, DT[grad]), device="cuda")
+    ops().embedding_backward(d, torch.tensor(ids, device="cuda"), dt[:, 1:width + 1], handle)
+    n = torch.bincount(torch.tensor(ids, device="cuda"), minlength=vocab)  # small whole numbers: exact in bf16
+    assert int(n.max()) <= 256
+    assert torch.equal(dt[:, 1:width + 1], n[:, None].to(dt.dtype).expand(vocab, width))
+    assert bool((dt[:, 0] == 77).all()) and bool((dt[:, width + 1:] == 77).all())
+
+
 def test_offsets_past_32_bits(torch, handle):
     """A table and its gradient of more than 2^32 bytes: first and last rows, zeros between."""
     vocab, width = 150000, 8192
