@@ -2,6 +2,8 @@
 // (snac_embedding, snac_embedding_backward in include/snac_ops.h).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ops.hpp"
 #include "rows.hpp"
 
@@ -51,7 +53,8 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 // (begun in it), and embedding_join_kernel adds those up in order.  So a
 // token that makes up half the text is spread over as many waves as a
 // hundred rare ones, no atomics are needed, and the order of every sum is
-// fixed by the ids alone.  The work is bound by HBM (dout once, dtable once),
+// fixed by the ids alone.  However long a run, its sum is off by one rounding
+// of each chunk's sum and one of the whole.  The work is bound by HBM (dout once, dtable once),
 // and the sort before it and the joining after it by latency, so the zeros of
 // the rows without a token are written beside all of them: workgroups past a
 // launch's own write zeros to a part of the table, before the keys are sorted
@@ -64,10 +67,27 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_kernel(const EmbeddingA
 // beside the other launches).  Zeros stream (150 us for 159); the sums do not,
 // whose lanes write 16 of every 32 bytes at a time (177 us for 150).
 
+// A lane's sums within a chunk.  Rows of binary32 are added in binary64: 32 of
+// them in binary32 are off by up to 31 half steps.  Rows of bf16 in binary32,
+// which holds a sum of 32 of them exactly unless some are 2^11 times smaller
+// than others; twice the registers would take a wave of three off each SIMD.
+template <typename T>
+using Sum = std::conditional_t<T::kSize == 4, double, float>;
+
+// A sum scaled, and (ACC) added to `old`, with one rounding to binary32.
+template <bool ACC>
+__device__ __forceinline__ float scaled(float sum, float scale, float old) {
+  return ACC ? __builtin_fmaf(sum, scale, old) : sum * scale;
+}
+template <bool ACC>
+__device__ __forceinline__ float scaled(double sum, float scale, float old) {
+  return (float)(ACC ? __builtin_fma(sum, (double)scale, (double)old) : sum * (double)scale);
+}
+
 // kUnit<T> sums of one lane -> columns first .. first + n of row `key`.
 template <typename T, typename TG, bool ACC>
 __device__ __forceinline__ void put_unit(const EmbedGradArgs& a, uint32_t key, uint32_t first, uint32_t n,
-                                         const float (&acc)[kUnit<T>]) {
+                                         const Sum<T> (&acc)[kUnit<T>]) {
   constexpr uint32_t N = kUnit<T>, NG = kUnit<TG>;
   char* p = a.dtable + (uint64_t)key * a.ld_dtable + (uint64_t)first * TG::kSize;
   // pieces of whole units of the gradient's type, or of half a unit (f32
@@ -79,23 +99,17 @@ __device__ __forceinline__ void put_unit(const EmbedGradArgs& a, uint32_t key, u
     char* q = p + c0 * TG::kSize;
     const uint32_t m = n - c0 < M ? n - c0 : M;
     if (M == NG && m == M) {
-      float f[NG];
+      float f[NG], old[NG] = {};
+      if constexpr (ACC) unpack<TG>(ld_unit<false>(q), old);
 #pragma unroll
-      for (uint32_t c = 0; c < NG; ++c) f[c] = c < M ? acc[c0 + (c < M ? c : 0)] * a.scale : 0.0f;
-      if constexpr (ACC) {
-        float old[NG];
-        unpack<TG>(ld_unit<false>(q), old);
-#pragma unroll
-        for (uint32_t c = 0; c < NG; ++c) f[c] = old[c] + f[c];
-      }
+      for (uint32_t c = 0; c < NG; ++c) f[c] = c < M ? scaled<ACC>(acc[c0 + (c < M ? c : 0)], a.scale, old[c]) : 0.0f;
       st_unit<false>(q, pack<TG>(f));
     } else {
 #pragma unroll
       for (uint32_t c = 0; c < M; ++c) {
         if (c < m) {
-          float v = acc[c0 + c] * a.scale;
-          if constexpr (ACC) v = load_elem<TG>(q + c * TG::kSize) + v;
-          store_elem<TG>(q + c * TG::kSize, v);
+          char* to = q + c * TG::kSize;
+          store_elem<TG>(to, scaled<ACC>(acc[c0 + c], a.scale, ACC ? load_elem<TG>(to) : 0.0f));
         }
       }
     }
@@ -182,9 +196,9 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
   auto key_of = [&](uint32_t i) { return (uint32_t)__builtin_amdgcn_readlane((int)my_key, (int)i); };
   uint32_t cur = key_of(0);
   bool head = key_of(62) == cur && lo > 0;
-  float acc[N];
+  Sum<T> acc[N];
 #pragma unroll
-  for (uint32_t c = 0; c < N; ++c) acc[c] = 0.0f;
+  for (uint32_t c = 0; c < N; ++c) acc[c] = 0;
   auto flush = [&](bool tail) {
     if (head || tail) {
       float* p = a.partial + ((uint64_t)chunk * 2 + (head ? 0 : 1)) * wide + first;
@@ -192,8 +206,9 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
       if (n) {
 #pragma unroll
         for (uint32_t c = 0; c < N; c += 4)
-          st_unit<false>(reinterpret_cast<char*>(p + c), u32x4{__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]),
-                                                              __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3])});
+          st_unit<false>(reinterpret_cast<char*>(p + c),
+                         u32x4{__float_as_uint((float)acc[c]), __float_as_uint((float)acc[c + 1]),
+                               __float_as_uint((float)acc[c + 2]), __float_as_uint((float)acc[c + 3])});
       }
     } else {
       put_unit<T, TG, ACC>(a, cur, first, n, acc);
@@ -223,7 +238,7 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
           head = false;
           cur = key;
 #pragma unroll
-          for (uint32_t c = 0; c < N; ++c) acc[c] = 0.0f;
+          for (uint32_t c = 0; c < N; ++c) acc[c] = 0;
         }
         float f[N];
         unpack<T>(v[j], f);
@@ -235,11 +250,14 @@ __device__ __forceinline__ void add_chunk(const EmbedGradArgs& a, uint32_t chunk
   flush(key_of(63) == cur);
 }
 
-// The first `adds` workgroups add, the rest write zeros as those finish.
+// The first `adds` workgroups add, the rest write zeros as those finish.  Three
+// waves a SIMD, but where the registers for that do not suffice.
+template <typename T, typename TG, bool ACC>
+constexpr int kGradWaves = ACC && T::kSize > TG::kSize ? 2 : 3;
+
 template <typename T, typename TG, bool ACC, uint32_t C>
-__global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const EmbedGradArgs a, uint32_t slabs,
-                                                                     uint64_t items, uint32_t adds, uint32_t zero_to,
-                                                                     const ZeroShape z) {
+__global__ __launch_bounds__(kEmbThreads, (kGradWaves<T, TG, ACC>)) void embedding_grad_kernel(
+    const EmbedGradArgs a, uint32_t slabs, uint64_t items, uint32_t adds, uint32_t zero_to, const ZeroShape z) {
   __shared__ uint32_t met[kZeroRows];
   __shared__ uint32_t start;
   if (!ACC && blockIdx.x >= adds) {
@@ -261,6 +279,10 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_grad_kernel(const Embed
 
 // The runs that cross chunks: the chunk that a run begins in adds up its
 // partial sums, a lane for each 4 columns, kJoinLoads rows of them in flight.
+// They are binary32 (as binary64 they would need twice the scratch), off by
+// half a step of each, but added in binary64: a run may have 2^19 of them, whose
+// sum in binary32 lost 1e-3 of itself.  65536 tokens into 1000 x 1024: 69 us
+// in all, 67 with a binary32 sum.
 constexpr int kJoinLoads = 16;
 
 template <typename TG, bool ACC, uint32_t C>
@@ -292,7 +314,8 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const Embed
   if (col >= a.width) return;
   const float* p = a.partial + (uint64_t)chunk * 2 * wide + col;
   typedef float f32x4 __attribute__((ext_vector_type(4)));
-  f32x4 acc = *reinterpret_cast<const f32x4*>(p + wide);
+  const f32x4 own = *reinterpret_cast<const f32x4*>(p + wide);
+  double sum[4] = {own[0], own[1], own[2], own[3]};
   for (uint32_t m = 1; m <= more; m += kJoinLoads) {
     f32x4 v[kJoinLoads];
 #pragma unroll
@@ -300,9 +323,11 @@ __global__ __launch_bounds__(kEmbThreads) void embedding_join_kernel(const Embed
       v[j] = *reinterpret_cast<const f32x4*>(p + (uint64_t)(m + j <= more ? m + j : more) * 2 * wide);
 #pragma unroll
     for (int j = 0; j < kJoinLoads; ++j)
-      if (m + j <= more) acc += v[j];
+      if (m + j <= more) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[c] += v[j][c];
+      }
   }
-  const float sum[4] = {acc[0], acc[1], acc[2], acc[3]};
   put_unit<F32, TG, ACC>(a, key, col, a.width - col < 4 ? a.width - col : 4, sum);
 }
 

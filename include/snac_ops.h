@@ -164,12 +164,15 @@ snac_status snac_embedding(const void* table, size_t ld_table, size_t vocab, int
 /*
  * snac_embedding_backward -- the gradient of the shard:
  *   dtable[v] = scale * sum of dout[t] over the tokens t with id first + v
- * in binary32: tokens in ascending order, in runs of the sorted order whose
- * sums are then added in order; one rounding to dtable's type.
+ * with tokens in ascending order: up to 32 of them make a partial sum (rows
+ * of binary32 added in binary64, rows of bf16 in binary32), rounded to binary32;
+ * a token's partial sums are added in order in binary64, and the scaled sum is
+ * rounded to binary32 and that to dtable's type.
  *   pad_id      ids equal to it have no gradient (any absent id: none)
  *   dtype, grad_dtype   types of dout and of dtable
  *   accumulate  0: dtable is written whole, zeros where no token came;
- *               1: the sums are added to it (one rounding), other rows stay
+ *               1: the scaled sums are added to it before that rounding, other
+ *               rows stay
  * Scratch is the context's staging rings: snac_embedding_scratch bytes
  * (SNAC_E_ARG if the rings together are smaller).  vocab < 2^30.
  */
