@@ -659,9 +659,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
 #pragma unroll
     for (int c = 0; c < C; ++c) g[c] = r[c] * g[c] * (dw[c] - dot);
   }
+  // zeros, then the other lanes' terms, then this lane's slots
+  wave_lds_order();
 #pragma unroll
   for (int c = 0; c < C; ++c)
     if (have[c]) atomicAdd(&row_up[id[c]], g[c]);
+  wave_lds_order();
   float d[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) d[j] = row_up[at(j)];

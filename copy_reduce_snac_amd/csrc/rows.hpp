@@ -142,6 +142,15 @@ __device__ __forceinline__ void st_piece(char* row, uint32_t left, const u32x4 (
   }
 }
 
+// What this wave's lanes wrote to LDS before is what its lanes read after: LDS
+// keeps a wave's order by itself, this keeps the compiler to it (which may
+// otherwise take a lane's own store for what it reads back).  No instructions.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 __device__ __forceinline__ uint32_t wave_id() { return uniform(threadIdx.x >> 6); }
 
 // ---- reductions over L = 16, 32 or 64 neighbouring lanes, every lane with
