@@ -84,7 +84,11 @@ __device__ __forceinline__ uint64_t same_bin(uint32_t bin, bool on, uint32_t bit
   return (uint64_t)hi << 32 | lo;
 }
 
-// Place of this lane's item among the wave's items of its bin, counting it.
+// Two of the 16-bit counters at a time.
+typedef uint32_t __attribute__((may_alias)) two_counts;
+
+// Place of this lane's item among the wave's items of its bin, counting it for
+// the lanes of the next call.
 __device__ __forceinline__ uint32_t place_in_wave(uint16_t* count, uint32_t bin, bool on, uint32_t bits, uint32_t lane) {
   const uint64_t same = same_bin(bin, on, bits);
   uint32_t place = 0;
@@ -92,6 +96,7 @@ __device__ __forceinline__ uint32_t place_in_wave(uint16_t* count, uint32_t bin,
     place = count[bin] + (uint32_t)__popcll(same & ((1ull << lane) - 1));
     if ((same >> lane) == 1) count[bin] = (uint16_t)(place + 1);  // the last of them
   }
+  wave_lds_order();
   return place;
 }
 
@@ -128,7 +133,8 @@ __device__ __forceinline__ void place_run(const SortArgs& a, Lds& lds, bool stay
   const uint32_t wlo = lo + wave * per < hi ? lo + wave * per : hi;
   const uint32_t whi = hi - wlo < per ? hi : wlo + per;
   uint16_t* mine = wave_count[wave];
-  for (uint32_t b = lane; b < BINS / 2; b += 64) reinterpret_cast<uint32_t*>(mine)[b] = 0;
+  for (uint32_t b = lane; b < BINS / 2; b += 64) reinterpret_cast<two_counts*>(mine)[b] = 0;
+  wave_lds_order();
   // R keys a lane at a time; a wave's part is seldom more, and then they stay
   constexpr uint32_t R = TH == kAloneThreads ? 8 : 4;
   uint32_t key[R], place[R], item[R];

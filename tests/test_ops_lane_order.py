@@ -15,7 +15,8 @@ from copy_reduce_snac_amd.build import CSRC, DEVICE_FLAGS, HIPCC, SOURCE_FLAGS
 
 pytestmark = pytest.mark.skipif(shutil.which(HIPCC) is None, reason="hipcc not available")
 
-EVENTS = {"ds_write": "W", "ds_add": "A", "ds_read": "R", "; wave barrier": "|", "s_barrier": "#"}
+EVENTS = {"ds_write_b16": "w", "ds_write": "W", "ds_add": "A", "ds_read_u16": "r", "ds_read": "R", "; wave barrier": "|",
+          "s_barrier": "#"}
 
 
 @pytest.fixture(scope="module")
@@ -47,3 +48,14 @@ def test_route_backward(lds_events):
     assert len(found) == 21
     for name, seen in found.items():
         assert re.fullmatch(r"W+\|A+\|R+", seen), (name, seen)
+
+
+@pytest.mark.parametrize("kernel,instances", [("sort_place_kernel", 7), ("sort_alone_kernel", 2)])
+def test_sort(lds_events, kernel, instances):
+    """A wave's 16-bit counters: their zeros, and each step's new counts, before the next step reads them.  (A step
+    reads a count and may write it; where the waves' counts are summed eight are read, then eight written.)"""
+    found = lds_events("sort.hip", kernel)
+    assert len(found) == instances
+    for name, seen in found.items():
+        assert seen.startswith("W|"), (name, seen)
+        assert seen.count("rw|") >= 4 and "rwr" not in seen, (name, seen)
