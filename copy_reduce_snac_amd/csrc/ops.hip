@@ -2,6 +2,7 @@
 // sizes and launches of the operators beside the collectives.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <new>
@@ -12,8 +13,17 @@
 
 using namespace snac;
 
+namespace {
+// addresses lo .. hi - 1, those of tensor `i` of a list
+struct Extent {
+  uintptr_t lo, hi;
+  size_t i;
+};
+}  // namespace
+
 struct snac_grads {
   int device;
+  std::vector<Extent> outs, all;  // what the list writes; and reads: neither holds a call's norm
   uint32_t ntiles;
   GradTile* tiles;   // device; then the partial sums, the ticket and the counters
   double* partial;   // kGradMaxBlocks
@@ -111,6 +121,42 @@ snac_status check_router(const snac_router* r, bool forward) {
     return fail(SNAC_E_ARG, "topk %d above the %d experts of the groups that stay", r->topk,
                 r->topk_groups * (r->experts / r->groups));
   return SNAC_OK;
+}
+
+// Extents in ascending order of which no two overlap (then their ends ascend
+// too): the first that ends after `at`.
+std::vector<Extent>::const_iterator first_after(const std::vector<Extent>& v, uintptr_t at) {
+  return std::upper_bound(v.begin(), v.end(), at, [](uintptr_t x, const Extent& e) { return x < e.hi; });
+}
+
+bool holds(const std::vector<Extent>& v, const void* p, uint64_t bytes) {
+  const auto e = first_after(v, (uintptr_t)p);
+  return e != v.end() && e->lo < (uintptr_t)p + bytes;
+}
+
+// An output of a list of tensors may be its own tensor's source and nothing
+// else of the list: it would be clipped twice, or while others read it.  Sorts
+// `outs` by address.
+snac_status check_outs(std::vector<Extent>& outs, const std::vector<Extent>& srcs) {
+  std::sort(outs.begin(), outs.end(), [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+  for (size_t k = 1; k < outs.size(); ++k)
+    if (outs[k].lo < outs[k - 1].hi)
+      return fail(SNAC_E_ARG, "the output of tensor %zu overlaps that of tensor %zu", outs[k].i, outs[k - 1].i);
+  for (const Extent& s : srcs)
+    for (auto o = first_after(outs, s.lo); o != outs.end() && o->lo < s.hi; ++o)
+      if (o->i != s.i) return fail(SNAC_E_ARG, "the output of tensor %zu overlaps src[%zu]", o->i, s.i);
+  return SNAC_OK;
+}
+
+// Overlapping and touching extents as one, in ascending order.
+void merge(std::vector<Extent>& v) {
+  std::sort(v.begin(), v.end(), [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+  size_t n = 0;
+  for (const Extent& e : v) {
+    if (n && e.lo <= v[n - 1].hi) v[n - 1].hi = std::max(v[n - 1].hi, e.hi);
+    else v[n++] = e;
+  }
+  v.resize(n);
 }
 
 // Row strides and counts of a matrix argument.
@@ -458,6 +504,18 @@ snac_status snac_grads_init(const void* const* src, void* const* dst, const size
   snac_grads* g = nullptr;
   char* mem = nullptr;
   try {
+    std::vector<Extent> outs, all;
+    for (size_t i = 0; i < n; ++i) {
+      if (counts[i] == 0) continue;
+      const uintptr_t s = (uintptr_t)src[i], d = dst ? (uintptr_t)dst[i] : s;
+      const uint64_t bytes = counts[i] * esize((snac_dtype)dtypes[i]);
+      all.push_back({s, s + bytes, i});
+      outs.push_back({d, d + bytes, i});
+    }
+    TRY(check_outs(outs, all));
+    all.insert(all.end(), outs.begin(), outs.end());
+    merge(all);
+    merge(outs);
     std::vector<GradTile> tiles;
     tiles.reserve(ntiles);
     for (size_t i = 0; i < n; ++i) {
@@ -477,6 +535,8 @@ snac_status snac_grads_init(const void* const* src, void* const* dst, const size
       }
     }
     g = new snac_grads();
+    g->outs.swap(outs);
+    g->all.swap(all);
     hipError_t e = hipGetDevice(&g->device);
     if (e != hipSuccess) {
       delete g;
@@ -520,10 +580,12 @@ snac_status snac_grads_finalize(snac_grads* grads, snac_stream stream) {
   return e == hipSuccess ? ok() : hip_fail(e, "snac_grads_finalize");
 }
 
-static snac_status check_grads(const snac_grads* g, const float* norm) {
+// `written`: the call writes the norm.
+static snac_status check_grads(const snac_grads* g, const float* norm, bool written) {
   if (!g) return fail(SNAC_E_ARG, "grads is NULL");
   if (!norm) return fail(SNAC_E_ARG, "norm is NULL");
   if ((uintptr_t)norm % 4) return fail(SNAC_E_ARG, "norm not aligned to 4 bytes");
+  if (holds(written ? g->all : g->outs, norm, 4)) return fail(SNAC_E_ARG, "norm overlaps a tensor of the list");
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return fail(SNAC_E_HIP, "hipGetDevice failed");
   if (dev != g->device) return fail(SNAC_E_STATE, "list belongs to device %d, current device is %d", g->device, dev);
@@ -536,21 +598,21 @@ static snac_status check_max_norm(float max_norm) {
 }
 
 snac_status snac_grad_norm(snac_grads* grads, float* norm, snac_stream stream) {
-  TRY(check_grads(grads, norm));
+  TRY(check_grads(grads, norm, true));
   const hipError_t e = launch_grad_norm(grads->tiles, grads->ntiles, grads->partial, grads->ticket, norm, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_grad_norm launch");
 }
 
 snac_status snac_clip_grads(snac_grads* grads, const float* norm, float max_norm, snac_stream stream) {
   TRY(check_max_norm(max_norm));
-  TRY(check_grads(grads, norm));
+  TRY(check_grads(grads, norm, false));
   const hipError_t e = launch_clip(grads->tiles, grads->ntiles, norm, max_norm, grads->pool, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_clip_grads launch");
 }
 
 snac_status snac_clip_grad_norm(snac_grads* grads, float max_norm, float* norm, snac_stream stream) {
   TRY(check_max_norm(max_norm));
-  TRY(check_grads(grads, norm));
+  TRY(check_grads(grads, norm, true));
   const hipError_t e = launch_norm_and_clip(grads->tiles, grads->ntiles, grads->partial, norm, max_norm, grads->pool,
                                             (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_clip_grad_norm launch");

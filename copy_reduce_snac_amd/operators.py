@@ -249,8 +249,9 @@ def embedding_backward(dout, ids, dtable, handle, *, first: int = 0, pad: int | 
 class GradList:
     """A fixed list of gradient tensors (bfloat16 and float32, contiguous, any
     shapes) for the norm and clipping; ``outs`` receives the clipped ones, by
-    default the tensors themselves.  It keeps the tensors alive and reads them
-    where they lie at each call.  ``close()``, or its end of life, waits for the
+    default the tensors themselves.  An output overlaps no other tensor of the
+    list (so none is listed twice in place), and ``norm`` none of them.  It
+    keeps the tensors alive and reads them where they lie at each call.  ``close()``, or its end of life, waits for the
     stream and frees it: not while a graph is captured."""
 
     def __init__(self, grads, outs=None, stream=None):

@@ -197,7 +197,7 @@ typedef struct snac_grads snac_grads;
  * snac_grads_init -- describe n tensors on the current device: src[i] with
  * counts[i] elements of dtypes[i] (snac_dtype values), clipped into dst[i].
  * dst NULL: in place; dst[i] may equal src[i], and may not otherwise overlap
- * any tensor of the list.  Any number of tensors, any length from 0, any
+ * any tensor of the list (SNAC_E_ARG; nor may a call's norm).  Any number of tensors, any length from 0, any
  * element alignment.  The list's own device memory is allocated here, once;
  * the tensors' addresses are kept and their contents are not.  Errors:
  * SNAC_E_ARG, SNAC_E_NOMEM, SNAC_E_HIP.  Not to be captured.

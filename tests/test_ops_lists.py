@@ -1,0 +1,56 @@
+"""Lists of gradient tensors on the CPU: overlapping outputs are refused before
+anything touches a GPU."""
+from __future__ import annotations
+
+import pytest
+
+import copy_reduce_snac_amd as snac
+
+A, B, C, D = 0x100000, 0x200000, 0x300000, 0x400000
+
+
+def status(srcs, dsts, counts, types=None):
+    """SNAC_E_ARG and what it says, or another status (without a GPU a sound list ends at its first HIP call)."""
+    try:
+        h = snac.snac_grads_init(srcs, dsts, counts, types or ["f32"] * len(srcs))
+    except snac.SnacError as e:
+        return e.status, str(e)
+    snac.snac_grads_finalize(h)
+    return 0, ""
+
+
+REFUSED = {
+    "twice in place": ([A, B, A], None, [4, 4, 4]),
+    "views of one buffer in place": ([A, A + 40, A + 60], None, [10, 10, 10]),
+    "one inside another": ([A, A + 16], None, [100, 4]),
+    "other types": ([A, A + 6], None, [2, 4], ["f32", "bf16"]),
+    "one output for two": ([A, B], [C, C], [4, 4]),
+    "outputs over one another": ([A, B], [C + 12, C], [4, 4]),
+    "an output over another source": ([A, B], [B + 12, D], [4, 4]),
+    "an output over another tensor's place": ([A, B], [A, A], [4, 4]),
+    "in place, and another tensor's source": ([A, A], [A, B], [4, 4]),
+    "the last of many": ([A + 64 * i for i in range(300)] + [A + 64 * 150 + 60], None, [16] * 301),
+}
+
+
+@pytest.mark.parametrize("which", REFUSED)
+def test_refused(which):
+    st, says = status(*REFUSED[which])
+    assert st == snac.SNAC_E_ARG and "overlaps" in says, (st, says)
+
+
+TAKEN = {
+    "neighbours": ([A, A + 16, A + 32], None, [4, 4, 4]),
+    "out of order": ([A + 32, A, A + 16], None, [4, 4, 4]),
+    "one source for two outputs": ([A, A], [B, C], [4, 4]),
+    "sources over one another": ([A, A + 8], [B, C], [4, 4]),
+    "some in place": ([A, B], [A, C], [4, 4]),
+    "nothing twice": ([A, A, A], None, [0, 4, 0]),
+}
+
+
+@pytest.mark.parametrize("which", TAKEN)
+def test_not_refused(which):
+    """With nothing but addresses the list is uploaded to a GPU if there is one, and never used."""
+    st, says = status(*TAKEN[which])
+    assert st != snac.SNAC_E_ARG, says
