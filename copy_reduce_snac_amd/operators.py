@@ -246,13 +246,26 @@ def embedding_backward(dout, ids, dtable, handle, *, first: int = 0, pad: int | 
                             int(accumulate), _stream(stream, on))
 
 
+# Lists that ended without close().  The collector may end one at any time, also
+# while a graph is captured, where waiting for a stream or freeing memory would
+# end the capture: they are freed at the next call that allows both.
+_ended: list[int] = []
+
+
+def _free_ended(stream) -> None:
+    while _ended:
+        snac_grads_finalize(_ended.pop(), stream)
+
+
 class GradList:
     """A fixed list of gradient tensors (bfloat16 and float32, contiguous, any
     shapes) for the norm and clipping; ``outs`` receives the clipped ones, by
     default the tensors themselves.  An output overlaps no other tensor of the
     list (so none is listed twice in place), and ``norm`` none of them.  It
-    keeps the tensors alive and reads them where they lie at each call.  ``close()``, or its end of life, waits for the
-    stream and frees it: not while a graph is captured."""
+    keeps the tensors alive and reads them where they lie at each call.
+    ``close()`` waits for the stream and frees it.  Making and closing lists is
+    not to be captured; a list that ends without ``close()`` is freed when the
+    next one is made or closed, so it may end at any time."""
 
     def __init__(self, grads, outs=None, stream=None):
         self._h = None
@@ -270,8 +283,9 @@ class GradList:
             _pair(g, o, "GradList: a tensor and its output")
             if g.numel() != o.numel():
                 raise ValueError("GradList: a tensor and its output differ in length")
-        self._h = snac_grads_init(self.grads, self.outs, [t.numel() for t in self.grads], types,
-                                  _stream(stream, self.device))
+        on = _stream(stream, self.device)
+        _free_ended(on)
+        self._h = snac_grads_init(self.grads, self.outs, [t.numel() for t in self.grads], types, on)
 
     @property
     def handle(self):
@@ -280,15 +294,16 @@ class GradList:
         return self._h
 
     def close(self, stream=None) -> None:
+        on = _stream(stream, self.device)
         h, self._h = self._h, None
         if h is not None:
-            snac_grads_finalize(h, _stream(stream, self.device))
+            snac_grads_finalize(h, on)
+        _free_ended(on)
 
     def __del__(self):
-        try:
-            self.close()
-        except Exception:  # the interpreter or the device is going away
-            pass
+        h = getattr(self, "_h", None)
+        if h is not None:
+            _ended.append(h)
 
 
 def _scalar(norm, what: str) -> int:

@@ -49,3 +49,38 @@ def test_one_source_for_two_outputs():
     want = (9000 * 9.0) ** 0.5
     assert abs(float(norm) - want) <= 1.01 * U * want
     assert not bool(outs[0].any()) and not bool(outs[1].any())
+
+
+def test_a_list_ends_during_a_capture():
+    """The collector ends a list while a graph is captured: the capture goes on and the graph is right."""
+    import gc
+
+    import torch
+
+    from copy_reduce_snac_amd import operators as ops
+
+    x = torch.empty(3000, device="cuda")
+    out, norm = torch.empty_like(x), torch.empty(1, device="cuda")
+    kept, other = ops.GradList([x], [out]), ops.GradList([torch.ones(50, device="cuda")])
+    other.itself = other
+    x.fill_(1.0)
+    ops.clip_grad_norm(kept, 1.0, norm)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.grad_norm(kept, norm)
+        del other
+        gc.collect()
+        ops.clip_grad_norm(kept, 1.0, norm)
+    for value in (2.0, 7.0, 0.5, 2.0):
+        x.fill_(value)
+        out.zero_()
+        torch.randn(1000, device="cuda").sum().item()
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        ops.clip_grad_norm(kept, 1.0, norm)
+        assert torch.equal(got, out) and bool((out > 0).all())
+    ops.GradList([x]).close()  # frees the one that ended
+    assert ops._ended == []
+    kept.close()

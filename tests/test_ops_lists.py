@@ -1,5 +1,5 @@
 """Lists of gradient tensors on the CPU: overlapping outputs are refused before
-anything touches a GPU."""
+anything touches a GPU, and a list's end frees nothing by itself."""
 from __future__ import annotations
 
 import pytest
@@ -54,3 +54,36 @@ def test_not_refused(which):
     """With nothing but addresses the list is uploaded to a GPU if there is one, and never used."""
     st, says = status(*TAKEN[which])
     assert st != snac.SNAC_E_ARG, says
+
+
+def test_the_end_of_a_list_touches_no_device(monkeypatch):
+    """The collector may end a list while a graph is captured: it is freed when another is made or closed."""
+    import gc
+
+    import torch
+
+    from copy_reduce_snac_amd import operators as ops
+
+    made, freed = iter(range(1, 9)), []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(ops, "_raw_stream", lambda device: 77)
+    monkeypatch.setattr(ops, "snac_grads_init", lambda *a: next(made))
+    monkeypatch.setattr(ops, "snac_grads_finalize", lambda h, stream: freed.append((h, stream)))
+    one, two = ops.GradList([]), ops.GradList([])
+    one.itself = one  # only the collector finds it
+    del one
+    gc.collect()
+    del two
+    assert freed == []
+    three, four = ops.GradList([]), ops.GradList([])
+    assert sorted(freed) == [(1, 77), (2, 77)]
+    del three
+    assert len(freed) == 2
+    four.close(stream=5)
+    assert sorted(freed[2:]) == [(3, 5), (4, 5)]
+    four.close()
+    del four
+    with pytest.raises(ValueError):
+        ops.GradList([torch.zeros(4).t() for _ in range(1)], [])  # not made at all
+    gc.collect()
+    assert len(freed) == 4
