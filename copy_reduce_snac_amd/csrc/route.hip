@@ -46,6 +46,27 @@ __device__ __forceinline__ double from_lane(double x, uint32_t l) {
   return __longlong_as_double((long long)from_lane((uint64_t)__double_as_longlong(x), l));
 }
 
+// 1 / x for a normal binary64 x, off by a few of its last bits: the
+// hardware's estimate (2^-24 or better) and one step of Newton's iteration.
+__device__ __forceinline__ double reciprocal(double x) {
+  const double r = __builtin_amdgcn_rcp(x);
+  return r * __builtin_fma(-x, r, 2.0);
+}
+
+// A chosen expert's share of `total`, scaled.  Scores are binary32, sums and
+// quotients of them binary64, so that a weight is off by its own exponential
+// and one rounding.  32768 x 256: 15.5 us (15.4 with binary32 throughout, whose
+// weights are off by half as much again), softmax 20.5 (19.8).
+__device__ __forceinline__ float share(float score, double total, float scale) {
+  return (float)((double)score * (double)scale * reciprocal(total));
+}
+
+// scale * sigmoid(x)
+__device__ __forceinline__ float scaled_sigmoid(float x, float scale) {
+  const float a = expf(-fabsf(x));
+  return share(x < 0.0f ? a : 1.0f, 1.0 + (double)a, scale);
+}
+
 template <typename T>
 __device__ __forceinline__ float load_logit(const char* row, uint32_t e) {
   return load_elem<T>(row + (uint64_t)e * T::kSize);
@@ -169,27 +190,18 @@ __device__ void route_exact(const RouteArgs& a, uint64_t t) {
   if (softmax) {
     const float m = a.r.renorm ? wave_max(my_x) : top;
     const float p = have ? expf(my_x - m) : 0.0f;
-    float total;
-    if (a.r.renorm) {
-      total = wave_sum(p);
-    } else {
-      total = 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : expf(x[j] - m);
-      total = wave_sum(total);
-    }
-    w = poison ? __builtin_nanf("") : p / total;
+    w = poison ? __builtin_nanf("") : share(p, a.r.renorm ? wave_sum((double)p) : sum, a.r.scale);
   } else if (a.r.renorm) {
     // s_i / sum s_j with both sides times exp(-m), m the largest chosen
     // logit where that is negative: nothing underflows
     const float m = fminf(wave_max(my_x), 0.0f);
     const float p = !have ? 0.0f : m < 0.0f ? expf(my_x - m) / (1.0f + expf(my_x)) : 1.0f / (1.0f + expf(-my_x));
-    w = p / wave_sum(p);
+    w = share(p, wave_sum((double)p), a.r.scale);
   } else {
-    w = 1.0f / (1.0f + expf(-my_x));
+    w = scaled_sigmoid(my_x, a.r.scale);
   }
   if (lane < K) {
-    a.weights[t * K + lane] = have ? w * a.r.scale : 0.0f;
+    a.weights[t * K + lane] = have ? w : 0.0f;
     a.ids[t * K + lane] = my_id;
   }
 }
@@ -282,7 +294,7 @@ enum : int { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 //     different logits are in doubt.
 //   else: the distance in fixed point over S = 2 max(|best|, largest score).
 //     A binary32 score with its bias is off by less than 3.5 S 2^-24 (sigmoid)
-//     or 16 S 2^-24 (softmax: 24 additions in the sum), the subtraction and the
+//     or 16 S 2^-24 (softmax: its exponent is a rounded product), the subtraction and the
 //     scaling by at most S 2^-24 each, cutting by one step: two keys by 12 or
 //     37 steps at QB = 24.
 template <typename T, int L, int V, int KB, int KEY>
@@ -354,7 +366,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
     const double s = softmax ? exp((double)x - (double)top) / sum64 : 1.0 / (1.0 + exp(-(double)x));
     return by_logit ? s : s + (double)b;
   };
-  float total = 0.0f;  // softmax: sum of exp(x - top)
+  double total = 0.0;  // softmax: sum of exp(x - top)
   if (softmax && !(by_logit && a.r.renorm)) {
 #pragma unroll
     for (int j = 0; j < V; ++j) total += x[j] == -inf ? 0.0f : __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
@@ -371,7 +383,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
   } else {
     float v[V];
     float best = -inf;
-    const float inv = 1.0f / total;
+    const float inv = 1.0f / (float)total;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float s = softmax ? __builtin_amdgcn_exp2f((x[j] - top) * kLog2e) * inv
@@ -533,17 +545,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
   if (softmax) {
     const float m = a.r.renorm ? lanes_max<L>(sx) : top;
     const float p = have ? expf(cx - m) : 0.0f;
-    w = p / (a.r.renorm ? lanes_sum<L>(p) : total);
+    w = share(p, a.r.renorm ? lanes_sum<L>((double)p) : total, a.r.scale);
   } else if (a.r.renorm) {
     const float m = fminf(lanes_max<L>(sx), 0.0f);
     const float p = !have ? 0.0f : m < 0.0f ? expf(cx - m) / (1.0f + expf(cx)) : 1.0f / (1.0f + expf(-cx));
-    w = p / lanes_sum<L>(p);
+    w = share(p, lanes_sum<L>((double)p), a.r.scale);
   } else {
-    w = 1.0f / (1.0f + expf(-cx));
+    w = scaled_sigmoid(cx, a.r.scale);
   }
   const uint64_t sub_lanes = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (sub * L % 64);
   if (l < K && live && !(again & sub_lanes)) {
-    a.weights[t * K + l] = have ? w * a.r.scale : 0.0f;
+    a.weights[t * K + l] = have ? w : 0.0f;
     a.ids[t * K + l] = have ? c.id : -1;
   }
   for (uint32_t s = 0; s < TPW; ++s)
@@ -556,7 +568,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
 // memory (32768 x 128 f32: 8.5 us; with a lane's 8 logits side by side, in two
 // units of every other 16 bytes, 10.1; 32 lanes of 4 logits 9.3).  The chosen
 // experts' terms come to their lanes by way of LDS: lane k < topk works choice
-// k out and adds it to the row's slot.  Bound by HBM: the row is read once (not
+// k out and adds it to the row's slot.  Sums over the row and quotients are
+// binary64, the exponentials binary32.  Bound by HBM: the row is read once (not
 // at all where only the chosen logits matter) and written once.
 template <typename T, int L, int V, bool UNITS>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const RouteBackwardArgs a) {
@@ -612,28 +625,38 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
 #pragma unroll
   for (int j = 0; j < V; ++j) row_up[at(j)] = 0.0f;
   float g[C];  // what goes to the chosen slots
-  float inv = 0.0f, dot = 0.0f, top = -inf;
+  double inv = 0.0, dot = 0.0;
+  float top = -inf;
   if (softmax && !renorm) {
 #pragma unroll
     for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
     top = lanes_max<L>(top);
-    float total = 0.0f;
+    double total = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       x[j] = x[j] == -inf ? 0.0f : __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
       total += x[j];
     }
     total = lanes_sum<L>(total);
-    inv = total == 0.0f ? 0.0f : 1.0f / total;  // 0: every logit masked
+    inv = total == 0.0 ? 0.0 : reciprocal(total);  // 0: every logit masked
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float r = !have[c] || cx[c] == -inf ? 0.0f : expf(cx[c] - top) * inv;
-      dot += have[c] ? r * dw[c] : 0.0f;
-      g[c] = dw[c];
+      const double r = !have[c] || cx[c] == -inf ? 0.0 : expf(cx[c] - top) * inv;
+      dot += have[c] ? r * dw[c] : 0.0;
     }
     dot = lanes_sum<L>(dot);
+    // dw - dot is made in binary64: for a score near 1 hardly anything is left
+    // of dw.  f32: with the product, below.  bf16: here, where a lane has one or
+    // two of them (512 experts 14.3 us; below 15.4, all in binary32 13.4); a slot
+    // of 0 is then one that was not chosen, so what is chosen is not 0.
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float up = (float)(dw[c] - dot);
+      g[c] = T::kSize == 4 ? dw[c] : fabsf(up) < 0x1p-126f ? 0x1p-126f : up;
+    }
   } else {
-    float m = cx[0], r[C], total = 0.0f;
+    float m = cx[0], r[C];
+    double total = 0.0, part[C];
     if constexpr (C == 2) m = fmaxf(m, cx[1]);
     if (renorm) m = lanes_max<L>(m);
     if (!softmax) m = fminf(m, 0.0f);
@@ -647,17 +670,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
       if (!softmax && renorm && m < 0.0f) r[c] *= g[c];
       total += r[c];
     }
-    if (renorm) {
-      total = lanes_sum<L>(total);
+    if (renorm) total = lanes_sum<L>(total);
+    inv = !renorm ? 1.0 : total == 0.0 ? 0.0 : reciprocal(total);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        r[c] = total == 0.0f ? 0.0f : r[c] / total;
-        dot += have[c] ? r[c] * dw[c] : 0.0f;
-      }
-      dot = lanes_sum<L>(dot);
+    for (int c = 0; c < C; ++c) {
+      part[c] = r[c] * inv;
+      dot += have[c] ? part[c] * dw[c] : 0.0;
     }
+    dot = renorm ? lanes_sum<L>(dot) : 0.0;
 #pragma unroll
-    for (int c = 0; c < C; ++c) g[c] = r[c] * g[c] * (dw[c] - dot);
+    for (int c = 0; c < C; ++c) g[c] = (float)(part[c] * g[c] * (dw[c] - dot));
   }
   // zeros, then the other lanes' terms, then this lane's slots
   wave_lds_order();
@@ -670,7 +692,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
   for (int j = 0; j < V; ++j) d[j] = row_up[at(j)];
   if (softmax && !renorm) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = x[j] * inv * (d[j] - dot);
+    for (int j = 0; j < V; ++j) {
+      if constexpr (T::kSize == 4) d[j] = (float)(x[j] * __builtin_fma((double)d[j], inv, -inv * dot));
+      else d[j] = x[j] * (float)inv * (d[j] == 0.0f ? (float)-dot : d[j]);
+    }
   }
   if (!live) return;
   char* p = static_cast<char*>(a.dlogits) + t * a.ld_d * T::kSize;

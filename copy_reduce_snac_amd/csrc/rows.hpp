@@ -196,6 +196,35 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
+// x + the x of the lane's partner at distance D
+template <int D>
+__device__ __forceinline__ double exchange_sum(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32), lo2 = lo, hi2 = hi;
+  if constexpr (D <= 8) {
+    constexpr int C = D == 1 ? kDppXor1 : D == 2 ? kDppXor2 : D == 4 ? kDppHalfMirror : kDppMirror;
+    lo2 = dpp<C>(lo), hi2 = dpp<C>(hi);
+  } else if constexpr (D == 16) {
+    const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    lo = l[0], lo2 = l[1], hi = h[0], hi2 = h[1];
+  } else {
+    const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    lo = l[0], lo2 = l[1], hi = h[0], hi2 = h[1];
+  }
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo)) + __longlong_as_double((long long)((uint64_t)hi2 << 32 | lo2));
+}
+template <int L>
+__device__ __forceinline__ double lanes_sum(double x) {
+  x = exchange_sum<1>(x);
+  x = exchange_sum<2>(x);
+  x = exchange_sum<4>(x);
+  x = exchange_sum<8>(x);
+  if constexpr (L >= 32) x = exchange_sum<16>(x);
+  if constexpr (L >= 64) x = exchange_sum<32>(x);
+  return x;
+}
 // the largest of the values that are not NaN
 template <int L>
 __device__ __forceinline__ float lanes_max(float x) {
