@@ -60,10 +60,12 @@ bool overlap(const Span& a, const Span& b) {
   if (empty(a) || empty(b)) return false;
   const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
   if (!(pa < pb + (uint64_t)extent(b) && pb < pa + (uint64_t)extent(a))) return false;
-  // columns of one wider matrix: the rows interleave without touching
-  if (a.rows > 1 && b.rows > 1 && a.ld == b.ld) {
-    const uint64_t d = pa < pb ? (pb - pa) % a.ld : (a.ld - (pa - pb) % a.ld) % a.ld;
-    if (d >= a.width && d + b.width <= a.ld) return false;
+  // columns of one wider matrix: the rows interleave without touching (a single
+  // row lies in the other's matrix, whatever its own stride)
+  const uint64_t ld = a.rows > 1 ? a.ld : b.ld;
+  if (b.rows == 1 || b.ld == ld) {
+    const uint64_t d = pa < pb ? (pb - pa) % ld : (ld - (pa - pb) % ld) % ld;
+    if (d >= a.width && d + b.width <= ld) return false;
   }
   return true;
 }
