@@ -300,10 +300,10 @@ class GradList:
             snac_grads_finalize(h, on)
         _free_ended(on)
 
-    def __del__(self):
+    def __del__(self, ended=_ended):  # bound here: the module's names go before its last lists do
         h = getattr(self, "_h", None)
         if h is not None:
-            _ended.append(h)
+            ended.append(h)
 
 
 def _scalar(norm, what: str) -> int:

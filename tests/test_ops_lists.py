@@ -87,3 +87,25 @@ def test_the_end_of_a_list_touches_no_device(monkeypatch):
         ops.GradList([torch.zeros(4).t() for _ in range(1)], [])  # not made at all
     gc.collect()
     assert len(freed) == 4
+
+
+def test_lists_left_at_the_end_of_the_program():
+    """Lists that live until the interpreter ends, when the module's names are gone already, end without a word."""
+    import os
+    import subprocess
+    import sys
+
+    program = """
+import torch
+from copy_reduce_snac_amd import operators as ops
+torch.cuda.current_device = lambda: 0
+ops._raw_stream = lambda device: 0
+ops.snac_grads_init = lambda *a: 1
+one, two = ops.GradList([]), ops.GradList([])
+one.other, two.other = two, one
+import sys
+sys.modules["torch"].kept = ops.GradList([])
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=120)
+    assert p.returncode == 0 and p.stderr == "", p.stderr
