@@ -121,8 +121,9 @@ __device__ __forceinline__ void put_unit(const EmbedGradArgs& a, uint32_t key, u
 // rows' part of the sorted keys and marks those that it meets.  Small groups
 // keep what is written at a time close together; the search, of kProbes keys
 // a step, must not read more lines than they write.  us, 16384 tokens into
-// 131072 x 4096 f32: groups of 12 / 16 / 32 KiB 628 / 369 / 426, of 16 rows
-// 418; 8 / 16 / 32 / 48 / 256 keys a step 418 / 392 / 369 / 367 / 447.
+// 131072 x 4096 f32: with 32 keys a step, groups of 12 / 16 / 32 KiB 628 / 369 /
+// 426, of 16 rows 418; with groups of 16 KiB, 8 / 16 / 32 / 48 / 256 keys a step
+// 418 / 392 / 369 / 367 / 447.
 constexpr uint32_t kZeroRows = 16;  // at most
 constexpr uint32_t kZeroBytes = 16384;
 constexpr uint32_t kProbes = 48;

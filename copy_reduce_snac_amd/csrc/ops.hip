@@ -185,11 +185,17 @@ snac_status check_topk(int topk) {
 constexpr uint32_t kDigitBits = 10;
 // Zeros written beside a counting and a placing launch, and by a workgroup.
 // They go to every row, also to those that get a sum later, so only where
-// there are fewer tokens than rows.  us, with these / half / a quarter of them:
-// 32768 tokens, 65536 x 2048 f32: 139 / 143 / 145 (none: 150); 4096 tokens,
-// 32768 x 4096 bf16: 60 / 68 / 71; 32768 tokens, 8192 x 2048 f32: 75 / 75 / 73.
-// Groups of 16 / 32 / 64 KiB: the first 135 / 136 / 136.4 by now, the second
-// 56.6 / 56.1 / 56.2, 8192 tokens into 16384 x 2048 f32 45.9 / 46.5 / 47.2.
+// there are fewer tokens than rows: how many of these are different is not known
+// before the sort.  us, with them / without:
+//   32768 x 2048 f32   4096 different tokens 57.4 / 67.9; 16384 88.9 / 96.7;
+//                      32440 126.1 / 126.5
+//   65536 x 2048 f32   32768 tokens, 10399 different 133 / 145; 64880 different
+//                      243 / 248
+//   32768 x 4096 bf16  4096 different 59.0 / 70.0; 24576 120 / 123; 32440 142 /
+//                      138, the only one of 77 cases that they cost anything
+// As many tokens as rows and more: 32768 into 8192 x 2048 f32 75 us with these,
+// 73 with a quarter of them.  Groups of 16 / 32 / 64 KiB: 32768 tokens into
+// 65536 x 2048 f32 135 / 136 / 136.4, 8192 into 16384 x 2048 45.9 / 46.5 / 47.2.
 constexpr uint64_t kHistZeroBytes = 40ull << 20, kPlaceZeroBytes = 80ull << 20, kZeroGroupBytes = 16ull << 10;
 uint32_t key_bits(uint64_t vocab) { return 64u - (uint32_t)__builtin_clzll(vocab); }
 uint32_t key_passes(uint64_t vocab) { return (key_bits(vocab) + kDigitBits - 1) / kDigitBits; }

@@ -273,7 +273,7 @@ enum : int { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 // experts begins at a lane of its own and has 1 << ps lanes).
 //
 // Choosing is bound by instructions, not by memory: 32768 tokens of 256 f32
-// logits, 8 of them from 4 of 8 groups, take 15.2 us, 860 vector instructions
+// logits, 8 of them from 4 of 8 groups, take 15.4 us, 863 vector instructions
 // (32 of them transcendental) a wave of 4 tokens, 12.7 us of issue; the same
 // logits are read in 5.4 us.  (All keys in binary64, by a wave a token: 147.)
 // So a key is one 32-bit number: the score's distance from the row's best, QB
@@ -565,8 +565,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a,
 // The gradient, L lanes a token, V logits a lane.  UNITS: in 16-byte units,
 // unit u of lane l being the row's unit u L + l, for rows of whole units; else
 // by elements, j L + l.  Either way neighbouring lanes touch neighbouring
-// memory (32768 x 128 f32: 8.5 us; with a lane's 8 logits side by side, in two
-// units of every other 16 bytes, 10.1; 32 lanes of 4 logits 9.3).  The chosen
+// memory (32768 x 128 f32: 7.7 us a call among others, the kernel 7.8 to 8.6;
+// when that was 8.5, a lane's 8 logits side by side, in two units of every other
+// 16 bytes, took 10.1, and 32 lanes of 4 logits 9.3).  The chosen
 // experts' terms come to their lanes by way of LDS: lane k < topk works choice
 // k out and adds it to the row's slot.  Sums over the row and quotients are
 // binary64, the exponentials binary32.  Bound by HBM: the row is read once (not

@@ -262,7 +262,9 @@ class GradList:
     shapes) for the norm and clipping; ``outs`` receives the clipped ones, by
     default the tensors themselves.  An output overlaps no other tensor of the
     list (so none is listed twice in place), and ``norm`` none of them.  It
-    keeps the tensors alive and reads them where they lie at each call.
+    keeps the tensors alive and reads them where they lie at each call, so it
+    is for gradients that stay in place (``zero_grad(set_to_none=False)``, or
+    buckets): making one takes 0.15 to 0.6 ms and waits for the stream.
     ``close()`` waits for the stream and frees it.  Making and closing lists is
     not to be captured; a list that ends without ``close()`` is freed when the
     next one is made or closed, so it may end at any time."""

@@ -199,7 +199,11 @@ typedef struct snac_grads snac_grads;
  * dst NULL: in place; dst[i] may equal src[i], and may not otherwise overlap
  * any tensor of the list (SNAC_E_ARG; nor may a call's norm).  Any number of tensors, any length from 0, any
  * element alignment.  The list's own device memory is allocated here, once;
- * the tensors' addresses are kept and their contents are not.  Errors:
+ * the tensors' addresses are kept and their contents are not.  Making a list
+ * uploads its tiles and waits for `stream`: 0.15 ms for 96 tensors of 1 M
+ * elements in all, 0.55 ms for 300 of 0.5 G, so a list is for tensors that stay
+ * where they are from step to step (gradients that a program keeps and zeroes,
+ * or writes in place), not for ones that are allocated anew each time.  Errors:
  * SNAC_E_ARG, SNAC_E_NOMEM, SNAC_E_HIP.  Not to be captured.
  */
 snac_status snac_grads_init(const void* const* src, void* const* dst, const size_t* counts, const int32_t* dtypes,
