@@ -74,8 +74,9 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const CombineArgs 
 }
 
 // One wave a slot: its rows of dout (read again by the token's other slots,
-// from L2) and of y once through, the dot product in binary32 per lane and
-// then over the lanes.
+// from L2) and of y once through.  The dot product is binary32 within a 16-byte
+// unit and binary64 from there on, so that its error does not grow with the
+// width.
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const CombineBackwardArgs a, uint64_t slots) {
   constexpr uint32_t N = kUnit<T>;
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const Com
     const char* g = a.dout + t * a.ld_dout;
     const char* y = a.y + (uint64_t)row * a.ld_y;
     char* dy = a.dy + (uint64_t)row * a.ld_dy;
-    float dot = 0.0f;
+    double dot = 0.0;
     for (uint32_t e = 0; e < a.width; e += kPieceElems<T, kPieceUnits>) {
       const uint64_t off = (uint64_t)e * T::kSize;
       u32x4 vg[kPieceUnits], vy[kPieceUnits];
@@ -102,17 +103,19 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const Com
         float fg[N], fy[N];
         unpack<T>(vg[j], fg);
         unpack<T>(vy[j], fy);
+        float part = 0.0f;
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c) {
-          dot = __builtin_fmaf(fg[c], fy[c], dot);
+          part = __builtin_fmaf(fg[c], fy[c], part);
           fg[c] = w * fg[c];
         }
+        dot += part;
         vg[j] = pack<T>(fg);
       }
       st_piece<T, kPieceUnits, true>(dy + off, a.width - e, vg);
     }
     dot = wave_sum(dot);
-    if (lane == 0) a.dweights[s] = dot;
+    if (lane == 0) a.dweights[s] = (float)dot;
   }
 }
 

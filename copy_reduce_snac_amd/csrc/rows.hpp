@@ -239,11 +239,7 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 
 __device__ __forceinline__ float wave_sum(float x) { return lanes_sum<64>(x); }
 __device__ __forceinline__ float wave_max(float x) { return lanes_max<64>(x); }
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) x = x + __shfl_xor(x, m);
-  return x;
-}
+__device__ __forceinline__ double wave_sum(double x) { return lanes_sum<64>(x); }
 
 // Zeros to `rows` rows of `width` elements from `p` on, but those that `skip`
 // names, by the whole workgroup: a wave a piece, in the order of the addresses.

@@ -142,7 +142,8 @@ snac_status snac_combine(const void* y, size_t ld_y, size_t rows, const int32_t*
  * snac_combine_backward -- from dout[tokens][width]:
  *   dy[row_of_slot[t][k]] = weights[t][k] * dout[t]   (other rows are left)
  *   dweights[t][k] = <dout[t], y[row_of_slot[t][k]]>  (0 for a dropped slot)
- * products and sums in binary32.  dy may be y itself (same ld).
+ * the products dy in binary32; the sums in binary32 within 16 bytes of a row,
+ * in binary64 over them, rounded once.  dy may be y itself (same ld).
  */
 snac_status snac_combine_backward(const void* dout, size_t ld_dout, const void* y, size_t ld_y, size_t rows,
                                   const int32_t* row_of_slot, const float* weights, size_t tokens, int topk,
