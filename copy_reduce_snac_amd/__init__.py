@@ -127,6 +127,18 @@ class snac_router(ctypes.Structure):
     ]
 
 
+class snac_teacher(ctypes.Structure):
+    _fields_ = [
+        ("ids", ctypes.c_void_p),
+        ("logits", ctypes.c_void_p),
+        ("vocab", ctypes.c_int64),
+        ("id_bytes", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("temperature", ctypes.c_float),
+    ]
+
+
 _lib = None
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
@@ -181,6 +193,16 @@ _SIGS = {
     "snac_grad_norm": (_I, [_VP, _VP, _VP]),
     "snac_clip_grads": (_I, [_VP, _VP, _F, _VP]),
     "snac_clip_grad_norm": (_I, [_VP, _F, _VP, _VP]),
+    "snac_layer_norm": (_I, [_VP, _SZ, _VP, _VP, _I, _SZ, _SZ, _F, _I, _VP, _SZ, _VP, _VP]),
+    "snac_layer_norm_scratch": (_SZ, [_SZ, _SZ, _I]),
+    "snac_layer_norm_backward": (_I, [_VP, _VP, _SZ, _VP, _SZ, _VP, _I, _VP, _SZ, _SZ, _I, _VP, _SZ, _VP, _VP, _I, _I, _VP]),
+    "snac_balance_load": (_I, [_VP, ctypes.POINTER(snac_router), _VP, _SZ, _VP, _SZ, _I, _VP, _VP]),
+    "snac_balance_loss": (_I, [_VP, _I, _F, _VP, _VP]),
+    "snac_balance_backward": (_I, [ctypes.POINTER(snac_router), _VP, _SZ, _VP, _VP, _F, _VP, _SZ, _I, _VP, _SZ, _I, _VP]),
+    "snac_distill": (_I, [ctypes.POINTER(snac_teacher), _VP, _SZ, _SZ, _I, _VP, _VP, _VP]),
+    "snac_distill_shard": (_I, [ctypes.POINTER(snac_teacher), _VP, _SZ, _I64, _SZ, _SZ, _I, _VP, _VP]),
+    "snac_distill_join": (_I, [ctypes.POINTER(snac_teacher), _VP, _I, _SZ, _VP, _VP, _VP]),
+    "snac_distill_backward": (_I, [ctypes.POINTER(snac_teacher), _VP, _SZ, _I64, _SZ, _VP, _VP, _F, _SZ, _I, _VP, _SZ, _VP]),
 }
 
 
@@ -581,3 +603,67 @@ def snac_clip_grads(grads, norm, max_norm: float, stream=None) -> None:
 
 def snac_clip_grad_norm(grads, max_norm: float, norm, stream=None) -> None:
     _check(lib().snac_clip_grad_norm(grads, max_norm, _ptr(norm), _stream(stream)), "snac_clip_grad_norm")
+
+
+def snac_layer_norm(x, ld_x: int, weight, bias, param_dtype, tokens: int, width: int, eps: float, dtype, out, ld_out: int,
+                    stats=None, stream=None) -> None:
+    _check(lib().snac_layer_norm(_ptr(x), ld_x, _ptr(weight), _ptr(bias), _dtype(param_dtype), tokens, width, eps,
+                                 _dtype(dtype), _ptr(out), ld_out, _ptr(stats), _stream(stream)), "snac_layer_norm")
+
+
+def snac_layer_norm_scratch(tokens: int, width: int, dtype) -> int:
+    return lib().snac_layer_norm_scratch(tokens, width, _dtype(dtype))
+
+
+def snac_layer_norm_backward(ctx, dout, ld_dout: int, x, ld_x: int, weight, param_dtype, stats, tokens: int, width: int,
+                             dtype, dx, ld_dx: int, dweight, dbias, grad_dtype, accumulate: int = 0, stream=None) -> None:
+    _check(lib().snac_layer_norm_backward(ctx, _ptr(dout), ld_dout, _ptr(x), ld_x, _ptr(weight), _dtype(param_dtype),
+                                          _ptr(stats), tokens, width, _dtype(dtype), _ptr(dx), ld_dx, _ptr(dweight),
+                                          _ptr(dbias), _dtype(grad_dtype), accumulate, _stream(stream)),
+           "snac_layer_norm_backward")
+
+
+def snac_balance_load(ctx, r: snac_router, logits, ld: int, ids, tokens: int, dtype, load, stream=None) -> None:
+    _check(lib().snac_balance_load(ctx, r, _ptr(logits), ld, _ptr(ids), tokens, _dtype(dtype), _ptr(load),
+                                   _stream(stream)), "snac_balance_load")
+
+
+def snac_balance_loss(load, experts: int, coefficient: float, loss, stream=None) -> None:
+    _check(lib().snac_balance_loss(_ptr(load), experts, coefficient, _ptr(loss), _stream(stream)), "snac_balance_loss")
+
+
+def snac_balance_backward(r: snac_router, logits, ld: int, ids, load, coefficient: float, dloss, tokens: int, dtype,
+                          dlogits, ld_d: int, accumulate: int = 0, stream=None) -> None:
+    _check(lib().snac_balance_backward(r, _ptr(logits), ld, _ptr(ids), _ptr(load), coefficient, _ptr(dloss), tokens,
+                                       _dtype(dtype), _ptr(dlogits), ld_d, accumulate, _stream(stream)),
+           "snac_balance_backward")
+
+
+SNAC_MAX_TEACHER = 256
+
+
+def teacher(ids, id_bytes: int, logits, dtype, topk: int, vocab: int, temperature: float = 1.0) -> snac_teacher:
+    """A snac_teacher; it holds the addresses of ``ids`` and ``logits``, which the caller keeps alive."""
+    return snac_teacher(_ptr(ids), _ptr(logits), vocab, id_bytes, _dtype(dtype), topk, temperature)
+
+
+def snac_distill(t: snac_teacher, logits, ld: int, tokens: int, dtype, loss, stats, stream=None) -> None:
+    _check(lib().snac_distill(t, _ptr(logits), ld, tokens, _dtype(dtype), _ptr(loss), _ptr(stats), _stream(stream)),
+           "snac_distill")
+
+
+def snac_distill_shard(t: snac_teacher, logits, ld: int, first: int, width: int, tokens: int, dtype, part,
+                       stream=None) -> None:
+    _check(lib().snac_distill_shard(t, _ptr(logits), ld, first, width, tokens, _dtype(dtype), _ptr(part),
+                                    _stream(stream)), "snac_distill_shard")
+
+
+def snac_distill_join(t: snac_teacher, parts, shards: int, tokens: int, loss, stats, stream=None) -> None:
+    _check(lib().snac_distill_join(t, _ptr(parts), shards, tokens, _ptr(loss), _ptr(stats), _stream(stream)),
+           "snac_distill_join")
+
+
+def snac_distill_backward(t: snac_teacher, logits, ld: int, first: int, width: int, stats, dloss, scale: float,
+                          tokens: int, dtype, dlogits, ld_d: int, stream=None) -> None:
+    _check(lib().snac_distill_backward(t, _ptr(logits), ld, first, width, _ptr(stats), _ptr(dloss), scale, tokens,
+                                       _dtype(dtype), _ptr(dlogits), ld_d, _stream(stream)), "snac_distill_backward")

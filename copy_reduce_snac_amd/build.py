@@ -31,7 +31,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsnac.so")
 SOURCES = ["api.hip", "collectives.hip", "pipeline.hip", "probes.hip", "noalloc.hip",
-           "ops.hip", "route.hip", "sort.hip", "dispatch.hip", "embedding.hip", "grads.hip"]
+           "ops.hip", "route.hip", "sort.hip", "dispatch.hip", "embedding.hip", "grads.hip",
+           "ops_step.hip", "layernorm.hip", "balance.hip", "distill.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,345 @@
+// distill.hip -- the divergence from a teacher's top logits, over the whole
+// vocabulary or a shard of it, and its gradient (snac_distill and its kin in
+// include/snac_ops.h).
+#include <hip/hip_runtime.h>
+
+#include "ops.hpp"
+#include "rows.hpp"
+
+namespace snac {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kChoices = SNAC_MAX_TEACHER / 64;  // of a lane
+constexpr double kLog2e = 1.4426950408889634;
+
+// A token's choices, choice c * 64 + lane in slot c of a lane: their columns
+// (-1: not valid), the teacher's logits, and after weigh() their q.
+struct Choices {
+  int64_t id[kChoices];
+  float t[kChoices], q[kChoices];
+  float top;     // the largest valid logit
+  double total;  // sum of exp((t - top) / temperature)
+  bool any;      // a valid choice: the token has a part
+
+  __device__ __forceinline__ void load(const snac_teacher& a, uint64_t token) {
+    const uint32_t lane = threadIdx.x & 63u;
+    const float inf = __builtin_inff();
+    const uint64_t at = token * (uint32_t)a.topk;
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) {
+      const uint32_t k = c * 64 + lane;
+      id[c] = -1;
+      t[c] = -inf;
+      if (c * 64 >= a.topk) continue;
+      if (k < (uint32_t)a.topk) {
+        id[c] = load_id(a.ids, a.id_bytes, at + k);
+        t[c] = a.dtype == SNAC_BF16 ? bf16_lo(static_cast<const uint16_t*>(a.logits)[at + k])
+                                    : static_cast<const float*>(a.logits)[at + k];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c)
+      if ((uint64_t)id[c] >= (uint64_t)a.vocab || t[c] == -inf) id[c] = -1, t[c] = -inf;
+  }
+  // scale: log2(e) / temperature
+  __device__ __forceinline__ void weigh(float scale) {
+    const float inf = __builtin_inff();
+    top = -inf;
+    bool mine = false;
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) top = fmaxf(top, t[c]), mine |= id[c] >= 0;
+    any = __any(mine);
+    top = wave_max(top);
+    if (top == -inf) top = 0.0f;
+    total = 0.0;
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) {
+      q[c] = __builtin_amdgcn_exp2f((t[c] - top) * scale);
+      total += q[c];
+    }
+    total = wave_sum(total);
+    const double inv = total == 0.0 ? 0.0 : 1.0 / total;
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) q[c] = (float)(q[c] * inv);
+  }
+  // sum of q log q
+  __device__ __forceinline__ double entropy(double inv_tau) const {
+    const double log_total = total == 0.0 ? 0.0 : log(total);
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c)
+      if (q[c] != 0.0f) s += (double)q[c] * (((double)t[c] - (double)top) * inv_tau - log_total);
+    return wave_sum(s);
+  }
+};
+
+__device__ __forceinline__ float choice_scale(const snac_teacher& a) { return (float)(kLog2e / (double)a.temperature); }
+
+// Largest logit and sum of exponentials of what a lane has seen of a row.  The
+// sum is taken relative to the largest so far: one pass.
+struct Running {
+  float m;
+  double s;
+  __device__ __forceinline__ void start() { m = -__builtin_inff(), s = 0.0; }
+  // brought to another maximum
+  __device__ __forceinline__ double at(float top, float scale) const {
+    return m == -__builtin_inff() ? s : s * (double)__builtin_amdgcn_exp2f((m - top) * scale);
+  }
+  template <int U, uint32_t N>
+  __device__ __forceinline__ void add(const float (&f)[U][N], float scale) {
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) top = fmaxf(top, f[j][c]);
+    if (__any(top > m)) {
+      s = at(top, scale);
+      m = top;
+    }
+    const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float part = 0.0f;
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) part += __builtin_amdgcn_exp2f((f[j][c] - ref) * scale);
+      s += part;
+    }
+  }
+  __device__ __forceinline__ void over_wave(float scale) {
+    const float top = wave_max(m);
+    s = wave_sum(at(top, scale));
+    m = top;
+  }
+};
+
+constexpr int kUnits = 4;  // of a lane at a time
+
+// A row by W waves (kWaves rows a workgroup where W is 1).
+template <typename T, int W>
+__global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(const DistillArgs a) {
+  constexpr uint32_t N = kUnit<T>, kPiece = 64u * kUnits * N;
+  constexpr uint32_t kRows = W == 1 ? kWaves : 1;
+  __shared__ float tops[W];
+  __shared__ double totals[W];
+  const uint32_t lane = threadIdx.x & 63u, w = W == 1 ? 0 : wave_id();
+  const float inf = __builtin_inff(), scale = choice_scale(a.teacher);
+  const double inv_tau = 1.0 / (double)a.teacher.temperature;
+  const uint32_t pieces = (uint32_t)(((uint64_t)a.width + kPiece - 1) / kPiece);
+  for (uint64_t t = (uint64_t)blockIdx.x * kRows + (W == 1 ? wave_id() : 0); t < a.tokens; t += (uint64_t)gridDim.x * kRows) {
+    const char* row = a.logits + t * a.ld;
+    Running r;
+    r.start();
+    u32x4 next[kUnits] = {};
+    auto load = [&](uint32_t p) { ld_piece<T, kUnits, true>(row + (uint64_t)p * kPiece * T::kSize, a.width - p * kPiece, next); };
+    if (w < pieces) load(w);
+    for (uint32_t p = w; p < pieces; p += W) {
+      float f[kUnits][N];
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) unpack<T>(next[j], f[j]);
+      const uint32_t left = a.width - p * kPiece;
+      if (pieces - p > W) load(p + W);
+      if (left < kPiece) {
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+          for (uint32_t c = 0; c < N; ++c)
+            if ((j * 64u + lane) * N + c >= left) f[j][c] = -inf;
+      }
+      r.add(f, scale);
+    }
+    r.over_wave(scale);
+    if constexpr (W > 1) {
+      __syncthreads();  // the last row's are read
+      if (lane == 0) tops[w] = r.m, totals[w] = r.s;
+      __syncthreads();
+      if (w != 0) continue;
+      r.start();
+      if (lane < W) r.m = tops[lane], r.s = totals[lane];
+      r.over_wave(scale);
+    }
+    Choices k;
+    k.load(a.teacher, t);
+    float z[kChoices];
+    bool here[kChoices];
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) {
+      const int64_t at = k.id[c] - a.first;
+      here[c] = k.id[c] >= 0 && (uint64_t)at < a.width;
+      z[c] = here[c] ? load_elem<T>(row + at * (int64_t)T::kSize) : 0.0f;
+    }
+    k.weigh(scale);
+    double d = 0.0, q = 0.0;
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) {
+      if (!here[c] || k.q[c] == 0.0f) continue;
+      d += (double)k.q[c] * (z[c] == -inf ? -HUGE_VAL : ((double)z[c] - (double)r.m) * inv_tau);
+      q += k.q[c];
+    }
+    d = wave_sum(d);
+    if (a.loss) {
+      const double ent = k.entropy(inv_tau);
+      if (lane == 0) {
+        a.loss[t] = !k.any || r.s == 0.0 ? 0.0f : (float)(ent - d + log(r.s));
+        a.stats[2 * t] = r.m;
+        a.stats[2 * t + 1] = (float)r.s;
+      }
+    } else {
+      q = wave_sum(q);
+      if (lane == 0) {
+        float* part = a.part + 4 * t;
+        part[0] = r.m;
+        part[1] = (float)r.s;
+        part[2] = (float)d;
+        part[3] = (float)q;
+      }
+    }
+  }
+}
+
+// A token a wave, a shard's part a lane.
+__global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArgs a) {
+  const uint32_t lane = threadIdx.x & 63u;
+  const float inf = __builtin_inff();
+  const double inv_tau = 1.0 / (double)a.teacher.temperature;
+  for (uint64_t t = (uint64_t)blockIdx.x * kWaves + wave_id(); t < a.tokens; t += (uint64_t)gridDim.x * kWaves) {
+    float m = -inf, s = 0.0f, d = 0.0f, q = 0.0f;
+    if (lane < (uint32_t)a.shards) {
+      const float* part = a.parts + 4 * (lane * a.tokens + t);
+      m = part[0], s = part[1], d = part[2], q = part[3];
+    }
+    Choices k;
+    k.load(a.teacher, t);
+    k.weigh(choice_scale(a.teacher));
+    const float top = wave_max(m);
+    const double gap = ((double)m - (double)top) * inv_tau;
+    const double total = wave_sum(m == -inf ? (double)s : (double)s * exp(gap));
+    const double dot = wave_sum(q == 0.0f ? 0.0 : (double)d + (double)q * gap);
+    const double ent = k.entropy(inv_tau);
+    if (lane == 0) {
+      a.loss[t] = !k.any || total == 0.0 ? 0.0f : (float)(ent - dot + log(total));
+      a.stats[2 * t] = top;
+      a.stats[2 * t + 1] = (float)total;
+    }
+  }
+}
+
+// One wave a run of a row's pieces; those that hold a choice's column take its q
+// off before the rounding.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void distill_backward_kernel(const DistillArgs a, uint32_t pieces, uint32_t per,
+                                                                    uint32_t runs, uint64_t items) {
+  constexpr uint32_t N = kUnit<T>, kPiece = 64u * kUnits * N;
+  const uint32_t lane = threadIdx.x & 63u;
+  const float scale = choice_scale(a.teacher);
+  for (uint64_t it = (uint64_t)blockIdx.x * kWaves + wave_id(); it < items; it += (uint64_t)gridDim.x * kWaves) {
+    const uint64_t t = it / runs;
+    const uint32_t p0 = (uint32_t)(it - t * runs) * per, p1 = pieces - p0 < per ? pieces : p0 + per;
+    const char* row = a.logits + t * a.ld;
+    char* out = a.dlogits + t * a.ld_d;
+    u32x4 next[kUnits];
+    auto load = [&](uint32_t p) { ld_piece<T, kUnits, true>(row + (uint64_t)p * kPiece * T::kSize, a.width - p * kPiece, next); };
+    load(p0);
+    Choices k;
+    k.load(a.teacher, t);
+    const float top = a.stats[2 * t], total = a.stats[2 * t + 1];
+    const float factor = (float)((double)a.scale / (double)a.teacher.temperature * (a.dloss ? (double)a.dloss[t] : 1.0));
+    k.weigh(scale);
+    const bool part = k.any && total != 0.0f;
+    const float f0 = (float)((double)factor / (double)total);
+    for (uint32_t p = p0; p < p1; ++p) {
+      const uint32_t left = a.width - p * kPiece;
+      float f[kUnits][N];
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) unpack<T>(next[j], f[j]);
+      if (p + 1 < p1) load(p + 1);
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c) f[j][c] = part ? f0 * __builtin_amdgcn_exp2f((f[j][c] - top) * scale) : 0.0f;
+      if (part) {
+        const int64_t e0 = a.first + (int64_t)p * kPiece;
+        const uint32_t many = left < kPiece ? left : kPiece;
+#pragma unroll
+        for (int c = 0; c < kChoices; ++c) {
+          if (c * 64 >= a.teacher.topk) break;
+          const int64_t at = k.id[c] - e0;
+          uint64_t hits = __ballot(k.id[c] >= 0 && (uint64_t)at < many);
+          while (hits) {
+            const uint32_t l = (uint32_t)__builtin_ctzll(hits);
+            hits &= hits - 1;
+            const uint32_t col = (uint32_t)__builtin_amdgcn_readlane((int)at, (int)l);
+            const float q = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(k.q[c]), (int)l));
+            const uint32_t unit = col / N, el = col % N;
+            const float off = (unit & 63u) == lane ? factor * q : 0.0f;
+#pragma unroll
+            for (uint32_t j = 0; j < kUnits; ++j) {
+              if (unit / 64 != j) continue;
+#pragma unroll
+              for (uint32_t i = 0; i < N; ++i)
+                if (el == i) f[j][i] = f[j][i] - off;
+            }
+          }
+        }
+      }
+      u32x4 v[kUnits];
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) v[j] = pack<T>(f[j]);
+      st_piece<T, kUnits, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
+    }
+  }
+}
+
+uint32_t cus() {
+  const int n = device_cu_count();
+  return n > 0 ? (uint32_t)n : 1;
+}
+
+constexpr uint64_t kMaxGrid = 1u << 22;  // workgroups; grid-stride past them
+
+template <typename T>
+void distill_any(const DistillArgs& a, hipStream_t stream) {
+  const uint64_t bytes = (uint64_t)a.width * T::kSize;
+  auto grid = [&](uint64_t rows) {
+    const uint64_t want = (a.tokens + rows - 1) / rows;
+    return dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid));
+  };
+  if (bytes <= 16384) hipLaunchKernelGGL((distill_kernel<T, 1>), grid(kWaves), dim3(kThreads), 0, stream, a);
+  else if (a.tokens >= cus() * 2) hipLaunchKernelGGL((distill_kernel<T, 4>), grid(1), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((distill_kernel<T, 16>), grid(1), dim3(1024), 0, stream, a);
+}
+
+template <typename T>
+void distill_backward_any(const DistillArgs& a, hipStream_t stream) {
+  constexpr uint32_t kPiece = 64u * kUnits * kUnit<T>;
+  const uint32_t pieces = (uint32_t)(((uint64_t)a.width + kPiece - 1) / kPiece);
+  uint32_t per = 1;
+  while (per < 8 && a.tokens * ((pieces + per - 1) / per) > (uint64_t)cus() * 64) per *= 2;
+  const uint32_t runs = (pieces + per - 1) / per;
+  const uint64_t items = a.tokens * runs, want = (items + kWaves - 1) / kWaves;
+  hipLaunchKernelGGL((distill_backward_kernel<T>), dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid)), dim3(kThreads), 0,
+                     stream, a, pieces, per, runs, items);
+}
+
+}  // namespace
+
+hipError_t launch_distill(const DistillArgs& a, bool bf16, hipStream_t stream) {
+  if (bf16) distill_any<BF16>(a, stream);
+  else distill_any<F32>(a, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_distill_join(const DistillArgs& a, hipStream_t stream) {
+  const uint64_t want = (a.tokens + kWaves - 1) / kWaves;
+  hipLaunchKernelGGL(distill_join_kernel, dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid)), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_distill_backward(const DistillArgs& a, bool bf16, hipStream_t stream) {
+  if (bf16) distill_backward_any<BF16>(a, stream);
+  else distill_backward_any<F32>(a, stream);
+  return hipGetLastError();
+}
+
+}  // namespace snac

@@ -201,4 +201,95 @@ hipError_t launch_clip(const GradTile* tiles, uint32_t ntiles, const float* norm
 hipError_t launch_norm_and_clip(const GradTile* tiles, uint32_t ntiles, double* partial, float* norm, float max_norm,
                                 unsigned long long* pool, hipStream_t stream);
 
+// ----------------------------------------------------------- layer norm
+struct LayerNormArgs {
+  const char* x;
+  uint64_t ld_x;  // bytes
+  const char* weight;  // nullptr: 1
+  const char* bias;    // nullptr: 0
+  uint64_t tokens;
+  uint32_t width;
+  float eps;
+  char* out;
+  uint64_t ld_out;  // bytes
+  float* stats;     // nullptr: not wanted
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, bool bf16, bool param_bf16, hipStream_t stream);
+
+// How the rows of a gradient are dealt out: `per` rows to each of the `blocks`
+// workgroups, which leave one partial sum each.  row_sums: rows too wide for a
+// workgroup's registers, whose own sums are made by a launch before.
+struct LayerNormShape {
+  uint32_t blocks, per;
+  bool row_sums;
+};
+LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize);
+struct LayerNormBackwardArgs {
+  const char* dout;
+  uint64_t ld_dout;  // bytes
+  const char* x;
+  uint64_t ld_x;  // bytes
+  const char* weight;  // nullptr: 1
+  const float* stats;
+  uint64_t tokens;
+  uint32_t width;
+  char* dx;
+  uint64_t ld_dx;  // bytes
+  void* dweight;   // nullptr: not wanted
+  void* dbias;
+  int32_t accumulate;
+  float* partial;   // [blocks][2][width], nullptr: neither is wanted
+  float* row_sums;  // [tokens][2], see LayerNormShape
+};
+hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const LayerNormShape& s, bool bf16,
+                                      bool param_bf16, bool grad_bf16, hipStream_t stream);
+
+// --------------------------------------------------------- balance loss
+struct BalanceArgs {
+  int32_t experts, topk, score;
+  const void* logits;
+  uint64_t ld;  // elements
+  const int32_t* ids;
+  uint64_t tokens;
+  // of the load: scratch of `blocks` workgroups, then the result
+  double* sums;      // [blocks][experts]
+  uint32_t* counts;  // [blocks][experts]
+  uint32_t blocks;
+  float* load;       // [2][experts]; an input of the gradient
+  // of the gradient
+  float coefficient;
+  const float* dloss;
+  void* dlogits;
+  uint64_t ld_d;  // elements
+  int32_t accumulate;
+};
+constexpr uint32_t kBalanceMaxBlocks = 512;
+uint32_t balance_blocks(uint64_t tokens, int experts);
+hipError_t launch_balance_load(const BalanceArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_balance_loss(const float* load, int experts, float coefficient, float* loss, hipStream_t stream);
+hipError_t launch_balance_backward(const BalanceArgs& a, bool bf16, hipStream_t stream);
+
+// --------------------------------------------------------- distillation
+struct DistillArgs {
+  snac_teacher teacher;
+  const char* logits;
+  uint64_t ld;  // bytes
+  int64_t first;
+  uint32_t width;
+  uint64_t tokens;
+  float* loss;   // nullptr: a shard, into part
+  float* stats;  // an input of the gradient
+  float* part;
+  const float* parts;  // of the joining
+  int32_t shards;
+  // of the gradient
+  const float* dloss;
+  float scale;
+  char* dlogits;
+  uint64_t ld_d;  // bytes
+};
+hipError_t launch_distill(const DistillArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_distill_join(const DistillArgs& a, hipStream_t stream);
+hipError_t launch_distill_backward(const DistillArgs& a, bool bf16, hipStream_t stream);
+
 }  // namespace snac

@@ -1,6 +1,7 @@
 """Tensor-level calls of the operators beside the collectives
 (include/snac_ops.h): routing, dispatch and combine around ``all_to_all_v``,
-the vocabulary-sharded embedding, and the global gradient norm.
+the vocabulary-sharded embedding, the global gradient norm, layer norm, the
+experts' balance loss and the loss against a teacher's top logits.
 
 As in ``tensors``: the caller creates the outputs, this module checks shapes,
 dtypes and devices and hands pointers and sizes to the library, whose kernels
@@ -12,9 +13,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (router, snac_clip_grad_norm, snac_clip_grads, snac_combine, snac_combine_backward, snac_dispatch,
-               snac_dispatch_plan, snac_embedding, snac_embedding_backward, snac_grad_norm, snac_grads_finalize,
-               snac_grads_init, snac_route, snac_route_backward)
+from . import (SNAC_MAX_TEACHER, router, snac_balance_backward, snac_balance_load, snac_balance_loss, snac_clip_grad_norm,
+               snac_clip_grads, snac_combine, snac_combine_backward, snac_dispatch, snac_dispatch_plan, snac_distill,
+               snac_distill_backward, snac_distill_join, snac_distill_shard, snac_embedding, snac_embedding_backward,
+               snac_grad_norm, snac_grads_finalize, snac_grads_init, snac_layer_norm, snac_layer_norm_backward,
+               snac_route, snac_route_backward)
+from . import teacher as teacher_of
 
 _FLOAT = {torch.bfloat16: "bf16", torch.float32: "f32"}
 _ID = {torch.int32: 4, torch.int64: 8}
@@ -330,3 +334,193 @@ def clip_grad_norm(grads: GradList, max_norm: float, norm, stream=None) -> None:
     """``grad_norm`` into ``norm``, then ``clip_grads`` by it."""
     on = _scalar(norm, "clip_grad_norm")
     snac_clip_grad_norm(grads.handle, max_norm, norm, _stream(stream, on))
+
+
+def _vector(t, width: int, what: str) -> str:
+    if t.shape != (width,):
+        raise ValueError(f"{what} must have shape {(width,)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _float(t, what)
+
+
+def _vectors(a, b, width: int, what: str, names) -> str:
+    """The common type of two vectors that may be None (float32 where both are)."""
+    types = [_vector(t, width, f"{what}: {n}") for t, n in zip((a, b), names) if t is not None]
+    if len(types) == 2:
+        _pair(a, b, f"{what}: {names[0]} and {names[1]}")
+    return types[0] if types else "f32"
+
+
+def layer_norm(x, weight, bias, out, *, eps: float = 1e-5, stats=None, stream=None) -> None:
+    """Each row of ``x`` [tokens, width] less its mean, over its deviation,
+    times ``weight`` plus ``bias`` ([width], bfloat16 or float32, each may be
+    None); ``out`` may be ``x``.  ``stats`` [tokens, 2] (float32) receives mean
+    and 1 / deviation for the gradient; a pass without one leaves it out."""
+    ld_x, ld_out = _matrix(x, "layer_norm: x"), _matrix(out, "layer_norm: out")
+    dt = _float(x, "layer_norm: x")
+    _pair(x, out, "layer_norm: x and out")
+    t, w = x.shape
+    if out.shape != x.shape:
+        raise ValueError("layer_norm: out must have the shape of x")
+    pt = _vectors(weight, bias, w, "layer_norm", ("weight", "bias"))
+    if stats is not None:
+        _packed(stats, (t, 2), torch.float32, "layer_norm: stats")
+    on = _device("layer_norm", x, weight, bias, out, stats)
+    snac_layer_norm(x, ld_x, weight, bias, pt, t, w, eps, dt, out, ld_out, stats, _stream(stream, on))
+
+
+def layer_norm_backward(dout, x, weight, stats, dx, dweight, dbias, handle=None, *, accumulate: bool = False,
+                        stream=None) -> None:
+    """``dx`` (may be ``dout``) and the sums over the tokens ``dweight`` and
+    ``dbias`` [width] (bfloat16 or float32, each may be None), written or with
+    ``accumulate`` added to.  ``stats`` is ``layer_norm``'s.  ``handle`` is a
+    context of ``snac_init`` whose staging rings hold
+    ``snac_layer_norm_scratch`` bytes; without dweight and dbias rows of up to
+    32 KiB need none."""
+    ld_g, ld_x, ld_dx = (_matrix(m, "layer_norm_backward: " + n) for m, n in ((dout, "dout"), (x, "x"), (dx, "dx")))
+    dt = _float(x, "layer_norm_backward: x")
+    _pair(x, dout, "layer_norm_backward: x and dout")
+    _pair(x, dx, "layer_norm_backward: x and dx")
+    t, w = x.shape
+    if dout.shape != x.shape or dx.shape != x.shape:
+        raise ValueError("layer_norm_backward: dout and dx must have the shape of x")
+    pt = _vectors(weight, None, w, "layer_norm_backward", ("weight", ""))
+    gt = _vectors(dweight, dbias, w, "layer_norm_backward", ("dweight", "dbias"))
+    _packed(stats, (t, 2), torch.float32, "layer_norm_backward: stats")
+    on = _device("layer_norm_backward", dout, x, weight, stats, dx, dweight, dbias)
+    snac_layer_norm_backward(handle, dout, ld_g, x, ld_x, weight, pt, stats, t, w, dt, dx, ld_dx, dweight, dbias, gt,
+                             int(accumulate), _stream(stream, on))
+
+
+def _chosen(logits, ids, what: str):
+    """Row stride, type, tokens, experts and choices of a router's logits and ids."""
+    ld = _matrix(logits, f"{what}: logits")
+    dt = _float(logits, f"{what}: logits")
+    t, e = logits.shape
+    if ids.dim() != 2:
+        raise ValueError(f"{what}: ids must have two dimensions")
+    k = ids.shape[1]
+    _packed(ids, (t, k), torch.int32, f"{what}: ids")
+    return ld, dt, t, e, k
+
+
+def balance_load(logits, ids, load, handle, *, score: str = "softmax", stream=None) -> None:
+    """``load`` [2, experts] (float32): how many slots of ``ids`` [tokens, topk]
+    (int32, what ``route`` chose; others than 0 .. experts - 1 are not in use)
+    each expert got, and the sum of its shares of the tokens' scores.  Padding
+    tokens, those without an id in use, have no part.  With tokens on several
+    ranks an ``all_reduce`` of their loads gives the common one.  ``handle`` is
+    a context of ``snac_init``; its staging rings are scratch."""
+    ld, dt, t, e, k = _chosen(logits, ids, "balance_load")
+    _packed(load, (2, e), torch.float32, "balance_load: load")
+    on = _device("balance_load", logits, ids, load)
+    snac_balance_load(handle, router(e, k, score), logits, ld, ids, t, dt, load, _stream(stream, on))
+
+
+def balance_loss(load, loss, *, coefficient: float = 1.0, stream=None) -> None:
+    """loss[0] = coefficient * experts * sum of the experts' parts of the slots
+    times their parts of the shares: ``coefficient`` where they are even."""
+    if load.dim() != 2:
+        raise ValueError("balance_loss: load must have two dimensions")
+    e = load.shape[1]
+    _packed(load, (2, e), torch.float32, "balance_loss: load")
+    if loss.numel() != 1 or loss.dtype != torch.float32:
+        raise ValueError("balance_loss: loss must be one float32")
+    on = _device("balance_loss", load, loss)
+    snac_balance_loss(load, e, coefficient, loss, _stream(stream, on))
+
+
+def balance_backward(logits, ids, load, dlogits, *, score: str = "softmax", coefficient: float = 1.0, dloss=None,
+                     accumulate: bool = False, stream=None) -> None:
+    """``dlogits`` [tokens, experts], written or with ``accumulate`` added to
+    (what ``route_backward`` left), for the ``load`` that the loss was made of
+    and ``dloss`` (one float32 on the device, None: 1)."""
+    ld, dt, t, e, k = _chosen(logits, ids, "balance_backward")
+    ld_d = _matrix(dlogits, "balance_backward: dlogits")
+    _pair(logits, dlogits, "balance_backward: logits and dlogits")
+    if dlogits.shape != logits.shape:
+        raise ValueError("balance_backward: dlogits must have the shape of logits")
+    _packed(load, (2, e), torch.float32, "balance_backward: load")
+    if dloss is not None and (dloss.numel() != 1 or dloss.dtype != torch.float32):
+        raise ValueError("balance_backward: dloss must be one float32")
+    on = _device("balance_backward", logits, ids, load, dloss, dlogits)
+    snac_balance_backward(router(e, k, score), logits, ld, ids, load, coefficient, dloss, t, dt, dlogits, ld_d,
+                          int(accumulate), _stream(stream, on))
+
+
+def _teacher(ids, logits, tokens: int, vocab: int, temperature: float, what: str):
+    size, dt = _ids(ids, f"{what}: ids"), _float(logits, f"{what}: teacher")
+    if ids.dim() != 2 or ids.shape[0] != tokens or logits.shape != ids.shape:
+        raise ValueError(f"{what}: ids and teacher must have shape [{tokens}, choices], not {tuple(ids.shape)} and "
+                         f"{tuple(logits.shape)}")
+    if not (ids.is_contiguous() and logits.is_contiguous()):
+        raise ValueError(f"{what}: ids and teacher must be contiguous")
+    k = ids.shape[1]
+    if not 1 <= k <= SNAC_MAX_TEACHER:
+        raise ValueError(f"{what}: {k} choices outside 1..{SNAC_MAX_TEACHER}")
+    return teacher_of(ids, size, logits, dt, k, vocab, temperature)
+
+
+def distill(logits, ids, teacher, loss, stats, *, temperature: float = 1.0, stream=None) -> None:
+    """``loss`` [tokens] = the divergence of softmax(``logits`` / temperature)
+    [tokens, vocab] from the softmax of a teacher's top logits ``teacher``
+    [tokens, choices] (bfloat16 or float32) for the columns ``ids`` (int32 or
+    int64; others than 0 .. vocab - 1 are no choices, a token without any has
+    loss 0).  ``stats`` [tokens, 2] is for the gradient; both float32.
+    snac_teacher in the C header has the formulas."""
+    ld = _matrix(logits, "distill: logits")
+    dt = _float(logits, "distill: logits")
+    t, v = logits.shape
+    h = _teacher(ids, teacher, t, v, temperature, "distill")
+    _packed(loss, (t,), torch.float32, "distill: loss")
+    _packed(stats, (t, 2), torch.float32, "distill: stats")
+    on = _device("distill", logits, ids, teacher, loss, stats)
+    snac_distill(h, logits, ld, t, dt, loss, stats, _stream(stream, on))
+
+
+def distill_shard(logits, ids, teacher, part, *, first: int, vocab: int, temperature: float = 1.0, stream=None) -> None:
+    """``part`` [tokens, 4] (float32) of a rank that holds columns ``first`` to
+    first + logits.shape[1] - 1 of a vocabulary of ``vocab`` columns; the ranks'
+    parts, brought together by an ``all_gather``, go to ``distill_join``."""
+    ld = _matrix(logits, "distill_shard: logits")
+    dt = _float(logits, "distill_shard: logits")
+    t, w = logits.shape
+    h = _teacher(ids, teacher, t, vocab, temperature, "distill_shard")
+    _packed(part, (t, 4), torch.float32, "distill_shard: part")
+    on = _device("distill_shard", logits, ids, teacher, part)
+    snac_distill_shard(h, logits, ld, first, w, t, dt, part, _stream(stream, on))
+
+
+def distill_join(parts, ids, teacher, loss, stats, *, vocab: int, temperature: float = 1.0, stream=None) -> None:
+    """``loss`` [tokens] and ``stats`` [tokens, 2] of the shards' ``parts``
+    [shards, tokens, 4]."""
+    if parts.dim() != 3:
+        raise ValueError("distill_join: parts must have three dimensions")
+    n, t = parts.shape[:2]
+    _packed(parts, (n, t, 4), torch.float32, "distill_join: parts")
+    h = _teacher(ids, teacher, t, vocab, temperature, "distill_join")
+    _packed(loss, (t,), torch.float32, "distill_join: loss")
+    _packed(stats, (t, 2), torch.float32, "distill_join: stats")
+    on = _device("distill_join", parts, ids, teacher, loss, stats)
+    snac_distill_join(h, parts, n, t, loss, stats, _stream(stream, on))
+
+
+def distill_backward(logits, ids, teacher, stats, dlogits, *, dloss=None, scale: float = 1.0, first: int = 0,
+                     vocab: int | None = None, temperature: float = 1.0, stream=None) -> None:
+    """``dlogits`` (may be ``logits``): the gradient of scale * sum of dloss *
+    loss with respect to ``logits``, the whole vocabulary's or (with ``first``
+    and ``vocab``) a shard's.  ``stats`` is ``distill``'s or ``distill_join``'s;
+    ``dloss`` [tokens] (float32) may be None for all 1."""
+    ld, ld_d = _matrix(logits, "distill_backward: logits"), _matrix(dlogits, "distill_backward: dlogits")
+    dt = _float(logits, "distill_backward: logits")
+    _pair(logits, dlogits, "distill_backward: logits and dlogits")
+    t, w = logits.shape
+    if dlogits.shape != logits.shape:
+        raise ValueError("distill_backward: dlogits must have the shape of logits")
+    h = _teacher(ids, teacher, t, first + w if vocab is None else vocab, temperature, "distill_backward")
+    _packed(stats, (t, 2), torch.float32, "distill_backward: stats")
+    if dloss is not None:
+        _packed(dloss, (t,), torch.float32, "distill_backward: dloss")
+    on = _device("distill_backward", logits, ids, teacher, stats, dloss, dlogits)
+    snac_distill_backward(h, logits, ld, first, w, stats, dloss, scale, t, dt, dlogits, ld_d, _stream(stream, on))

@@ -15,6 +15,15 @@
  *       shard's gradient by sorted tokens
  *   snac_grads_init, snac_grad_norm, snac_clip_grads, snac_clip_grad_norm
  *       the global norm over many tensors, and clipping by it
+ *   snac_layer_norm, snac_layer_norm_backward
+ *       rows of mean 0 and variance 1, weighted, and the gradients
+ *   snac_balance_load, snac_balance_loss, snac_balance_backward
+ *       how evenly a router's choices load the experts, as a loss, and its
+ *       gradient (an AllReduce sums the ranks' loads)
+ *   snac_distill, snac_distill_shard, snac_distill_join, snac_distill_backward
+ *       the divergence from a teacher's top logits, over the whole vocabulary
+ *       or in shards of it (an AllGather brings their parts together), and
+ *       its gradient
  *
  * The conventions are those of snac.h: device pointers that the caller owns,
  * asynchronous on `stream`, argument errors reported at once with nothing
@@ -231,6 +240,164 @@ snac_status snac_clip_grads(snac_grads* grads, const float* norm, float max_norm
 
 /* snac_clip_grad_norm -- snac_grad_norm, then snac_clip_grads by it. */
 snac_status snac_clip_grad_norm(snac_grads* grads, float max_norm, float* norm, snac_stream stream);
+
+/* ----------------------------------------------------------- layer norm */
+
+/*
+ * snac_layer_norm -- for each row x of x[tokens][width]:
+ *   mean = sum x / width,  var = sum (x - mean)^2 / width,
+ *   rstd = 1 / sqrt(var + eps),  out = (x - mean) * rstd * weight + bias
+ * weight and bias: `width` values of param_dtype, or NULL (1 and 0; they may be
+ * given one without the other).  stats: NULL, or [tokens][2] binary32 that
+ * receive mean and rstd for the gradient.  The sums are binary32 within 16 bytes
+ * of a row and binary64 over them, the mean is subtracted in more than binary32's
+ * precision, each output is rounded once.  eps finite and >= 0 (with 0 a constant
+ * row gives NaN, by the formula).  out may be x itself (same ld).
+ */
+snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, const void* bias, snac_dtype param_dtype,
+                            size_t tokens, size_t width, float eps, snac_dtype dtype, void* out, size_t ld_out,
+                            float* stats, snac_stream stream);
+
+/*
+ * snac_layer_norm_backward -- from dout[tokens][width], with
+ * h = (x - mean) * rstd and g = dout * weight:
+ *   dx      = rstd * (g - sum g / width - h * (sum g h) / width)
+ *   dweight = sum over the tokens of dout * h   (NULL: not wanted)
+ *   dbias   = sum over the tokens of dout       (NULL: not wanted)
+ * stats: what snac_layer_norm left for these rows.  A row's sums are binary32
+ * within 16 bytes and binary64 over them; the sums over tokens are binary32 over
+ * at most 32 tokens, binary64 over those, rounded to binary32 and that to
+ * grad_dtype.
+ *   accumulate  0: dweight and dbias are written; 1: the sums are added to them
+ *               before the rounding
+ * dx may be dout itself (same ld).  Scratch is the context's staging rings:
+ * snac_layer_norm_scratch bytes (SNAC_E_ARG if the rings together are smaller);
+ * without dweight and dbias rows of up to 32 KiB need none, and ctx may be NULL.
+ */
+snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_dout, const void* x, size_t ld_x,
+                                     const void* weight, snac_dtype param_dtype, const float* stats, size_t tokens,
+                                     size_t width, snac_dtype dtype, void* dx, size_t ld_dx, void* dweight, void* dbias,
+                                     snac_dtype grad_dtype, int accumulate, snac_stream stream);
+
+/* Scratch of snac_layer_norm_backward with dweight or dbias, rows of `dtype`:
+ * staging bytes per rank times ranks must be at least this (0 for arguments that
+ * the call refuses). */
+size_t snac_layer_norm_scratch(size_t tokens, size_t width, snac_dtype dtype);
+
+/* --------------------------------------------------------- balance loss */
+
+/*
+ * A token with at least one id in 0 .. experts - 1 counts, others (padding) have
+ * no part.  For token t with logits x, its shares are
+ *   p = softmax(x), or sigmoid(x) / sum of sigmoid(x)     (router->score)
+ * (0 for a masked expert; all 0 where every logit is masked), and
+ *   c[e] = how many of the counting tokens' slots have id e
+ *   s[e] = sum of p[e] over the counting tokens
+ *   loss = coefficient * experts * sum over e of (c[e] / C) * (s[e] / S)
+ * with C and S the sums of c and s over the experts (0 where C or S is 0).  C is
+ * the number of slots in use and S of the counting tokens: even loads give
+ * `coefficient`.  The choice has no gradient, the shares have.  Very low logits
+ * keep their ratios; NaN spreads by the formulas.
+ */
+
+/*
+ * snac_balance_load -- load[0][experts] = c and load[1][experts] = s, binary32
+ * (c exactly, up to 2^24), from logits[tokens][experts] (row stride ld, `dtype`)
+ * and the ids[tokens][topk] that snac_route chose.  Of the router, experts, topk
+ * and score are used.  The sums over tokens are binary64.  An AllReduce of
+ * `load` gives the ranks' common load.  tokens * topk at most SNAC_MAX_IDS.
+ * Scratch is the context's staging rings, 12 bytes * experts * 512 at most;
+ * SNAC_E_ARG if they are smaller.
+ */
+snac_status snac_balance_load(snac_ctx* ctx, const snac_router* router, const void* logits, size_t ld,
+                              const int32_t* ids, size_t tokens, snac_dtype dtype, float* load, snac_stream stream);
+
+/* snac_balance_loss -- loss[0] of load[2][experts], sums in binary64. */
+snac_status snac_balance_loss(const float* load, int experts, float coefficient, float* loss, snac_stream stream);
+
+/*
+ * snac_balance_backward -- dlogits[tokens][experts] (row stride ld_d, `dtype`,
+ * every element written) of this rank's tokens, for the `load` that the loss was
+ * made of (the ranks' common one, where there are several):
+ *   a[e]    = dloss * coefficient * experts * c[e] / (C S)
+ *   dlogits = p[e] * (a[e] - sum over j of p[j] a[j])     (softmax)
+ *             the same * (1 - sigmoid(x[e]))              (sigmoid)
+ * and 0 for a token that does not count.  dloss: one binary32 on the device,
+ * NULL: 1.
+ *   accumulate  1: added to what dlogits holds (snac_route_backward's), rounded
+ *               once; a token that does not count is left as it is
+ */
+snac_status snac_balance_backward(const snac_router* router, const void* logits, size_t ld, const int32_t* ids,
+                                  const float* load, float coefficient, const float* dloss, size_t tokens,
+                                  snac_dtype dtype, void* dlogits, size_t ld_d, int accumulate, snac_stream stream);
+
+/* --------------------------------------------------------- distillation */
+
+/* most choices of a teacher that are given for a token */
+#define SNAC_MAX_TEACHER 256
+
+/*
+ * snac_teacher -- a teacher's top logits.  For a token with teacher's choices
+ * id_k, t_k (k = 0 .. topk - 1) and student's logits z over the vocabulary:
+ *   q_k  = softmax over its valid choices of t / temperature
+ *   p    = softmax over the vocabulary of z / temperature
+ *   loss = sum over k with q_k > 0 of q_k * (log q_k - log p[id_k])
+ * A choice is valid where 0 <= id_k < vocab and t_k is not -infinity; ids need
+ * not be ordered, and one that comes twice counts twice.  A masked z (-infinity)
+ * has p = 0; a valid choice of one makes the loss infinite.  A token without a
+ * valid choice, or whose logits are all masked, has no part: loss 0, gradient 0.
+ * NaN spreads by the formulas, +infinity as in softmax.  No factor of
+ * temperature^2 is applied; dloss and scale of the gradient can hold it.
+ */
+typedef struct snac_teacher {
+  const void* ids;     /* [tokens][topk], columns of the whole vocabulary */
+  const void* logits;  /* [tokens][topk] */
+  int64_t vocab;       /* columns of the whole vocabulary, 1 .. SNAC_MAX_BYTES */
+  int32_t id_bytes;    /* 4 or 8 */
+  int32_t dtype;       /* SNAC_F32 or SNAC_BF16, of `logits` here */
+  int32_t topk;        /* 1 .. SNAC_MAX_TEACHER */
+  float temperature;   /* 2^-64 .. 2^64 */
+} snac_teacher;
+
+/*
+ * snac_distill -- loss[tokens] and stats[tokens][2] of logits[tokens][vocab]
+ * (row stride ld, `dtype`).  stats: a row's largest logit m and
+ * S = sum of exp((z - m) / temperature), for the gradient.  Exponentials are
+ * binary32; they are summed in binary32 within 16 bytes of a row and in binary64
+ * over them; the loss is made in binary64 and rounded once.
+ */
+snac_status snac_distill(const snac_teacher* teacher, const void* logits, size_t ld, size_t tokens, snac_dtype dtype,
+                         float* loss, float* stats, snac_stream stream);
+
+/*
+ * snac_distill_shard -- the same for a rank that holds columns
+ * first .. first + width - 1 of the vocabulary, logits[tokens][width]:
+ * part[tokens][4] receives m and S of the shard's columns,
+ * D = sum of q_k * (z[id_k] - m) / temperature and Q = sum of q_k over the choices
+ * in the shard (q over all valid choices; a term of q_k = 0 is 0).
+ */
+snac_status snac_distill_shard(const snac_teacher* teacher, const void* logits, size_t ld, int64_t first, size_t width,
+                               size_t tokens, snac_dtype dtype, float* part, snac_stream stream);
+
+/*
+ * snac_distill_join -- loss and stats of the shards' parts
+ * parts[shards][tokens][4] (what an AllGather of `part` leaves), 1 ..
+ * SNAC_MAX_RANKS shards whose columns make up the vocabulary, in any order.
+ * Every rank that joins them gets the same bits.
+ */
+snac_status snac_distill_join(const snac_teacher* teacher, const float* parts, int shards, size_t tokens, float* loss,
+                              float* stats, snac_stream stream);
+
+/*
+ * snac_distill_backward -- the gradient of columns first .. first + width - 1:
+ *   dlogits[t][j] = scale * dloss[t] / temperature * (p_j - sum of q_k, id_k = j)
+ * with p from `stats` of the whole row.  dloss: [tokens] binary32, NULL: all 1.
+ * In binary32, choices in ascending k, rounded once.  dlogits may be logits
+ * itself (same ld).
+ */
+snac_status snac_distill_backward(const snac_teacher* teacher, const void* logits, size_t ld, int64_t first,
+                                  size_t width, const float* stats, const float* dloss, float scale, size_t tokens,
+                                  snac_dtype dtype, void* dlogits, size_t ld_d, snac_stream stream);
 
 #ifdef __cplusplus
 }
