@@ -9,8 +9,11 @@ namespace snac {
 namespace {
 
 // The widest rows that a workgroup holds in registers: 16 waves of 64 lanes of 4
-// units, or 2 where the gradient's sums over tokens are held too.
-constexpr uint64_t kHeldKib = 64, kHeldBackwardKib = 32;
+// units, or 2 where wider parameters or the gradient's sums over tokens are held
+// too.
+template <typename T, typename P>
+constexpr uint64_t kHeldKib = P::kSize > T::kSize ? 32 : 64;
+constexpr uint64_t kHeldBackwardKib = 32;
 constexpr uint32_t kSumTokens = 32;  // binary32 sums over tokens go no further
 
 // 16 bytes' worth of T elements' parameters of type P, raw.
@@ -19,7 +22,6 @@ struct Params {
   static constexpr int kWords = kUnit<T> * P::kSize / 4;
   uint32_t w[kWords];
 };
-typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 
 // Parameters of the kUnit<T> elements from `e` on; those past `width` read as 0.
 template <typename T, typename P>
@@ -49,10 +51,33 @@ __device__ __forceinline__ void ld_params(const char* p, uint32_t e, uint32_t wi
     }
   }
 }
+// All of them 1 (absent weights) or -0 (absent biases: x + -0 is x, also for -0).
+template <typename T, typename P>
+__device__ __forceinline__ void fill_params(float v, Params<T, P>& r) {
+  const uint32_t w = __float_as_uint(v);
+#pragma unroll
+  for (int c = 0; c < Params<T, P>::kWords; ++c) r.w[c] = P::kSize == 4 ? w : w | w >> 16;
+}
 template <typename T, typename P>
 __device__ __forceinline__ float param(const Params<T, P>& r, uint32_t i) {
   if constexpr (P::kSize == 4) return __uint_as_float(r.w[i]);
   else return i & 1 ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+}
+
+// Sum over W neighbouring lanes, W a power of two up to 16, in each of them.
+template <int D>
+__device__ __forceinline__ float exchange_sum(float x) {
+  return __uint_as_float(exchange<D>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int W, typename F>
+__device__ __forceinline__ F few_lanes_sum(F x) {
+  if constexpr (W > 1) x = exchange_sum<1>(x);
+  if constexpr (W > 2) x = exchange_sum<2>(x);
+  if constexpr (W > 4) x = exchange_sum<4>(x);
+  if constexpr (W > 8) x = exchange_sum<8>(x);
+  return x;
 }
 
 // Sums of a and b over the W waves of a row (`lds`: room for two numbers of each
@@ -65,30 +90,18 @@ __device__ __forceinline__ void row_sum(double& a, double& b, double (*lds)[2]) 
     const uint32_t lane = threadIdx.x & 63u, w = wave_id(), w0 = w / W * W;
     if (lane == 0) lds[w][0] = a, lds[w][1] = b;
     __syncthreads();
-    if constexpr (W == 16) {
-      a = lanes_sum<16>(lds[lane & 15][0]);
-      b = lanes_sum<16>(lds[lane & 15][1]);
-    } else {
-      a = lds[w0][0], b = lds[w0][1];
-#pragma unroll
-      for (int i = 1; i < W; ++i) a += lds[w0 + i][0], b += lds[w0 + i][1];
-    }
+    a = few_lanes_sum<W>(lds[w0 + lane % W][0]);
+    b = few_lanes_sum<W>(lds[w0 + lane % W][1]);
   }
 }
 template <int W, int NW>
-__device__ __forceinline__ double row_sum(double a, double (*lds)[2]) {
+__device__ __forceinline__ float row_sum(float a, float* lds) {
   a = wave_sum(a);
   if constexpr (W > 1) {
     const uint32_t lane = threadIdx.x & 63u, w = wave_id(), w0 = w / W * W;
-    if (lane == 0) lds[w][0] = a;
+    if (lane == 0) lds[w] = a;
     __syncthreads();
-    if constexpr (W == 16) {
-      a = lanes_sum<16>(lds[lane & 15][0]);
-    } else {
-      a = lds[w0][0];
-#pragma unroll
-      for (int i = 1; i < W; ++i) a += lds[w0 + i][0];
-    }
+    a = few_lanes_sum<W>(lds[w0 + lane % W]);
   }
   return a;
 }
@@ -100,6 +113,9 @@ __device__ __forceinline__ float inverse_root(double v) {
   return (float)(v > 0.0 && v < HUGE_VAL ? r * __builtin_fma(-0.5 * v * r, r, 1.5) : r);
 }
 
+// Rows that begin on lines are read past the caches; others share lines.
+__device__ __forceinline__ bool whole_lines(const char* p, uint64_t ld) { return (((uint64_t)(uintptr_t)p | ld) & 127) == 0; }
+
 // Sum over a unit of f(element), in binary32.
 template <uint32_t N, typename F>
 __device__ __forceinline__ float unit_sum(F f) {
@@ -109,19 +125,28 @@ __device__ __forceinline__ float unit_sum(F f) {
   return s;
 }
 
+// Sum over a unit of the products, fused in binary32.
+template <uint32_t N>
+__device__ __forceinline__ float unit_dot(const float (&x)[N], const float (&y)[N]) {
+  float s = x[0] * y[0];
+#pragma unroll
+  for (uint32_t c = 1; c < N; ++c) s = __builtin_fmaf(x[c], y[c], s);
+  return s;
+}
+
 // ------------------------------------------------------------------ forward
 
-// What a row's sums give.  The first sum over x is off by its own size's
-// roundings, which matter where the row is far from 0 and hardly varies: so the
-// second pass sums the distances d from that mean `near` too, and d - rest is
-// as good as x - mean with the exact mean.
+// What a row's sums give.  The mean `near` of the first pass is binary32
+// throughout and off by its sum's roundings, which matter where the row is far
+// from 0 and hardly varies: so the second pass sums the distances d from it as
+// well as their squares, and (d - rest) rstd is as good as with the exact mean.
 struct Moments {
-  float mean, rest, rstd;
+  float mean, rstd, shift;  // h = d * rstd + shift
   __device__ __forceinline__ Moments(float near, double mean_d, double mean_dd, float eps) {
     const double var = mean_dd - mean_d * mean_d;
-    rest = (float)mean_d;
     mean = (float)((double)near + mean_d);
     rstd = inverse_root((var < 0.0 ? 0.0 : var) + (double)eps);
+    shift = (float)(-mean_d * (double)rstd);
   }
 };
 
@@ -131,73 +156,93 @@ constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 // once although its mean is needed before its variance and that before the
 // result.
 template <typename T, typename P, int W, int U>
-__global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_norm_kernel(const LayerNormArgs a) {
+__global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_norm_kernel(const LayerNormArgs a,
+                                                                                                     const uint32_t per) {
   constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W;
   constexpr uint32_t N = kUnit<T>;
-  __shared__ double lds[2][NW][2];
+  __shared__ float first_sums[NW];
+  __shared__ double lds[NW][2];
   const uint32_t lane = threadIdx.x & 63u, w = wave_id(), g = w / W;
   const uint32_t first = (w % W) * 64u * U * N;  // the wave's piece of a row
   const uint32_t left = first < a.width ? a.width - first : 0;
+  const bool whole = whole_piece<T, U>(left);
   // the parameters are kept, and the next row is loaded while this one is worked
   // on, where registers allow it
   constexpr bool kAhead = W * U < 64;
   Params<T, P> weight[U], bias[U];
   auto params = [&](int j) {
     const uint32_t e = first + (j * 64u + lane) * N;
-    if (a.weight) ld_params<T, P>(a.weight, e, a.width, weight[j]);
-    if (a.bias) ld_params<T, P>(a.bias, e, a.width, bias[j]);
+    const char *pw = a.weight, *pb = a.bias;
+    // opaque here, so that they are not loaded before the loop after all
+    if constexpr (!kAhead) asm volatile("" : "+s"(pw), "+s"(pb));
+    if (pw) ld_params<T, P>(pw, e, a.width, weight[j]);
+    else fill_params<T, P>(1.0f, weight[j]);
+    if (pb) ld_params<T, P>(pb, e, a.width, bias[j]);
+    else fill_params<T, P>(-0.0f, bias[j]);
   };
   if constexpr (kAhead) {
 #pragma unroll
     for (int j = 0; j < U; ++j) params(j);
   }
   const double inv = 1.0 / (double)a.width;
-  const uint64_t step = (uint64_t)gridDim.x * G;
-  uint64_t t = (uint64_t)blockIdx.x * G + g;
+  const float inv_f = (float)inv;
+  const uint64_t t0 = (uint64_t)blockIdx.x * per, end = a.tokens - t0 < per ? a.tokens : t0 + per;
   u32x4 next[U] = {};
+  const bool lines = whole_lines(a.x, a.ld_x);
   auto load = [&](uint64_t row) {
-    if (row < a.tokens) ld_piece<T, U, true>(a.x + row * a.ld_x + (uint64_t)first * T::kSize, left, next);
+    if (row >= end) return;
+    const char* x = a.x + row * a.ld_x + (uint64_t)first * T::kSize;
+    if (lines) ld_held<T, U, true>(x, left, next);
+    else ld_held<T, U, false>(x, left, next);
   };
-  if constexpr (kAhead) load(t);
+  if constexpr (kAhead) load(t0 + g);
   // every wave of the workgroup goes round as often as its first
-  for (uint64_t t0 = (uint64_t)blockIdx.x * G; t0 < a.tokens; t0 += step, t += step) {
+  for (uint64_t s = t0; s < end; s += G) {
+    const uint64_t t = s + g;
     if constexpr (!kAhead) load(t);
     u32x4 v[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) v[j] = next[j];
-    if constexpr (kAhead) load(t + step);
-    float f[U][N];
-    double sum = 0.0;
+    if constexpr (kAhead) load(t + G);
+    float f[U][N], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       unpack<T>(v[j], f[j]);
       sum += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
     }
-    const float near = (float)(row_sum<W, NW>(sum, lds[0]) * inv);
+    const float near = row_sum<W, NW>(sum, first_sums) * inv_f;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) f[j][c] = f[j][c] - near;
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c)
+          if ((j * 64u + lane) * N + c >= left) f[j][c] = 0.0f;
+    }
     double sd = 0.0, sq = 0.0;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const uint32_t e = (j * 64u + lane) * N;  // within the wave's piece
-#pragma unroll
-      for (uint32_t c = 0; c < N; ++c) f[j][c] = e + c < left ? f[j][c] - near : 0.0f;
       sd += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
-      sq += unit_sum<N>([&](uint32_t c) { return f[j][c] * f[j][c]; });
+      sq += unit_dot<N>(f[j], f[j]);
     }
-    row_sum<W, NW>(sd, sq, lds[1]);
+    row_sum<W, NW>(sd, sq, lds);
     const Moments m(near, sd * inv, sq * inv, a.eps);
-    if (t < a.tokens) {
+    if (t < end) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        if constexpr (!kAhead) params(j);
-#pragma unroll
-        for (uint32_t c = 0; c < N; ++c) {
-          f[j][c] = (f[j][c] - m.rest) * m.rstd;
-          if (a.weight) f[j][c] = f[j][c] * param<T, P>(weight[j], c);
-          if (a.bias) f[j][c] = f[j][c] + param<T, P>(bias[j], c);
+        if constexpr (!kAhead) {
+          __builtin_amdgcn_sched_barrier(0);  // not all of them at once
+          params(j);
         }
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c)
+          f[j][c] = __builtin_fmaf(__builtin_fmaf(f[j][c], m.rstd, m.shift), param<T, P>(weight[j], c), param<T, P>(bias[j], c));
         v[j] = pack<T>(f[j]);
       }
-      st_piece<T, U, true>(a.out + t * a.ld_out + (uint64_t)first * T::kSize, left, v);
+      st_held<T, U, true>(a.out + t * a.ld_out + (uint64_t)first * T::kSize, left, v);
       if (a.stats && w % W == 0 && lane == 0) {
         a.stats[2 * t] = m.mean;
         a.stats[2 * t + 1] = m.rstd;
@@ -211,7 +256,8 @@ template <typename T, typename P>
 __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormArgs a) {
   constexpr int NW = 16;
   constexpr uint32_t N = kUnit<T>, kStep = 64u * NW * N;
-  __shared__ double lds[2][NW][2];
+  __shared__ float first_sums[NW];
+  __shared__ double lds[NW][2];
   const uint32_t lane = threadIdx.x & 63u, w = wave_id();
   const double inv = 1.0 / (double)a.width;
   for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
@@ -229,26 +275,25 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
     };
     double sum = 0.0, sd = 0.0, sq = 0.0;
     row([&](uint32_t, uint32_t, float (&u)[N]) { sum += unit_sum<N>([&](uint32_t c) { return u[c]; }); });
-    const float near = (float)(row_sum<NW, NW>(sum, lds[0]) * inv);
+    const float near = row_sum<NW, NW>((float)sum, first_sums) * (float)inv;
     row([&](uint32_t, uint32_t left, float (&u)[N]) {
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c) u[c] = lane * N + c < left ? u[c] - near : 0.0f;
       sd += unit_sum<N>([&](uint32_t c) { return u[c]; });
-      sq += unit_sum<N>([&](uint32_t c) { return u[c] * u[c]; });
+      sq += unit_dot<N>(u, u);
     });
-    row_sum<NW, NW>(sd, sq, lds[1]);
+    row_sum<NW, NW>(sd, sq, lds);
     const Moments m(near, sd * inv, sq * inv, a.eps);
     row([&](uint32_t e0, uint32_t left, float (&u)[N]) {
       Params<T, P> weight, bias;
       const uint32_t e = e0 + lane * N;
       if (a.weight && e < a.width) ld_params<T, P>(a.weight, e, a.width, weight);
+      else fill_params<T, P>(1.0f, weight);
       if (a.bias && e < a.width) ld_params<T, P>(a.bias, e, a.width, bias);
+      else fill_params<T, P>(-0.0f, bias);
 #pragma unroll
-      for (uint32_t c = 0; c < N; ++c) {
-        u[c] = ((u[c] - near) - m.rest) * m.rstd;
-        if (a.weight) u[c] = u[c] * param<T, P>(weight, c);
-        if (a.bias) u[c] = u[c] + param<T, P>(bias, c);
-      }
+      for (uint32_t c = 0; c < N; ++c)
+        u[c] = __builtin_fmaf(__builtin_fmaf(u[c] - near, m.rstd, m.shift), param<T, P>(weight, c), param<T, P>(bias, c));
       const u32x4 v[1] = {pack<T>(u)};
       st_piece<T, 1, true>(out + (uint64_t)e0 * T::kSize, left, v);
     });
@@ -262,8 +307,8 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
 
 // ----------------------------------------------------------------- backward
 
-constexpr int kGradWaves = 8;  // of a workgroup whose rows take up to 8 waves
-constexpr uint32_t kGradBlocks = 512;
+constexpr int kGradWaves = 16;  // of a workgroup
+constexpr uint32_t kGradBlocks = 256;
 
 // N binary32 values to `p`, the first `left` of them.
 template <uint32_t N>
@@ -280,9 +325,9 @@ __device__ __forceinline__ void st_sums(float* p, uint32_t left, const float (&f
 // W waves a row, U units a lane, G rows at a time; the sums over tokens stay in
 // registers and leave as one partial sum a workgroup.
 template <typename T, typename P, int W, int U>
-__global__ __launch_bounds__(64 * (W > kGradWaves ? W : kGradWaves)) void layer_norm_backward_kernel(
-    const LayerNormBackwardArgs a, const uint32_t per) {
-  constexpr int NW = W > kGradWaves ? W : kGradWaves, G = NW / W;
+__global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
+    const LayerNormBackwardArgs a) {
+  constexpr int NW = kGradWaves, G = NW / W;
   constexpr uint32_t N = kUnit<T>, kPiece = 64u * U * N;
   __shared__ double lds[2][NW][2];
   __shared__ __align__(16) float join[G > 1 ? G / 2 * W : 1][2][G > 1 ? kPiece : 1];
@@ -290,10 +335,12 @@ __global__ __launch_bounds__(64 * (W > kGradWaves ? W : kGradWaves)) void layer_
   const uint32_t first = (w % W) * kPiece;
   const uint32_t left = first < a.width ? a.width - first : 0;
   const uint64_t off = (uint64_t)first * T::kSize;
+  const bool whole = whole_piece<T, U>(left);
   Params<T, P> weight[U];
-  if (a.weight) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) ld_params<T, P>(a.weight, first + (j * 64u + lane) * N, a.width, weight[j]);
+  for (int j = 0; j < U; ++j) {
+    if (a.weight) ld_params<T, P>(a.weight, first + (j * 64u + lane) * N, a.width, weight[j]);
+    else fill_params<T, P>(1.0f, weight[j]);
   }
   float dw[U][N], db[U][N];
 #pragma unroll
@@ -301,52 +348,71 @@ __global__ __launch_bounds__(64 * (W > kGradWaves ? W : kGradWaves)) void layer_
 #pragma unroll
     for (uint32_t c = 0; c < N; ++c) dw[j][c] = db[j][c] = 0.0f;
   const float inv = (float)(1.0 / (double)a.width);
-  const uint64_t t0 = (uint64_t)blockIdx.x * per;
-  const uint64_t end = a.tokens - t0 < per ? a.tokens : t0 + per;
+  const bool lines = whole_lines(a.x, a.ld_x) && whole_lines(a.dout, a.ld_dout);
   u32x4 next_x[U] = {}, next_g[U] = {};
   auto load = [&](uint64_t t) {
-    ld_piece<T, U, true>(a.x + t * a.ld_x + off, left, next_x);
-    ld_piece<T, U, true>(a.dout + t * a.ld_dout + off, left, next_g);
+    if (t >= a.tokens) return;
+    if (lines) {
+      ld_held<T, U, true>(a.x + t * a.ld_x + off, left, next_x);
+      ld_held<T, U, true>(a.dout + t * a.ld_dout + off, left, next_g);
+    } else {
+      ld_held<T, U, false>(a.x + t * a.ld_x + off, left, next_x);
+      ld_held<T, U, false>(a.dout + t * a.ld_dout + off, left, next_g);
+    }
   };
-  if (t0 + g < end) load(t0 + g);
+  // rows of all workgroups' same turn lie side by side
+  const uint64_t step = (uint64_t)gridDim.x * G;
+  load((uint64_t)blockIdx.x * G + g);
   uint32_t turn = 0;
-  for (uint64_t s = t0; s < end; s += G, turn ^= 1) {
+  for (uint64_t s = (uint64_t)blockIdx.x * G; s < a.tokens; s += step, turn ^= 1) {
     const uint64_t t = s + g;
-    const bool live = t < end;
-    u32x4 vx[U], vg[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) vx[j] = next_x[j], vg[j] = next_g[j];
-    const float mean = live ? a.stats[2 * t] : 0.0f, rstd = live ? a.stats[2 * t + 1] : 0.0f;
-    if (t + G < end) load(t + G);
-    double c1 = 0.0, c2 = 0.0;
+    const bool live = t < a.tokens;
     float h[U][N], up[U][N];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      unpack<T>(next_x[j], h[j]);
+      unpack<T>(next_g[j], up[j]);
+    }
+    const float mean = live ? a.stats[2 * t] : 0.0f, rstd = live ? a.stats[2 * t + 1] : 0.0f;
+    load(t + step);
+    double c1 = 0.0, c2 = 0.0;
     if (live) {
 #pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c) h[j][c] = (h[j][c] - mean) * rstd;
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+          for (uint32_t c = 0; c < N; ++c)
+            if ((j * 64u + lane) * N + c >= left) h[j][c] = 0.0f;
+      }
+#pragma unroll
       for (int j = 0; j < U; ++j) {
-        unpack<T>(vx[j], h[j]);
-        unpack<T>(vg[j], up[j]);
-        const uint32_t e = (j * 64u + lane) * N;
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c) {
-          h[j][c] = e + c < left ? (h[j][c] - mean) * rstd : 0.0f;
+          if (c % (N / Params<T, P>::kWords ? N / Params<T, P>::kWords : 1) == 0)  // kept as it is stored
+            asm volatile("" : "+v"(weight[j].w[c * Params<T, P>::kWords / N]));
           dw[j][c] = __builtin_fmaf(up[j][c], h[j][c], dw[j][c]);
           db[j][c] += up[j][c];
-          if (a.weight) up[j][c] = up[j][c] * param<T, P>(weight[j], c);
+          up[j][c] = up[j][c] * param<T, P>(weight[j], c);
         }
         c1 += unit_sum<N>([&](uint32_t c) { return up[j][c]; });
-        c2 += unit_sum<N>([&](uint32_t c) { return up[j][c] * h[j][c]; });
+        c2 += unit_dot<N>(up[j], h[j]);
       }
     }
     row_sum<W, NW>(c1, c2, lds[turn]);
     if (!live) continue;
     const float m1 = (float)c1 * inv, m2 = (float)c2 * inv;
+    u32x4 v[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c) h[j][c] = rstd * __builtin_fmaf(-h[j][c], m2, up[j][c] - m1);
-      vx[j] = pack<T>(h[j]);
+      v[j] = pack<T>(h[j]);
     }
-    st_piece<T, U, true>(a.dx + t * a.ld_dx + off, left, vx);
+    st_held<T, U, true>(a.dx + t * a.ld_dx + off, left, v);
   }
   if (!a.partial) return;
   // the rows that went beside each other: the upper half of them to the lower
@@ -511,12 +577,24 @@ uint32_t cus() {
   return n > 0 ? (uint32_t)n : 1;
 }
 
+// The rows of a workgroup, one after another: its parameters are loaded once for
+// them.
 template <typename T, typename P, int W, int U>
 void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
   constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W;
-  const uint64_t want = (a.tokens + G - 1) / G, most = (uint64_t)cus() * 32 / NW;
-  hipLaunchKernelGGL((layer_norm_kernel<T, P, W, U>), dim3((uint32_t)(want < most ? want : most)), dim3(64 * NW), 0,
-                     stream, a);
+  const uint32_t row = (a.width * T::kSize + 1023) / 1024 * G;
+  uint32_t per = G * (row > 16 ? 4 : row > 1 ? (32 + row - 1) / row : 32);
+  while (per > G && (a.tokens + per - 1) / per < cus() * 4) per /= 2;
+  const uint64_t most = (uint64_t)per << 22;  // rows of a launch
+  LayerNormArgs c = a;
+  for (uint64_t t = 0; t < a.tokens; t += most) {
+    c.tokens = a.tokens - t < most ? a.tokens - t : most;
+    c.x = a.x + t * a.ld_x;
+    c.out = a.out + t * a.ld_out;
+    c.stats = a.stats ? a.stats + 2 * t : nullptr;
+    hipLaunchKernelGGL((layer_norm_kernel<T, P, W, U>), dim3((uint32_t)((c.tokens + per - 1) / per)), dim3(64 * NW), 0,
+                       stream, c, per);
+  }
 }
 
 // The narrowest shape that holds a row, in units of 1 KiB (64 lanes).
@@ -528,9 +606,10 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   else if (kib <= 4) layer_norm_in<T, P, 1, 4>(a, stream);
   else if (kib <= 8) layer_norm_in<T, P, 4, 2>(a, stream);
   else if (kib <= 16) layer_norm_in<T, P, 4, 4>(a, stream);
-  else if (kib <= 32) layer_norm_in<T, P, 16, 2>(a, stream);
-  else if (kib <= kHeldKib) layer_norm_in<T, P, 16, 4>(a, stream);
-  else {
+  else if (kib <= 32) layer_norm_in<T, P, 8, 4>(a, stream);
+  else if (kib <= kHeldKib<T, P>) {
+    if constexpr (kHeldKib<T, P> > 32) layer_norm_in<T, P, 16, 4>(a, stream);
+  } else {
     const uint64_t most = (uint64_t)cus() * 2;
     hipLaunchKernelGGL((layer_norm_wide_kernel<T, P>), dim3((uint32_t)(a.tokens < most ? a.tokens : most)), dim3(1024),
                        0, stream, a);
@@ -539,8 +618,7 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
 
 template <typename T, typename P, int W, int U>
 void layer_norm_backward_in(const LayerNormBackwardArgs& a, const LayerNormShape& s, hipStream_t stream) {
-  constexpr int NW = W > kGradWaves ? W : kGradWaves;
-  hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, W, U>), dim3(s.blocks), dim3(64 * NW), 0, stream, a, s.per);
+  hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, W, U>), dim3(s.blocks), dim3(64 * kGradWaves), 0, stream, a);
 }
 
 template <typename T, typename P>
@@ -555,9 +633,9 @@ void layer_norm_backward_any(const LayerNormBackwardArgs& a, const LayerNormShap
                        s.per);
   } else if (kib <= 1) layer_norm_backward_in<T, P, 1, 1>(a, s, stream);
   else if (kib <= 2) layer_norm_backward_in<T, P, 1, 2>(a, s, stream);
-  else if (kib <= 4) layer_norm_backward_in<T, P, 1, 4>(a, s, stream);
+  else if (kib <= 4) layer_norm_backward_in<T, P, 2, 2>(a, s, stream);
   else if (kib <= 8) layer_norm_backward_in<T, P, 4, 2>(a, s, stream);
-  else if (kib <= 16) layer_norm_backward_in<T, P, 4, 4>(a, s, stream);
+  else if (kib <= 16) layer_norm_backward_in<T, P, 8, 2>(a, s, stream);
   else layer_norm_backward_in<T, P, 16, 2>(a, s, stream);
 }
 
@@ -573,9 +651,13 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
   const uint64_t bytes = width * esize;
   LayerNormShape s{0, kSumTokens, bytes > kHeldBackwardKib * 1024};
   if (tokens == 0) return s;
-  // rows beside each other in a workgroup of layer_norm_backward_kernel
-  const uint64_t rows = s.row_sums || bytes > 16384 ? 1 : bytes > 4096 ? kGradWaves / 4 : kGradWaves;
-  uint64_t turns = (tokens + rows * kGradBlocks - 1) / (rows * kGradBlocks);
+  // rows side by side in a workgroup of layer_norm_backward_kernel, and how many
+  // workgroups they are dealt out to
+  const uint64_t kib = (bytes + 1023) / 1024;
+  uint64_t rows = 1, most = kGradBlocks;
+  if (s.row_sums) most = kGradBlocks * 16 / kib + 1;
+  else rows = kib <= 2 ? 16 : kib <= 4 ? 8 : kib <= 8 ? 4 : kib <= 16 ? 2 : 1;
+  uint64_t turns = (tokens + rows * most - 1) / (rows * most);
   if (turns > kSumTokens) turns = kSumTokens;
   s.per = (uint32_t)(rows * turns);
   s.blocks = (uint32_t)((tokens + s.per - 1) / s.per);

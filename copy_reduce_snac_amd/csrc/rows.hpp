@@ -142,6 +142,92 @@ __device__ __forceinline__ void st_piece(char* row, uint32_t left, const u32x4 (
   }
 }
 
+// 8, 4 or 2 bytes at any element alignment
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+
+// ld_part and st_part with `n` the same in all lanes: an access for each of its
+// bits instead of one for each element.
+template <typename T>
+__device__ __forceinline__ u32x4 ld_rest(const char* p, uint32_t n) {
+  auto two = [&](uint32_t at) { return *(global_ptr<const u32x2_a2>)(p + at); };
+  auto one = [&](uint32_t at) { return (uint32_t) * (global_ptr<const u32_a2>)(p + at); };
+  auto half = [&](uint32_t at) { return (uint32_t) * (global_ptr<const uint16_t>)(p + at); };
+  u32x4 v = {0, 0, 0, 0};
+  const uint32_t words = T::kSize == 4 ? n : n / 2;
+  if (words & 2) {
+    const auto w = two(0);
+    v[0] = w[0], v[1] = w[1];
+    if (words & 1) v[2] = one(8);
+  } else if (words & 1) {
+    v[0] = one(0);
+  }
+  if (T::kSize == 2 && (n & 1)) {
+    const uint32_t h = half(words * 4);
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      if (words == c) v[c] = h;
+  }
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void st_rest(char* p, u32x4 v, uint32_t n) {
+  const uint32_t words = T::kSize == 4 ? n : n / 2;
+  if (words & 2) {
+    *(global_ptr<u32x2_a2>)(p) = u32x2_a2{v[0], v[1]};
+    if (words & 1) *(global_ptr<u32_a2>)(p + 8) = v[2];
+  } else if (words & 1) {
+    *(global_ptr<u32_a2>)(p) = v[0];
+  }
+  if (T::kSize == 2 && (n & 1)) {
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      if (words == c) *(global_ptr<uint16_t>)(p + words * 4) = (uint16_t)v[c];
+  }
+}
+
+// Pieces that are often not whole (a row held in registers, every row's last
+// one): `left` is the same in all lanes, so the elements of a part unit go under
+// one branch of the wave instead of a branch for each of its units.
+template <typename T, int U, bool NT>
+__device__ __forceinline__ void ld_held(const char* row, uint32_t left, u32x4 (&v)[U]) {
+  const uint32_t lane = threadIdx.x & 63u;
+  if (whole_piece<T, U>(left)) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) v[j] = ld_unit<NT>(row + (j * 64u + lane) * 16u);
+    return;
+  }
+  const uint32_t units = left / kUnit<T>, rest = left % kUnit<T>;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    v[j] = u32x4{0, 0, 0, 0};
+    if (j * 64u + lane < units) v[j] = ld_unit<NT>(row + (j * 64u + lane) * 16u);
+  }
+  if (rest != 0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (j * 64u + lane == units) v[j] = ld_rest<T>(row + units * 16u, rest);
+  }
+}
+template <typename T, int U, bool NT>
+__device__ __forceinline__ void st_held(char* row, uint32_t left, const u32x4 (&v)[U]) {
+  const uint32_t lane = threadIdx.x & 63u;
+  if (whole_piece<T, U>(left)) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) st_unit<NT>(row + (j * 64u + lane) * 16u, v[j]);
+    return;
+  }
+  const uint32_t units = left / kUnit<T>, rest = left % kUnit<T>;
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+    if (j * 64u + lane < units) st_unit<NT>(row + (j * 64u + lane) * 16u, v[j]);
+  if (rest != 0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (j * 64u + lane == units) st_rest<T>(row + units * 16u, v[j], rest);
+  }
+}
+
 // What this wave's lanes wrote to LDS before is what its lanes read after: LDS
 // keeps a wave's order by itself, this keeps the compiler to it (which may
 // otherwise take a lane's own store for what it reads back).  No instructions.
