@@ -11,14 +11,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kChoices = SNAC_MAX_TEACHER / 64;  // of a lane
+constexpr int kMaxSlots = SNAC_MAX_TEACHER / 64;  // of a lane, see Choices
 constexpr double kLog2e = 1.4426950408889634;
 
-// A token's choices, choice c * 64 + lane in slot c of a lane: their columns
-// (-1: not valid), the teacher's logits, and after weigh() their q.
+// A token's choices, up to 64 C of them, choice c * 64 + lane in slot c of a lane:
+// their columns (-1: not valid), the teacher's logits, and after weigh() their q.
+template <int C>
 struct Choices {
-  int64_t id[kChoices];
-  float t[kChoices], q[kChoices];
+  int64_t id[C];
+  float t[C], q[C];
   float top;     // the largest valid logit
   double total;  // sum of exp((t - top) / temperature)
   bool any;      // a valid choice: the token has a part
@@ -28,7 +29,7 @@ struct Choices {
     const float inf = __builtin_inff();
     const uint64_t at = token * (uint32_t)a.topk;
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c) {
+    for (int c = 0; c < C; ++c) {
       const uint32_t k = c * 64 + lane;
       id[c] = -1;
       t[c] = -inf;
@@ -40,7 +41,7 @@ struct Choices {
       }
     }
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c)
+    for (int c = 0; c < C; ++c)
       if ((uint64_t)id[c] >= (uint64_t)a.vocab || t[c] == -inf) id[c] = -1, t[c] = -inf;
   }
   // scale: log2(e) / temperature
@@ -49,27 +50,27 @@ struct Choices {
     top = -inf;
     bool mine = false;
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c) top = fmaxf(top, t[c]), mine |= id[c] >= 0;
+    for (int c = 0; c < C; ++c) top = fmaxf(top, t[c]), mine |= id[c] >= 0;
     any = __any(mine);
     top = wave_max(top);
     if (top == -inf) top = 0.0f;
     total = 0.0;
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c) {
+    for (int c = 0; c < C; ++c) {
       q[c] = __builtin_amdgcn_exp2f((t[c] - top) * scale);
       total += q[c];
     }
     total = wave_sum(total);
     const double inv = total == 0.0 ? 0.0 : 1.0 / total;
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c) q[c] = (float)(q[c] * inv);
+    for (int c = 0; c < C; ++c) q[c] = (float)(q[c] * inv);
   }
   // sum of q log q
   __device__ __forceinline__ double entropy(double inv_tau) const {
     const double log_total = total == 0.0 ? 0.0 : log(total);
     double s = 0.0;
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c)
+    for (int c = 0; c < C; ++c)
       if (q[c] != 0.0f) s += (double)q[c] * (((double)t[c] - (double)top) * inv_tau - log_total);
     return wave_sum(s);
   }
@@ -116,8 +117,10 @@ struct Running {
 
 constexpr int kUnits = 4;  // of a lane at a time
 
-// A row by W waves (kWaves rows a workgroup where W is 1).
-template <typename T, int W>
+// A row by W waves (kWaves rows a workgroup where W is 1), once through.  The last
+// wave, which has the fewest pieces, sees to the choices before it begins and
+// makes the loss of them in the end.
+template <typename T, int W, int C>
 __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(const DistillArgs a) {
   constexpr uint32_t N = kUnit<T>, kPiece = 64u * kUnits * N;
   constexpr uint32_t kRows = W == 1 ? kWaves : 1;
@@ -127,13 +130,33 @@ __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(con
   const float inf = __builtin_inff(), scale = choice_scale(a.teacher);
   const double inv_tau = 1.0 / (double)a.teacher.temperature;
   const uint32_t pieces = (uint32_t)(((uint64_t)a.width + kPiece - 1) / kPiece);
+  const bool lines = whole_lines(a.logits, a.ld);
   for (uint64_t t = (uint64_t)blockIdx.x * kRows + (W == 1 ? wave_id() : 0); t < a.tokens; t += (uint64_t)gridDim.x * kRows) {
     const char* row = a.logits + t * a.ld;
+    u32x4 next[kUnits] = {};
+    auto load = [&](uint32_t p) {
+      const char* at = row + (uint64_t)p * kPiece * T::kSize;
+      if (lines) ld_held<T, kUnits, true>(at, a.width - p * kPiece, next);
+      else ld_held<T, kUnits, false>(at, a.width - p * kPiece, next);
+    };
+    if (w < pieces) load(w);
+    Choices<C> k;
+    float z[C];
+    bool here[C];
+    auto choices = [&] {
+      k.load(a.teacher, t);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int64_t at = k.id[c] - a.first;
+        here[c] = k.id[c] >= 0 && (uint64_t)at < a.width;
+        z[c] = here[c] ? load_elem<T>(row + at * (int64_t)T::kSize) : 0.0f;
+      }
+      k.weigh(scale);
+    };
+    constexpr bool kEarly = C == 1 && W < 16;  // else they cost the loop registers
+    if (kEarly && w == W - 1) choices();
     Running r;
     r.start();
-    u32x4 next[kUnits] = {};
-    auto load = [&](uint32_t p) { ld_piece<T, kUnits, true>(row + (uint64_t)p * kPiece * T::kSize, a.width - p * kPiece, next); };
-    if (w < pieces) load(w);
     for (uint32_t p = w; p < pieces; p += W) {
       float f[kUnits][N];
 #pragma unroll
@@ -151,28 +174,20 @@ __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(con
     }
     r.over_wave(scale);
     if constexpr (W > 1) {
-      __syncthreads();  // the last row's are read
       if (lane == 0) tops[w] = r.m, totals[w] = r.s;
       __syncthreads();
-      if (w != 0) continue;
-      r.start();
-      if (lane < W) r.m = tops[lane], r.s = totals[lane];
-      r.over_wave(scale);
+      if (w == W - 1) {
+        r.start();
+        if (lane < W) r.m = tops[lane], r.s = totals[lane];
+        r.over_wave(scale);
+      }
+      if (a.tokens - t > gridDim.x) __syncthreads();  // they are read
+      if (w != W - 1) continue;
     }
-    Choices k;
-    k.load(a.teacher, t);
-    float z[kChoices];
-    bool here[kChoices];
-#pragma unroll
-    for (int c = 0; c < kChoices; ++c) {
-      const int64_t at = k.id[c] - a.first;
-      here[c] = k.id[c] >= 0 && (uint64_t)at < a.width;
-      z[c] = here[c] ? load_elem<T>(row + at * (int64_t)T::kSize) : 0.0f;
-    }
-    k.weigh(scale);
+    if (!kEarly) choices();
     double d = 0.0, q = 0.0;
 #pragma unroll
-    for (int c = 0; c < kChoices; ++c) {
+    for (int c = 0; c < C; ++c) {
       if (!here[c] || k.q[c] == 0.0f) continue;
       d += (double)k.q[c] * (z[c] == -inf ? -HUGE_VAL : ((double)z[c] - (double)r.m) * inv_tau);
       q += k.q[c];
@@ -199,6 +214,7 @@ __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(con
 }
 
 // A token a wave, a shard's part a lane.
+template <int C>
 __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArgs a) {
   const uint32_t lane = threadIdx.x & 63u;
   const float inf = __builtin_inff();
@@ -209,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArg
       const float* part = a.parts + 4 * (lane * a.tokens + t);
       m = part[0], s = part[1], d = part[2], q = part[3];
     }
-    Choices k;
+    Choices<C> k;
     k.load(a.teacher, t);
     k.weigh(choice_scale(a.teacher));
     const float top = wave_max(m);
@@ -225,56 +241,80 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArg
   }
 }
 
-// One wave a run of a row's pieces; those that hold a choice's column take its q
-// off before the rounding.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void distill_backward_kernel(const DistillArgs a, uint32_t pieces, uint32_t per,
-                                                                    uint32_t runs, uint64_t items) {
-  constexpr uint32_t N = kUnit<T>, kPiece = 64u * kUnits * N;
-  const uint32_t lane = threadIdx.x & 63u;
+// One workgroup a run of a row's pieces, a wave every kBackWaves-th of them.  Its
+// first wave makes the choices' q while the others' logits are on their way; a
+// piece that holds a choice's column takes its q off before the rounding.
+constexpr int kBackWaves = 4;
+constexpr int kBackUnits = 2;  // of a lane at a time
+constexpr uint32_t kBackTurns = 2;
+
+template <typename T, int C>
+__global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const DistillArgs a, uint32_t pieces, uint32_t per,
+                                                                           uint32_t runs, uint64_t items) {
+  constexpr uint32_t N = kUnit<T>, kPiece = 64u * kBackUnits * N;
+  __shared__ uint32_t columns[C * 64];  // of the run's choices, counted from its first
+  __shared__ float offs[C * 64];
+  __shared__ uint32_t some;
+  const uint32_t lane = threadIdx.x & 63u, w = wave_id();
   const float scale = choice_scale(a.teacher);
-  for (uint64_t it = (uint64_t)blockIdx.x * kWaves + wave_id(); it < items; it += (uint64_t)gridDim.x * kWaves) {
+  const bool lines = whole_lines(a.logits, a.ld);
+  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const uint64_t t = it / runs;
     const uint32_t p0 = (uint32_t)(it - t * runs) * per, p1 = pieces - p0 < per ? pieces : p0 + per;
     const char* row = a.logits + t * a.ld;
     char* out = a.dlogits + t * a.ld_d;
-    u32x4 next[kUnits];
-    auto load = [&](uint32_t p) { ld_piece<T, kUnits, true>(row + (uint64_t)p * kPiece * T::kSize, a.width - p * kPiece, next); };
-    load(p0);
-    Choices k;
-    k.load(a.teacher, t);
+    u32x4 next[kBackUnits];
+    auto load = [&](uint32_t p) {
+      const char* at = row + (uint64_t)p * kPiece * T::kSize;
+      if (lines) ld_held<T, kBackUnits, true>(at, a.width - p * kPiece, next);
+      else ld_held<T, kBackUnits, false>(at, a.width - p * kPiece, next);
+    };
+    if (p0 + w < p1) load(p0 + w);
     const float top = a.stats[2 * t], total = a.stats[2 * t + 1];
     const float factor = (float)((double)a.scale / (double)a.teacher.temperature * (a.dloss ? (double)a.dloss[t] : 1.0));
-    k.weigh(scale);
-    const bool part = k.any && total != 0.0f;
     const float f0 = (float)((double)factor / (double)total);
-    for (uint32_t p = p0; p < p1; ++p) {
+    if (w == 0) {
+      Choices<C> k;
+      k.load(a.teacher, t);
+      k.weigh(scale);
+      const int64_t e0 = a.first + (int64_t)p0 * kPiece;
+      const uint64_t many = (uint64_t)(p1 - p0) * kPiece, left = a.width - (uint64_t)p0 * kPiece;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int64_t at = k.id[c] - e0;
+        columns[c * 64 + lane] = k.id[c] >= 0 && (uint64_t)at < (left < many ? left : many) ? (uint32_t)at : ~0u;
+        offs[c * 64 + lane] = factor * k.q[c];
+      }
+      if (lane == 0) some = k.any;
+    }
+    __syncthreads();
+    const bool part = some != 0 && total != 0.0f;
+    uint32_t column[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) column[c] = columns[c * 64 + lane];
+    for (uint32_t p = p0 + w; p < p1; p += kBackWaves) {
       const uint32_t left = a.width - p * kPiece;
-      float f[kUnits][N];
+      float f[kBackUnits][N];
 #pragma unroll
-      for (int j = 0; j < kUnits; ++j) unpack<T>(next[j], f[j]);
-      if (p + 1 < p1) load(p + 1);
+      for (int j = 0; j < kBackUnits; ++j) unpack<T>(next[j], f[j]);
+      if (p1 - p > kBackWaves) load(p + kBackWaves);
 #pragma unroll
-      for (int j = 0; j < kUnits; ++j)
+      for (int j = 0; j < kBackUnits; ++j)
 #pragma unroll
-        for (uint32_t c = 0; c < N; ++c) f[j][c] = part ? f0 * __builtin_amdgcn_exp2f((f[j][c] - top) * scale) : 0.0f;
+        for (uint32_t c = 0; c < N; ++c) f[j][c] = f0 * __builtin_amdgcn_exp2f((f[j][c] - top) * scale);
       if (part) {
-        const int64_t e0 = a.first + (int64_t)p * kPiece;
-        const uint32_t many = left < kPiece ? left : kPiece;
 #pragma unroll
-        for (int c = 0; c < kChoices; ++c) {
-          if (c * 64 >= a.teacher.topk) break;
-          const int64_t at = k.id[c] - e0;
-          uint64_t hits = __ballot(k.id[c] >= 0 && (uint64_t)at < many);
+        for (int c = 0; c < C; ++c) {
+          const uint32_t at = column[c] - (p - p0) * kPiece;
+          uint64_t hits = __ballot(column[c] != ~0u && at < kPiece);
           while (hits) {
             const uint32_t l = (uint32_t)__builtin_ctzll(hits);
             hits &= hits - 1;
             const uint32_t col = (uint32_t)__builtin_amdgcn_readlane((int)at, (int)l);
-            const float q = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(k.q[c]), (int)l));
             const uint32_t unit = col / N, el = col % N;
-            const float off = (unit & 63u) == lane ? factor * q : 0.0f;
+            const float off = (unit & 63u) == lane ? offs[c * 64 + l] : 0.0f;
 #pragma unroll
-            for (uint32_t j = 0; j < kUnits; ++j) {
+            for (uint32_t j = 0; j < kBackUnits; ++j) {
               if (unit / 64 != j) continue;
 #pragma unroll
               for (uint32_t i = 0; i < N; ++i)
@@ -283,11 +323,12 @@ __global__ __launch_bounds__(kThreads) void distill_backward_kernel(const Distil
           }
         }
       }
-      u32x4 v[kUnits];
+      u32x4 v[kBackUnits];
 #pragma unroll
-      for (int j = 0; j < kUnits; ++j) v[j] = pack<T>(f[j]);
-      st_piece<T, kUnits, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
+      for (int j = 0; j < kBackUnits; ++j) v[j] = part ? pack<T>(f[j]) : u32x4{0, 0, 0, 0};
+      st_held<T, kBackUnits, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
     }
+    if (items - it > gridDim.x) __syncthreads();  // the choices are read
   }
 }
 
@@ -298,47 +339,50 @@ uint32_t cus() {
 
 constexpr uint64_t kMaxGrid = 1u << 22;  // workgroups; grid-stride past them
 
-template <typename T>
+template <typename T, int C>
 void distill_any(const DistillArgs& a, hipStream_t stream) {
   const uint64_t bytes = (uint64_t)a.width * T::kSize;
   auto grid = [&](uint64_t rows) {
     const uint64_t want = (a.tokens + rows - 1) / rows;
     return dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid));
   };
-  if (bytes <= 16384) hipLaunchKernelGGL((distill_kernel<T, 1>), grid(kWaves), dim3(kThreads), 0, stream, a);
-  else if (a.tokens >= cus() * 2) hipLaunchKernelGGL((distill_kernel<T, 4>), grid(1), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((distill_kernel<T, 16>), grid(1), dim3(1024), 0, stream, a);
+  if (bytes <= 16384) hipLaunchKernelGGL((distill_kernel<T, 1, C>), grid(kWaves), dim3(kThreads), 0, stream, a);
+  else if (a.tokens >= cus() * 2) hipLaunchKernelGGL((distill_kernel<T, 4, C>), grid(1), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((distill_kernel<T, 16, C>), grid(1), dim3(1024), 0, stream, a);
 }
 
-template <typename T>
+template <typename T, int C>
 void distill_backward_any(const DistillArgs& a, hipStream_t stream) {
-  constexpr uint32_t kPiece = 64u * kUnits * kUnit<T>;
+  constexpr uint32_t kPiece = 64u * kBackUnits * kUnit<T>;
   const uint32_t pieces = (uint32_t)(((uint64_t)a.width + kPiece - 1) / kPiece);
-  uint32_t per = 1;
-  while (per < 8 && a.tokens * ((pieces + per - 1) / per) > (uint64_t)cus() * 64) per *= 2;
+  const uint32_t per = kBackWaves * kBackTurns;
   const uint32_t runs = (pieces + per - 1) / per;
-  const uint64_t items = a.tokens * runs, want = (items + kWaves - 1) / kWaves;
-  hipLaunchKernelGGL((distill_backward_kernel<T>), dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid)), dim3(kThreads), 0,
-                     stream, a, pieces, per, runs, items);
+  const uint64_t items = a.tokens * runs;
+  hipLaunchKernelGGL((distill_backward_kernel<T, C>), dim3((uint32_t)(items < kMaxGrid ? items : kMaxGrid)),
+                     dim3(64 * kBackWaves), 0, stream, a, pieces, per, runs, items);
 }
 
 }  // namespace
 
 hipError_t launch_distill(const DistillArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16) distill_any<BF16>(a, stream);
-  else distill_any<F32>(a, stream);
+  const bool few = a.teacher.topk <= 64;
+  if (bf16) few ? distill_any<BF16, 1>(a, stream) : distill_any<BF16, kMaxSlots>(a, stream);
+  else few ? distill_any<F32, 1>(a, stream) : distill_any<F32, kMaxSlots>(a, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_distill_join(const DistillArgs& a, hipStream_t stream) {
   const uint64_t want = (a.tokens + kWaves - 1) / kWaves;
-  hipLaunchKernelGGL(distill_join_kernel, dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid)), dim3(kThreads), 0, stream, a);
+  const dim3 grid((uint32_t)(want < kMaxGrid ? want : kMaxGrid));
+  if (a.teacher.topk <= 64) hipLaunchKernelGGL((distill_join_kernel<1>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((distill_join_kernel<kMaxSlots>), grid, dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 hipError_t launch_distill_backward(const DistillArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16) distill_backward_any<BF16>(a, stream);
-  else distill_backward_any<F32>(a, stream);
+  const bool few = a.teacher.topk <= 64;
+  if (bf16) few ? distill_backward_any<BF16, 1>(a, stream) : distill_backward_any<BF16, kMaxSlots>(a, stream);
+  else few ? distill_backward_any<F32, 1>(a, stream) : distill_backward_any<F32, kMaxSlots>(a, stream);
   return hipGetLastError();
 }
 

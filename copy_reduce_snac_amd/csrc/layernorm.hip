@@ -113,9 +113,6 @@ __device__ __forceinline__ float inverse_root(double v) {
   return (float)(v > 0.0 && v < HUGE_VAL ? r * __builtin_fma(-0.5 * v * r, r, 1.5) : r);
 }
 
-// Rows that begin on lines are read past the caches; others share lines.
-__device__ __forceinline__ bool whole_lines(const char* p, uint64_t ld) { return (((uint64_t)(uintptr_t)p | ld) & 127) == 0; }
-
 // Sum over a unit of f(element), in binary32.
 template <uint32_t N, typename F>
 __device__ __forceinline__ float unit_sum(F f) {

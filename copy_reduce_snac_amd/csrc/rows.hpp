@@ -186,6 +186,10 @@ __device__ __forceinline__ void st_rest(char* p, u32x4 v, uint32_t n) {
   }
 }
 
+// Whether every row begins on a line (`ld` in bytes).  Such rows may be read past
+// the caches; of others two share a line, and each would fetch it.
+__device__ __forceinline__ bool whole_lines(const char* p, uint64_t ld) { return (((uint64_t)(uintptr_t)p | ld) & 127) == 0; }
+
 // Pieces that are often not whole (a row held in registers, every row's last
 // one): `left` is the same in all lanes, so the elements of a part unit go under
 // one branch of the wave instead of a branch for each of its units.
