@@ -31,24 +31,33 @@ struct Row {
   // the row's element that is this lane's j-th
   __device__ __forceinline__ uint32_t at(int j) const { return UNITS ? ((j / N) * L + l) * N + j % N : j * L + l; }
 
-  // a lane without an element reads the row's first; `rest` is put in its place
-  __device__ __forceinline__ void load(const char* row, float rest, float (&x)[V]) const {
+  // a lane without an element reads the row's first
+  struct Raw {
+    u32x4 unit[UNITS ? V / N : 1];
+    float one[UNITS ? 1 : V];
+  };
+  __device__ __forceinline__ void fetch(const char* row, Raw& raw) const {
     if constexpr (UNITS) {
-      u32x4 w[V / N];
 #pragma unroll
-      for (int u = 0; u < V / N; ++u) w[u] = ld_unit<false>(row + (at(u * N) < E ? at(u * N) : 0) * T::kSize);
+      for (int u = 0; u < V / N; ++u) raw.unit[u] = ld_unit<false>(row + (at(u * N) < E ? at(u * N) : 0) * T::kSize);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) raw.one[j] = load_elem<T>(row + (at(j) < E ? at(j) : 0) * T::kSize);
+    }
+  }
+  // what was fetched; `rest` is put in the place of what a lane has not
+  __device__ __forceinline__ void take(const Raw& raw, float rest, float (&x)[V]) const {
+    if constexpr (UNITS) {
 #pragma unroll
       for (int u = 0; u < V / N; ++u) {
         float f[N];
-        unpack<T>(w[u], f);
+        unpack<T>(raw.unit[u], f);
 #pragma unroll
         for (int c = 0; c < N; ++c) x[u * N + c] = at(u * N) < E ? f[c] : rest;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = load_elem<T>(row + (at(j) < E ? at(j) : 0) * T::kSize);
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = at(j) < E ? x[j] : rest;
+      for (int j = 0; j < V; ++j) x[j] = at(j) < E ? raw.one[j] : rest;
     }
   }
   __device__ __forceinline__ void store(char* row, const float (&x)[V]) const {
@@ -68,18 +77,22 @@ struct Row {
   }
 };
 
+// The largest of a row's logits; 0 where all are masked.
+template <int L, int V>
+__device__ __forceinline__ float row_top(const float (&x)[V]) {
+  float top = x[0];
+#pragma unroll
+  for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
+  top = lanes_max<L>(top);
+  return top == -__builtin_inff() || top != top ? 0.0f : top;
+}
+
 // A row's scores x -> e and 1 over their sum: e * inv are the shares.
 // Exponentials are binary32, their sum binary64.  Sigmoids where all are small
 // are taken times exp(-m), m the largest logit, so that they do not underflow.
 // far: 1 - sigmoid of each logit.
 template <int L, int V, bool FAR>
-__device__ __forceinline__ double shares(bool softmax, float (&x)[V], float (&far)[FAR ? V : 1]) {
-  const float inf = __builtin_inff();
-  float top = -inf;
-#pragma unroll
-  for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
-  top = lanes_max<L>(top);
-  if (top == -inf) top = 0.0f;  // every logit masked (or NaN)
+__device__ __forceinline__ double shares(bool softmax, float top, float (&x)[V], float (&far)[FAR ? V : 1]) {
   double total = 0.0;
   if (softmax) {
 #pragma unroll
@@ -105,91 +118,126 @@ __device__ __forceinline__ double shares(bool softmax, float (&x)[V], float (&fa
   return total == 0.0 ? 0.0 : reciprocal(total);
 }
 
-// Whether the token of this lane's L lanes has an id in range; with COUNT, its
-// ids are counted.
-template <int L, bool COUNT>
-__device__ __forceinline__ bool counts(const BalanceArgs& a, uint64_t t, bool live, uint32_t l, uint32_t* hist) {
-  bool any = false;
-  for (uint32_t k = l; k < (uint32_t)a.topk; k += L) {
-    const int32_t id = live ? a.ids[t * (uint32_t)a.topk + k] : -1;
-    if ((uint32_t)id < (uint32_t)a.experts) {
-      any = true;
-      if constexpr (COUNT) atomicAdd(&hist[id], 1u);
+// The ids of a token's choices, choice c L + l in slot c of lane l.
+template <int L>
+struct Ids {
+  static constexpr int C = (SNAC_MAX_TOPK + L - 1) / L;
+  int32_t id[C];
+  __device__ __forceinline__ void fetch(const BalanceArgs& a, uint64_t t) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t k = c * L + threadIdx.x % L;
+      id[c] = k < (uint32_t)a.topk ? a.ids[t * (uint32_t)a.topk + k] : -1;
     }
   }
-  const uint64_t mask = __ballot(any), lanes = L == 64 ? ~0ull : ((1ull << (L & 63)) - 1) << ((threadIdx.x & 63u) / L * L);
-  return (mask & lanes) != 0;
-}
+  // whether the token of this lane's L lanes has an id in range
+  __device__ __forceinline__ bool any(uint32_t experts) const {
+    bool mine = false;
+#pragma unroll
+    for (int c = 0; c < C; ++c) mine |= (uint32_t)id[c] < experts;
+    const uint64_t lanes = L == 64 ? ~0ull : ((1ull << (L & 63)) - 1) << ((threadIdx.x & 63u) / L * L);
+    return (__ballot(mine) & lanes) != 0;
+  }
+};
+
+constexpr int kLoadThreads = 1024;
+constexpr int kLoadWaves = kLoadThreads / 64;
 
 // Sums of the shares and counts of the ids of this workgroup's tokens.
 template <typename T, int L, int V, bool UNITS>
-__global__ __launch_bounds__(kThreads) void balance_load_kernel(const BalanceArgs a) {
-  constexpr uint32_t TPW = 64 / L, kRows = kWaves * TPW;
+__global__ __launch_bounds__(kLoadThreads) void balance_load_kernel(const BalanceArgs a) {
+  constexpr uint32_t TPW = 64 / L, kRows = kLoadWaves * TPW;
+  constexpr int kPer = L * V <= 512 ? V : 512 / L;  // elements of a lane that are added up at a time
   __shared__ uint32_t hist[L * V];
-  __shared__ double sums[kRows][L * V <= 256 ? L * V : 256];
-  const Row<T, L, V, UNITS> r((uint32_t)a.experts);
-  const uint32_t sub = (threadIdx.x & 63u) / L;
+  __shared__ double sums[kLoadWaves][kPer * L];
+  using R = Row<T, L, V, UNITS>;
+  const R r((uint32_t)a.experts);
+  const uint32_t lane = threadIdx.x & 63u, sub = lane / L;
   const bool softmax = a.score == SNAC_SCORE_SOFTMAX;
-  for (uint32_t e = threadIdx.x; e < L * V; e += kThreads) hist[e] = 0;
+  const uint64_t step = (uint64_t)gridDim.x * kRows;
+  uint64_t t = (uint64_t)blockIdx.x * kRows + wave_id() * TPW + sub;
+  typename R::Raw next;
+  Ids<L> ids;
+  auto fetch = [&](uint64_t token) {  // (one past the last reads the last, and counts for nothing)
+    const uint64_t at = token < a.tokens ? token : a.tokens - 1;
+    r.fetch(static_cast<const char*>(a.logits) + at * a.ld * T::kSize, next);
+    ids.fetch(a, at);
+  };
+  constexpr bool kAhead = UNITS;  // else it costs too many registers
+  if (kAhead) fetch(t);
+  for (uint32_t e = threadIdx.x; e < L * V; e += kLoadThreads) hist[e] = 0;
   __syncthreads();
   double acc[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) acc[j] = 0.0;
-  const uint64_t step = (uint64_t)gridDim.x * kRows;
-  for (uint64_t t0 = (uint64_t)blockIdx.x * kRows + wave_id() * TPW; t0 < a.tokens; t0 += step) {
-    const bool live = t0 + sub < a.tokens;
-    const uint64_t t = live ? t0 + sub : t0;
+  for (uint64_t t0 = t - sub; t0 < a.tokens; t0 += step, t += step) {
     float x[V], none[1];
-    r.load(static_cast<const char*>(a.logits) + t * a.ld * T::kSize, -__builtin_inff(), x);
-    const bool in = counts<L, true>(a, t, live, r.l, hist);
-    const double inv = shares<L, V, false>(softmax, x, none);
+    if (!kAhead) fetch(t);
+    r.take(next, -__builtin_inff(), x);
+    const bool in = ids.any(r.E) && t < a.tokens;
+    if (t < a.tokens) {
+#pragma unroll
+      for (int c = 0; c < ids.C; ++c)
+        if ((uint32_t)ids.id[c] < r.E) atomicAdd(&hist[ids.id[c]], 1u);
+    }
+    if (kAhead && t0 + step < a.tokens) fetch(t + step);
+    const double inv = shares<L, V, false>(softmax, row_top<L>(x), x, none);
     if (in) {
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = __builtin_fma((double)x[j], inv, acc[j]);
     }
   }
-  // the workgroup's rows are added up in order, up to 256 experts at a time
-  constexpr int kPer = L * V <= 256 ? V : 256 / L;
+  // the tokens side by side in a wave, then the waves, in order
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if constexpr (L <= 16) acc[j] = exchange_sum<16>(acc[j]);
+    if constexpr (L <= 32) acc[j] = exchange_sum<32>(acc[j]);
+  }
   double* out = a.sums + (uint64_t)blockIdx.x * r.E;
 #pragma unroll
   for (int j0 = 0; j0 < V; j0 += kPer) {
     __syncthreads();
+    if (sub == 0) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) sums[wave_id() * TPW + sub][j * L + r.l] = acc[j0 + j];
+      for (int j = 0; j < kPer; ++j) sums[wave_id()][j * L + r.l] = acc[j0 + j];
+    }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < (uint32_t)(kPer * L); i += kThreads) {
+    const uint32_t i = threadIdx.x;
+    if (i < (uint32_t)(kPer * L)) {
       double s = 0.0;
 #pragma unroll
-      for (uint32_t k = 0; k < kRows; ++k) s += sums[k][i];
-      Row<T, L, V, UNITS> other(r.E);
+      for (uint32_t k = 0; k < kLoadWaves; ++k) s += sums[k][i];
+      R other(r.E);
       other.l = i % L;
       const uint32_t e = other.at((int)(j0 + i / L));
       if (e < r.E) out[e] = s;
     }
   }
-  for (uint32_t e = threadIdx.x; e < r.E; e += kThreads) a.counts[(uint64_t)blockIdx.x * r.E + e] = hist[e];
+  for (uint32_t e = threadIdx.x; e < r.E; e += kLoadThreads) a.counts[(uint64_t)blockIdx.x * r.E + e] = hist[e];
 }
 
-// load from the workgroups' sums and counts: 64 experts a workgroup, its waves
-// taking every 16th.
+// load from the workgroups' sums and counts: 16 experts a workgroup, a lane
+// taking every 64th of an expert's numbers.
 constexpr int kJoinWaves = 16;
 __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(const BalanceArgs a) {
-  __shared__ double sums[kJoinWaves][64];
-  __shared__ uint32_t counts[kJoinWaves][64];
-  const uint32_t lane = threadIdx.x & 63u, w = wave_id(), E = (uint32_t)a.experts, e = blockIdx.x * 64 + lane;
+  __shared__ double sums[kJoinWaves][16];
+  __shared__ uint32_t counts[kJoinWaves][16];
+  const uint32_t lane = threadIdx.x & 63u, w = wave_id(), E = (uint32_t)a.experts, e = blockIdx.x * 16 + lane % 16;
   double s = 0.0;
   uint32_t c = 0;
   if (e < E) {
 #pragma unroll 4
-    for (uint32_t b = w; b < a.blocks; b += kJoinWaves) {
+    for (uint32_t b = threadIdx.x / 16; b < a.blocks; b += 4 * kJoinWaves) {
       s += a.sums[(uint64_t)b * E + e];
       c += a.counts[(uint64_t)b * E + e];
     }
   }
-  sums[w][lane] = s;
-  counts[w][lane] = c;
+  auto add = [](uint32_t x, uint32_t y) { return x + y; };
+  s = exchange_sum<32>(exchange_sum<16>(s));
+  c = exchange<32>(exchange<16>(c, add), add);
+  if (lane < 16) sums[w][lane] = s, counts[w][lane] = c;
   __syncthreads();
-  if (w != 0 || e >= E) return;
+  if (threadIdx.x >= 16 || e >= E) return;
 #pragma unroll
   for (int i = 1; i < kJoinWaves; ++i) s += sums[i][lane], c += counts[i][lane];
   a.load[e] = (float)c;
@@ -211,53 +259,84 @@ __global__ __launch_bounds__(64) void balance_loss_kernel(const float* load, uin
 }
 
 // The gradient.  A token's shares sum to 1, so a constant may be taken off every
-// expert's slope: counts are taken less their mean, which leaves small numbers
-// where the loads are nearly even.  Sums over a row are binary64.
+// expert's slope: counts are taken less that of the token's best expert.  These
+// differences of whole numbers are exact, and the best expert's own term, which
+// is what the others leave, is not a small difference of large ones.
 template <typename T, int L, int V, bool UNITS>
 __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const BalanceArgs a) {
   constexpr uint32_t TPW = 64 / L, kRows = kWaves * TPW;
-  const Row<T, L, V, UNITS> r((uint32_t)a.experts);
+  using R = Row<T, L, V, UNITS>;
+  const R r((uint32_t)a.experts);
+  const float inf = __builtin_inff();
   const uint32_t sub = (threadIdx.x & 63u) / L;
   const bool softmax = a.score == SNAC_SCORE_SOFTMAX;
-  float slope[V];
-  double c = 0.0, s = 0.0;
+  const uint64_t step = (uint64_t)gridDim.x * kRows;
+  uint64_t t = (uint64_t)blockIdx.x * kRows + wave_id() * TPW + sub;
+  typename R::Raw next;
+  Ids<L> ids;
+  auto fetch = [&](uint64_t token) {  // (one past the last reads the last)
+    const uint64_t at = token < a.tokens ? token : a.tokens - 1;
+    r.fetch(static_cast<const char*>(a.logits) + at * a.ld * T::kSize, next);
+    ids.fetch(a, at);
+  };
+  fetch(t);
+  // 16 bytes at a time (by single numbers, which lie 32 bytes apart from lane to
+  // lane, 32768 x 256 bf16 took 19.9 us instead of 10.9)
+  float count[V];
+  if constexpr (UNITS) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const bool in = r.at(j) < r.E;
-    slope[j] = in ? a.load[r.at(j)] : 0.0f;
-    c += slope[j];
-    s += in ? a.load[r.E + r.at(j)] : 0.0f;
+    for (int j = 0; j < V; j += 4) {
+      const uint32_t e = r.at(j);
+      const u32x4 v = ld_unit<false>(reinterpret_cast<const char*>(a.load + (e < r.E ? e : 0)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) count[j + i] = e < r.E ? __uint_as_float(v[i]) : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) count[j] = r.at(j) < r.E ? a.load[r.at(j)] : 0.0f;
   }
-  c = lanes_sum<L>(c);
-  s = lanes_sum<L>(s);
-  const double mean = c / (double)r.E;
+  double c = 0.0, s = 0.0;
+  for (uint32_t e = threadIdx.x & 63u; e < r.E; e += 64) c += a.load[e], s += a.load[r.E + e];
+  c = wave_sum(c);
+  s = wave_sum(s);
   const double scale = c == 0.0 || s == 0.0 ? 0.0
                                             : (a.dloss ? (double)a.dloss[0] : 1.0) * (double)a.coefficient * (double)r.E / (c * s);
+  for (uint64_t t0 = t - sub; t0 < a.tokens; t0 += step, t += step) {
+    float x[V], far[V];
+    r.take(next, -inf, x);
+    const bool in = ids.any(r.E);
+    if (t0 + step < a.tokens) fetch(t + step);
+    const float top = row_top<L>(x);
+    float best = -inf;
 #pragma unroll
-  for (int j = 0; j < V; ++j) slope[j] = (float)(((double)slope[j] - mean) * scale);
-  const uint64_t step = (uint64_t)gridDim.x * kRows;
-  for (uint64_t t0 = (uint64_t)blockIdx.x * kRows + wave_id() * TPW; t0 < a.tokens; t0 += step) {
-    const bool live = t0 + sub < a.tokens;
-    const uint64_t t = live ? t0 + sub : t0;
-    float x[V], far[V], old[V];
-    r.load(static_cast<const char*>(a.logits) + t * a.ld * T::kSize, -__builtin_inff(), x);
-    char* out = static_cast<char*>(a.dlogits) + t * a.ld_d * T::kSize;
-    if (a.accumulate) r.load(out, 0.0f, old);
-    uint32_t* nothing = nullptr;
-    const bool in = counts<L, false>(a, t, live, r.l, nothing);
-    const double inv = shares<L, V, true>(softmax, x, far);
-    double dot = 0.0;
+    for (int j = 0; j < V; ++j) best = x[j] == top ? fmaxf(best, count[j]) : best;
+    best = lanes_max<L>(best);
+    if (best == -inf) best = 0.0f;
+    const double inv = shares<L, V, true>(softmax, top, x, far);
+    float dot[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < V; ++j) dot = __builtin_fma((double)x[j], (double)slope[j], dot);
-    dot = lanes_sum<L>(dot) * inv;
+    for (int j = 0; j < V; ++j) dot[j % 4] = __builtin_fmaf(x[j], count[j] - best, dot[j % 4]);
+    const float mean = (float)((double)lanes_sum<L>((dot[0] + dot[1]) + (dot[2] + dot[3])) * inv);
+    const float f = (float)(inv * scale);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float d = (float)((double)x[j] * inv * ((double)slope[j] - dot));
-      if (!softmax) d = d * far[j];
-      x[j] = in ? d : 0.0f;
-      if (a.accumulate) x[j] = in ? old[j] + d : old[j];
+      x[j] = x[j] * f * ((count[j] - best) - mean);
+      if (!softmax) x[j] = x[j] * far[j];
     }
-    if (live) r.store(out, x);
+    char* out = static_cast<char*>(a.dlogits) + (t < a.tokens ? t : a.tokens - 1) * a.ld_d * T::kSize;
+    if (a.accumulate) {
+      typename R::Raw raw;
+      float old[V];
+      r.fetch(out, raw);
+      r.take(raw, 0.0f, old);
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = old[j] + x[j];
+      if (t < a.tokens && in) r.store(out, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = in ? x[j] : 0.0f;
+      if (t < a.tokens) r.store(out, x);
+    }
   }
 }
 
@@ -285,7 +364,7 @@ struct LoadLauncher {
   hipStream_t stream;
   template <typename T, int L, int V, bool UNITS>
   void operator()() const {
-    hipLaunchKernelGGL((balance_load_kernel<T, L, V, UNITS>), dim3(a.blocks), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((balance_load_kernel<T, L, V, UNITS>), dim3(a.blocks), dim3(kLoadThreads), 0, stream, a);
   }
 };
 struct BackwardLauncher {
@@ -295,7 +374,7 @@ struct BackwardLauncher {
   void operator()() const {
     constexpr uint64_t rows = kWaves * (64 / L);
     const int n = device_cu_count();
-    const uint64_t want = (a.tokens + rows - 1) / rows, most = (uint64_t)(n > 0 ? n : 1) * 8;
+    const uint64_t want = (a.tokens + rows - 1) / rows, most = (uint64_t)(n > 0 ? n : 1) * 3;
     hipLaunchKernelGGL((balance_backward_kernel<T, L, V, UNITS>), dim3((uint32_t)(want < most ? want : most)),
                        dim3(kThreads), 0, stream, a);
   }
@@ -304,7 +383,7 @@ struct BackwardLauncher {
 }  // namespace
 
 uint32_t balance_blocks(uint64_t tokens, int experts) {
-  const uint64_t rows = kWaves * (experts <= 256 ? 4 : experts <= 512 ? 2 : 1);
+  const uint64_t rows = kLoadWaves * (experts <= 256 ? 4 : experts <= 512 ? 2 : 1);
   const uint64_t want = (tokens + rows - 1) / rows;
   return (uint32_t)(want < kBalanceMaxBlocks ? want : kBalanceMaxBlocks);
 }
@@ -316,7 +395,7 @@ hipError_t launch_balance_load(const BalanceArgs& a, bool bf16, hipStream_t stre
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(balance_join_kernel, dim3((a.experts + 63) / 64), dim3(64 * kJoinWaves), 0, stream, a);
+  hipLaunchKernelGGL(balance_join_kernel, dim3((a.experts + 15) / 16), dim3(64 * kJoinWaves), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -263,7 +263,7 @@ struct BalanceArgs {
   uint64_t ld_d;  // elements
   int32_t accumulate;
 };
-constexpr uint32_t kBalanceMaxBlocks = 512;
+constexpr uint32_t kBalanceMaxBlocks = 256;
 uint32_t balance_blocks(uint64_t tokens, int experts);
 hipError_t launch_balance_load(const BalanceArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_balance_loss(const float* load, int experts, float coefficient, float* loss, hipStream_t stream);

@@ -306,7 +306,7 @@ size_t snac_layer_norm_scratch(size_t tokens, size_t width, snac_dtype dtype);
  * and the ids[tokens][topk] that snac_route chose.  Of the router, experts, topk
  * and score are used.  The sums over tokens are binary64.  An AllReduce of
  * `load` gives the ranks' common load.  tokens * topk at most SNAC_MAX_IDS.
- * Scratch is the context's staging rings, 12 bytes * experts * 512 at most;
+ * Scratch is the context's staging rings, 12 bytes * experts * 256 at most;
  * SNAC_E_ARG if they are smaller.
  */
 snac_status snac_balance_load(snac_ctx* ctx, const snac_router* router, const void* logits, size_t ld,

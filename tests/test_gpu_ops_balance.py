@@ -9,10 +9,12 @@ share p is off by p (r + sum p r + 1) u.
   load     counts exact; the sum of the shares' errors over the tokens, a
            rounding of the sum
   loss     of the load that the call got: a rounding
-  dlogits  p (a - sum p a) with a less its mean: the share's error times the
-           last factor, p times the errors of p in the sum and a rounding of a,
-           2 roundings more, (9 + 5 |x|) u for the sigmoid's slope, and half a
-           step; accumulated: a rounding of the sum more
+  dlogits  p (a - sum p a) with a less that of the row's best expert (exact: a
+           difference of counts): the share's error times the last factor, p
+           times the errors of p in the sum and 12 u of the sum's terms (4 fused
+           multiply-adds, 2 additions, 6 over the lanes), its rounding and the
+           difference's, 4 roundings more, (9 + 5 |x|) u for the sigmoid's slope,
+           and half a step; accumulated: a rounding of the sum more
 """
 from __future__ import annotations
 
@@ -114,11 +116,13 @@ def test_both_ways(torch, ops, handle, dtype, score, tokens, experts, topk):
 
     dloss = torch.full((1,), 1.5, device="cuda")
     slope = ref.balance_slope(got, np.float32(COEFFICIENT), 1.5)
-    a = slope - slope.mean()
+    finite = np.where(np.isnan(hx), -np.inf, hx)
+    best = np.where(finite == finite.max(axis=1, keepdims=True), slope, -np.inf).max(axis=1, keepdims=True)
+    a = slope - best
     want = ref.balance_backward(hx, hi, got, score, np.float32(COEFFICIENT), 1.5)
     dot = (p * a).sum(axis=1, keepdims=True)
-    err = off * np.abs(a - dot) + p * ((off * np.abs(a)).sum(axis=1, keepdims=True) + (p * np.abs(a)).sum(axis=1, keepdims=True)
-                                       + np.abs(a)) + 3 * np.abs(want)
+    err = off * np.abs(a - dot) + p * ((off * np.abs(a)).sum(axis=1, keepdims=True)
+                                       + 13 * (p * np.abs(a)).sum(axis=1, keepdims=True) + np.abs(a - dot)) + 4 * np.abs(want)
     if score == "sigmoid":
         err = err + np.abs(want) * (9 + 5 * np.abs(np.where(np.isinf(hx), 0, hx)))
     err = U * err * some + TINY
