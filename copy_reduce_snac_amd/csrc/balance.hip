@@ -95,23 +95,37 @@ template <int L, int V, bool FAR>
 __device__ __forceinline__ double shares(bool softmax, float top, float (&x)[V], float (&far)[FAR ? V : 1]) {
   double total = 0.0;
   if (softmax) {
+    asm volatile("");  // a branch, and not both sides and a choice
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       x[j] = __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
       total += x[j];
     }
   } else {
+    asm volatile("");
     const float m = fminf(top, 0.0f);
     const bool low = __any(m < 0.0f);
+    constexpr int P = V < 8 ? V : 8;  // at a time: more would cost registers
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float a = __builtin_amdgcn_exp2f(-fabsf(x[j]) * kLog2e);
-      const float r = __builtin_amdgcn_rcpf(1.0f + a);
-      float up = x[j] < 0.0f ? a : 1.0f;
-      if (low && m < 0.0f) up = __builtin_amdgcn_exp2f((x[j] - m) * kLog2e);
-      if constexpr (FAR) far[j] = (x[j] < 0.0f ? 1.0f : a) * r;
-      x[j] = up * r;
-      total += x[j];
+    for (int j0 = 0; j0 < V; j0 += P) {
+      float up[P], r[P];
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const float a = __builtin_amdgcn_exp2f(-fabsf(x[j0 + j]) * kLog2e);
+        r[j] = __builtin_amdgcn_rcpf(1.0f + a);
+        if constexpr (FAR) far[j0 + j] = (x[j0 + j] < 0.0f ? 1.0f : a) * r[j];
+        up[j] = x[j0 + j] < 0.0f ? a : 1.0f;
+      }
+      if (low) {
+        asm volatile("");
+#pragma unroll
+        for (int j = 0; j < P; ++j) up[j] = m < 0.0f ? __builtin_amdgcn_exp2f((x[j0 + j] - m) * kLog2e) : up[j];
+      }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        x[j0 + j] = up[j] * r[j];
+        total += x[j0 + j];
+      }
     }
   }
   total = lanes_sum<L>(total);

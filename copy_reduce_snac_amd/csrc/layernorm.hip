@@ -581,7 +581,8 @@ void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
   constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W;
   const uint32_t row = (a.width * T::kSize + 1023) / 1024 * G;
   uint32_t per = G * (row > 16 ? 4 : row > 1 ? (32 + row - 1) / row : 32);
-  while (per > G && (a.tokens + per - 1) / per < cus() * 4) per /= 2;
+  const uint64_t fill = (uint64_t)cus() * 4;
+  while (per > G && (a.tokens + per - 1) / per < fill) per /= 2;
   const uint64_t most = (uint64_t)per << 22;  // rows of a launch
   LayerNormArgs c = a;
   for (uint64_t t = 0; t < a.tokens; t += most) {

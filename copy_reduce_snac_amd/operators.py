@@ -336,20 +336,23 @@ def clip_grad_norm(grads: GradList, max_norm: float, norm, stream=None) -> None:
     snac_clip_grad_norm(grads.handle, max_norm, norm, _stream(stream, on))
 
 
-def _vector(t, width: int, what: str) -> str:
-    if t.shape != (width,):
-        raise ValueError(f"{what} must have shape {(width,)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return _float(t, what)
+# the calls below build their messages where they raise: a formatted string takes
+# as long as the check that it is for
+def _vector(t, shape, what: str, name: str) -> str:
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _FLOAT.get(t.dtype) or _float(t, f"{what}: {name}")
 
 
-def _vectors(a, b, width: int, what: str, names) -> str:
+def _vectors(a, b, width: int, what: str, name_a: str, name_b: str) -> str:
     """The common type of two vectors that may be None (float32 where both are)."""
-    types = [_vector(t, width, f"{what}: {n}") for t, n in zip((a, b), names) if t is not None]
-    if len(types) == 2:
-        _pair(a, b, f"{what}: {names[0]} and {names[1]}")
-    return types[0] if types else "f32"
+    dt = None if a is None else _vector(a, (width,), what, name_a)
+    if b is None:
+        return dt or "f32"
+    dt_b = _vector(b, (width,), what, name_b)
+    if dt is not None and dt != dt_b:
+        raise TypeError(f"{what}: {name_a} and {name_b} must have the same dtype, not {a.dtype} and {b.dtype}")
+    return dt_b
 
 
 def layer_norm(x, weight, bias, out, *, eps: float = 1e-5, stats=None, stream=None) -> None:
@@ -363,7 +366,7 @@ def layer_norm(x, weight, bias, out, *, eps: float = 1e-5, stats=None, stream=No
     t, w = x.shape
     if out.shape != x.shape:
         raise ValueError("layer_norm: out must have the shape of x")
-    pt = _vectors(weight, bias, w, "layer_norm", ("weight", "bias"))
+    pt = _vectors(weight, bias, w, "layer_norm", "weight", "bias")
     if stats is not None:
         _packed(stats, (t, 2), torch.float32, "layer_norm: stats")
     on = _device("layer_norm", x, weight, bias, out, stats)
@@ -378,15 +381,16 @@ def layer_norm_backward(dout, x, weight, stats, dx, dweight, dbias, handle=None,
     context of ``snac_init`` whose staging rings hold
     ``snac_layer_norm_scratch`` bytes; without dweight and dbias rows of up to
     32 KiB need none."""
-    ld_g, ld_x, ld_dx = (_matrix(m, "layer_norm_backward: " + n) for m, n in ((dout, "dout"), (x, "x"), (dx, "dx")))
+    ld_g, ld_x = _matrix(dout, "layer_norm_backward: dout"), _matrix(x, "layer_norm_backward: x")
+    ld_dx = _matrix(dx, "layer_norm_backward: dx")
     dt = _float(x, "layer_norm_backward: x")
     _pair(x, dout, "layer_norm_backward: x and dout")
     _pair(x, dx, "layer_norm_backward: x and dx")
     t, w = x.shape
     if dout.shape != x.shape or dx.shape != x.shape:
         raise ValueError("layer_norm_backward: dout and dx must have the shape of x")
-    pt = _vectors(weight, None, w, "layer_norm_backward", ("weight", ""))
-    gt = _vectors(dweight, dbias, w, "layer_norm_backward", ("dweight", "dbias"))
+    pt = _vectors(weight, None, w, "layer_norm_backward", "weight", "")
+    gt = _vectors(dweight, dbias, w, "layer_norm_backward", "dweight", "dbias")
     _packed(stats, (t, 2), torch.float32, "layer_norm_backward: stats")
     on = _device("layer_norm_backward", dout, x, weight, stats, dx, dweight, dbias)
     snac_layer_norm_backward(handle, dout, ld_g, x, ld_x, weight, pt, stats, t, w, dt, dx, ld_dx, dweight, dbias, gt,
@@ -395,14 +399,14 @@ def layer_norm_backward(dout, x, weight, stats, dx, dweight, dbias, handle=None,
 
 def _chosen(logits, ids, what: str):
     """Row stride, type, tokens, experts and choices of a router's logits and ids."""
-    ld = _matrix(logits, f"{what}: logits")
-    dt = _float(logits, f"{what}: logits")
+    ld = _matrix(logits, what)
+    dt = _FLOAT.get(logits.dtype) or _float(logits, f"{what}: logits")
     t, e = logits.shape
-    if ids.dim() != 2:
-        raise ValueError(f"{what}: ids must have two dimensions")
-    k = ids.shape[1]
-    _packed(ids, (t, k), torch.int32, f"{what}: ids")
-    return ld, dt, t, e, k
+    if ids.dim() != 2 or ids.shape[0] != t or not ids.is_contiguous():
+        raise ValueError(f"{what}: ids must be contiguous with shape [{t}, choices], not {tuple(ids.shape)}")
+    if ids.dtype != torch.int32:
+        raise TypeError(f"{what}: ids must be int32, not {ids.dtype}")
+    return ld, dt, t, e, ids.shape[1]
 
 
 def balance_load(logits, ids, load, handle, *, score: str = "softmax", stream=None) -> None:
@@ -450,16 +454,17 @@ def balance_backward(logits, ids, load, dlogits, *, score: str = "softmax", coef
 
 
 def _teacher(ids, logits, tokens: int, vocab: int, temperature: float, what: str):
-    size, dt = _ids(ids, f"{what}: ids"), _float(logits, f"{what}: teacher")
-    if ids.dim() != 2 or ids.shape[0] != tokens or logits.shape != ids.shape:
+    size = _ID.get(ids.dtype) or _ids(ids, f"{what}: ids")
+    dt = _FLOAT.get(logits.dtype) or _float(logits, f"{what}: teacher")
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != tokens or logits.shape != shape:
         raise ValueError(f"{what}: ids and teacher must have shape [{tokens}, choices], not {tuple(ids.shape)} and "
                          f"{tuple(logits.shape)}")
     if not (ids.is_contiguous() and logits.is_contiguous()):
         raise ValueError(f"{what}: ids and teacher must be contiguous")
-    k = ids.shape[1]
-    if not 1 <= k <= SNAC_MAX_TEACHER:
-        raise ValueError(f"{what}: {k} choices outside 1..{SNAC_MAX_TEACHER}")
-    return teacher_of(ids, size, logits, dt, k, vocab, temperature)
+    if not 1 <= shape[1] <= SNAC_MAX_TEACHER:
+        raise ValueError(f"{what}: {shape[1]} choices outside 1..{SNAC_MAX_TEACHER}")
+    return teacher_of(ids, size, logits, dt, shape[1], vocab, temperature)
 
 
 def distill(logits, ids, teacher, loss, stats, *, temperature: float = 1.0, stream=None) -> None:
