@@ -80,12 +80,12 @@ __device__ __forceinline__ F few_lanes_sum(F x) {
   return x;
 }
 
-// Sums of a and b over the W waves of a row (`lds`: room for two numbers of each
+// Sums of a and b over the L lanes or the W waves of a row (`lds`: room for two numbers of each
 // of the workgroup's waves, not used by the call before), in every lane.
-template <int W, int NW>
+template <int L, int W>
 __device__ __forceinline__ void row_sum(double& a, double& b, double (*lds)[2]) {
-  a = wave_sum(a);
-  b = wave_sum(b);
+  a = lanes_sum<L>(a);
+  b = lanes_sum<L>(b);
   if constexpr (W > 1) {
     const uint32_t lane = threadIdx.x & 63u, w = wave_id(), w0 = w / W * W;
     if (lane == 0) lds[w][0] = a, lds[w][1] = b;
@@ -94,9 +94,9 @@ __device__ __forceinline__ void row_sum(double& a, double& b, double (*lds)[2]) 
     b = few_lanes_sum<W>(lds[w0 + lane % W][1]);
   }
 }
-template <int W, int NW>
+template <int L, int W>
 __device__ __forceinline__ float row_sum(float a, float* lds) {
-  a = wave_sum(a);
+  a = lanes_sum<L>(a);
   if constexpr (W > 1) {
     const uint32_t lane = threadIdx.x & 63u, w = wave_id(), w0 = w / W * W;
     if (lane == 0) lds[w] = a;
@@ -131,6 +131,22 @@ __device__ __forceinline__ float unit_dot(const float (&x)[N], const float (&y)[
   return s;
 }
 
+// Unit `l` of a row of `width` elements, which may have a part of it or none.
+template <typename T>
+__device__ __forceinline__ u32x4 ld_lane(const char* row, uint32_t l, uint32_t width) {
+  const uint32_t units = width / kUnit<T>, rest = width % kUnit<T>;
+  u32x4 v = {0, 0, 0, 0};
+  if (l < units) v = ld_unit<false>(row + l * 16u);
+  if (rest != 0 && l == units) v = ld_rest<T>(row + units * 16u, rest);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void st_lane(char* row, uint32_t l, uint32_t width, u32x4 v) {
+  const uint32_t units = width / kUnit<T>, rest = width % kUnit<T>;
+  if (l < units) st_unit<true>(row + l * 16u, v);
+  if (rest != 0 && l == units) st_rest<T>(row + units * 16u, v, rest);
+}
+
 // ------------------------------------------------------------------ forward
 
 // What a row's sums give.  The mean `near` of the first pass is binary32
@@ -149,26 +165,27 @@ struct Moments {
 
 constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 
-// W waves a row, U units a lane: the row stays in registers, so that it is read
-// once although its mean is needed before its variance and that before the
-// result.
-template <typename T, typename P, int W, int U>
+// L lanes of one wave a row (L < 64: W and U are 1), or W waves of U units a lane:
+// the row stays in registers, so that it is read once although its mean is needed
+// before its variance and that before the result.
+template <typename T, typename P, int L, int W, int U>
 __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_norm_kernel(const LayerNormArgs a,
                                                                                                      const uint32_t per) {
-  constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W;
+  constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W * (64 / L);
   constexpr uint32_t N = kUnit<T>;
   __shared__ float first_sums[NW];
   __shared__ double lds[NW][2];
-  const uint32_t lane = threadIdx.x & 63u, w = wave_id(), g = w / W;
-  const uint32_t first = (w % W) * 64u * U * N;  // the wave's piece of a row
+  const uint32_t l = threadIdx.x % L, w = wave_id();
+  const uint32_t g = L < 64 ? threadIdx.x / L : w / W;  // the row of those side by side
+  const uint32_t first = (w % W) * 64u * U * N * (L == 64);  // the wave's piece of it
   const uint32_t left = first < a.width ? a.width - first : 0;
-  const bool whole = whole_piece<T, U>(left);
+  const bool whole = left >= L * U * N;
   // the parameters are kept, and the next row is loaded while this one is worked
   // on, where registers allow it
   constexpr bool kAhead = W * U < 64;
   Params<T, P> weight[U], bias[U];
   auto params = [&](int j) {
-    const uint32_t e = first + (j * 64u + lane) * N;
+    const uint32_t e = first + (j * L + l) * N;
     const char *pw = a.weight, *pb = a.bias;
     // opaque here, so that they are not loaded before the loop after all
     if constexpr (!kAhead) asm volatile("" : "+s"(pw), "+s"(pb));
@@ -189,7 +206,8 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
   auto load = [&](uint64_t row) {
     if (row >= end) return;
     const char* x = a.x + row * a.ld_x + (uint64_t)first * T::kSize;
-    if (lines) ld_held<T, U, true>(x, left, next);
+    if constexpr (L < 64) next[0] = ld_lane<T>(x, l, a.width);
+    else if (lines) ld_held<T, U, true>(x, left, next);
     else ld_held<T, U, false>(x, left, next);
   };
   if constexpr (kAhead) load(t0 + g);
@@ -207,7 +225,7 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
       unpack<T>(v[j], f[j]);
       sum += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
     }
-    const float near = row_sum<W, NW>(sum, first_sums) * inv_f;
+    const float near = row_sum<L, W>(sum, first_sums) * inv_f;
 #pragma unroll
     for (int j = 0; j < U; ++j)
 #pragma unroll
@@ -217,7 +235,7 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
       for (int j = 0; j < U; ++j)
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c)
-          if ((j * 64u + lane) * N + c >= left) f[j][c] = 0.0f;
+          if ((j * L + l) * N + c >= left) f[j][c] = 0.0f;
     }
     double sd = 0.0, sq = 0.0;
 #pragma unroll
@@ -225,7 +243,7 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
       sd += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
       sq += unit_dot<N>(f[j], f[j]);
     }
-    row_sum<W, NW>(sd, sq, lds);
+    row_sum<L, W>(sd, sq, lds);
     const Moments m(near, sd * inv, sq * inv, a.eps);
     if (t < end) {
 #pragma unroll
@@ -239,8 +257,10 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
           f[j][c] = __builtin_fmaf(__builtin_fmaf(f[j][c], m.rstd, m.shift), param<T, P>(weight[j], c), param<T, P>(bias[j], c));
         v[j] = pack<T>(f[j]);
       }
-      st_held<T, U, true>(a.out + t * a.ld_out + (uint64_t)first * T::kSize, left, v);
-      if (a.stats && w % W == 0 && lane == 0) {
+      char* out = a.out + t * a.ld_out + (uint64_t)first * T::kSize;
+      if constexpr (L < 64) st_lane<T>(out, l, a.width, v[0]);
+      else st_held<T, U, true>(out, left, v);
+      if (a.stats && w % W == 0 && l == 0) {
         a.stats[2 * t] = m.mean;
         a.stats[2 * t + 1] = m.rstd;
       }
@@ -272,14 +292,14 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
     };
     double sum = 0.0, sd = 0.0, sq = 0.0;
     row([&](uint32_t, uint32_t, float (&u)[N]) { sum += unit_sum<N>([&](uint32_t c) { return u[c]; }); });
-    const float near = row_sum<NW, NW>((float)sum, first_sums) * (float)inv;
+    const float near = row_sum<64, NW>((float)sum, first_sums) * (float)inv;
     row([&](uint32_t, uint32_t left, float (&u)[N]) {
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c) u[c] = lane * N + c < left ? u[c] - near : 0.0f;
       sd += unit_sum<N>([&](uint32_t c) { return u[c]; });
       sq += unit_dot<N>(u, u);
     });
-    row_sum<NW, NW>(sd, sq, lds);
+    row_sum<64, NW>(sd, sq, lds);
     const Moments m(near, sd * inv, sq * inv, a.eps);
     row([&](uint32_t e0, uint32_t left, float (&u)[N]) {
       Params<T, P> weight, bias;
@@ -319,24 +339,25 @@ __device__ __forceinline__ void st_sums(float* p, uint32_t left, const float (&f
   }
 }
 
-// W waves a row, U units a lane, G rows at a time; the sums over tokens stay in
+// L lanes of one wave a row (L < 64: W and U are 1), or W waves of U units a lane; the sums over tokens stay in
 // registers and leave as one partial sum a workgroup.
-template <typename T, typename P, int W, int U>
+template <typename T, typename P, int L, int W, int U>
 __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     const LayerNormBackwardArgs a) {
-  constexpr int NW = kGradWaves, G = NW / W;
+  constexpr int NW = kGradWaves, Q = NW / W, G = Q * (64 / L);
   constexpr uint32_t N = kUnit<T>, kPiece = 64u * U * N;
   __shared__ double lds[2][NW][2];
-  __shared__ __align__(16) float join[G > 1 ? G / 2 * W : 1][2][G > 1 ? kPiece : 1];
-  const uint32_t lane = threadIdx.x & 63u, w = wave_id(), g = w / W;
-  const uint32_t first = (w % W) * kPiece;
+  __shared__ __align__(16) float join[Q > 1 ? Q / 2 * W : 1][2][Q > 1 ? kPiece : 1];
+  const uint32_t lane = threadIdx.x & 63u, l = lane % L, w = wave_id(), q = w / W;
+  const uint32_t g = L < 64 ? threadIdx.x / L : q;  // the row of those side by side
+  const uint32_t first = (w % W) * kPiece * (L == 64);
   const uint32_t left = first < a.width ? a.width - first : 0;
   const uint64_t off = (uint64_t)first * T::kSize;
-  const bool whole = whole_piece<T, U>(left);
+  const bool whole = left >= L * U * N;
   Params<T, P> weight[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    if (a.weight) ld_params<T, P>(a.weight, first + (j * 64u + lane) * N, a.width, weight[j]);
+    if (a.weight) ld_params<T, P>(a.weight, first + (j * L + l) * N, a.width, weight[j]);
     else fill_params<T, P>(1.0f, weight[j]);
   }
   float dw[U][N], db[U][N];
@@ -349,7 +370,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   u32x4 next_x[U] = {}, next_g[U] = {};
   auto load = [&](uint64_t t) {
     if (t >= a.tokens) return;
-    if (lines) {
+    if constexpr (L < 64) {
+      next_x[0] = ld_lane<T>(a.x + t * a.ld_x, l, a.width);
+      next_g[0] = ld_lane<T>(a.dout + t * a.ld_dout, l, a.width);
+    } else if (lines) {
       ld_held<T, U, true>(a.x + t * a.ld_x + off, left, next_x);
       ld_held<T, U, true>(a.dout + t * a.ld_dout + off, left, next_g);
     } else {
@@ -383,7 +407,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
         for (int j = 0; j < U; ++j)
 #pragma unroll
           for (uint32_t c = 0; c < N; ++c)
-            if ((j * 64u + lane) * N + c >= left) h[j][c] = 0.0f;
+            if ((j * L + l) * N + c >= left) h[j][c] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -399,8 +423,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
         c2 += unit_dot<N>(up[j], h[j]);
       }
     }
-    row_sum<W, NW>(c1, c2, lds[turn]);
-    if (!live) continue;
+    row_sum<L, W>(c1, c2, lds[turn]);
     const float m1 = (float)c1 * inv, m2 = (float)c2 * inv;
     u32x4 v[U];
 #pragma unroll
@@ -409,15 +432,26 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
       for (uint32_t c = 0; c < N; ++c) h[j][c] = rstd * __builtin_fmaf(-h[j][c], m2, up[j][c] - m1);
       v[j] = pack<T>(h[j]);
     }
-    st_held<T, U, true>(a.dx + t * a.ld_dx + off, left, v);
+    if (live) {
+      if constexpr (L < 64) st_lane<T>(a.dx + t * a.ld_dx, l, a.width, v[0]);
+      else st_held<T, U, true>(a.dx + t * a.ld_dx + off, left, v);
+    }
   }
   if (!a.partial) return;
-  // the rows that went beside each other: the upper half of them to the lower
-  if constexpr (G > 1) {
+  // the rows that went side by side: those of a wave, then the upper half of the
+  // waves to the lower
+  if constexpr (L < 64) {
 #pragma unroll
-    for (uint32_t half = G / 2; half > 0; half /= 2) {
+    for (uint32_t c = 0; c < N; ++c) {
+      if constexpr (L == 16) dw[0][c] = exchange_sum<16>(dw[0][c]), db[0][c] = exchange_sum<16>(db[0][c]);
+      dw[0][c] = exchange_sum<32>(dw[0][c]), db[0][c] = exchange_sum<32>(db[0][c]);
+    }
+  }
+  if constexpr (Q > 1) {
+#pragma unroll
+    for (uint32_t half = Q / 2; half > 0; half /= 2) {
       __syncthreads();
-      if (g >= half && g < 2 * half) {
+      if (q >= half && q < 2 * half) {
         float(&to)[2][kPiece] = join[w - half * W];
 #pragma unroll
         for (int j = 0; j < U; ++j)
@@ -432,28 +466,28 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
           }
       }
       __syncthreads();
-      if (g < half) {
+      if (q < half) {
         const float(&from)[2][kPiece] = join[w];
 #pragma unroll
         for (int j = 0; j < U; ++j)
 #pragma unroll
           for (uint32_t c = 0; c < N; c += 4) {
-            const u32x4 p = *reinterpret_cast<const u32x4*>(&from[0][(j * N + c) * 64 + lane * 4]);
-            const u32x4 q = *reinterpret_cast<const u32x4*>(&from[1][(j * N + c) * 64 + lane * 4]);
+            const u32x4 vw = *reinterpret_cast<const u32x4*>(&from[0][(j * N + c) * 64 + lane * 4]);
+            const u32x4 vb = *reinterpret_cast<const u32x4*>(&from[1][(j * N + c) * 64 + lane * 4]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              dw[j][c + i] += __uint_as_float(p[i]);
-              db[j][c + i] += __uint_as_float(q[i]);
+              dw[j][c + i] += __uint_as_float(vw[i]);
+              db[j][c + i] += __uint_as_float(vb[i]);
             }
           }
       }
     }
   }
-  if (g != 0) return;
+  if (q != 0 || l != lane) return;
   float* part = a.partial + (uint64_t)blockIdx.x * 2 * a.width;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    const uint32_t e = first + (j * 64u + lane) * N;
+    const uint32_t e = first + (j * L + l) * N;
     if (e >= a.width) continue;
     st_sums<N>(part + e, a.width - e, dw[j]);
     st_sums<N>(part + a.width + e, a.width - e, db[j]);
@@ -489,7 +523,7 @@ __global__ __launch_bounds__(1024) void layer_norm_row_sums_kernel(const LayerNo
       c1 += unit_sum<N>([&](uint32_t c) { return up[c]; });
       c2 += unit_sum<N>([&](uint32_t c) { return up[c] * h[c]; });
     }
-    row_sum<NW, NW>(c1, c2, lds);
+    row_sum<64, NW>(c1, c2, lds);
     if (threadIdx.x == 0) {
       a.row_sums[2 * t] = (float)(c1 / (double)a.width);
       a.row_sums[2 * t + 1] = (float)(c2 / (double)a.width);
@@ -576,11 +610,11 @@ uint32_t cus() {
 
 // The rows of a workgroup, one after another: its parameters are loaded once for
 // them.
-template <typename T, typename P, int W, int U>
+template <typename T, typename P, int L, int W, int U>
 void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
-  constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W;
-  const uint32_t row = (a.width * T::kSize + 1023) / 1024 * G;
-  uint32_t per = G * (row > 16 ? 4 : row > 1 ? (32 + row - 1) / row : 32);
+  constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W * (64 / L);
+  const uint32_t kib = (a.width * T::kSize * G + 1023) / 1024;  // of the rows side by side
+  uint32_t per = G * (kib > 16 ? 4 : (32 + kib - 1) / kib);
   const uint64_t fill = (uint64_t)cus() * 4;
   while (per > G && (a.tokens + per - 1) / per < fill) per /= 2;
   const uint64_t most = (uint64_t)per << 22;  // rows of a launch
@@ -590,7 +624,7 @@ void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
     c.x = a.x + t * a.ld_x;
     c.out = a.out + t * a.ld_out;
     c.stats = a.stats ? a.stats + 2 * t : nullptr;
-    hipLaunchKernelGGL((layer_norm_kernel<T, P, W, U>), dim3((uint32_t)((c.tokens + per - 1) / per)), dim3(64 * NW), 0,
+    hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U>), dim3((uint32_t)((c.tokens + per - 1) / per)), dim3(64 * NW), 0,
                        stream, c, per);
   }
 }
@@ -598,15 +632,17 @@ void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
 // The narrowest shape that holds a row, in units of 1 KiB (64 lanes).
 template <typename T, typename P>
 void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
-  const uint64_t kib = ((uint64_t)a.width * T::kSize + 1023) / 1024;
-  if (kib <= 1) layer_norm_in<T, P, 1, 1>(a, stream);
-  else if (kib <= 2) layer_norm_in<T, P, 1, 2>(a, stream);
-  else if (kib <= 4) layer_norm_in<T, P, 1, 4>(a, stream);
-  else if (kib <= 8) layer_norm_in<T, P, 4, 2>(a, stream);
-  else if (kib <= 16) layer_norm_in<T, P, 4, 4>(a, stream);
-  else if (kib <= 32) layer_norm_in<T, P, 8, 4>(a, stream);
+  const uint64_t bytes = (uint64_t)a.width * T::kSize, kib = (bytes + 1023) / 1024;
+  if (bytes <= 256) layer_norm_in<T, P, 16, 1, 1>(a, stream);
+  else if (bytes <= 512) layer_norm_in<T, P, 32, 1, 1>(a, stream);
+  else if (kib <= 1) layer_norm_in<T, P, 64, 1, 1>(a, stream);
+  else if (kib <= 2) layer_norm_in<T, P, 64, 1, 2>(a, stream);
+  else if (kib <= 4) layer_norm_in<T, P, 64, 1, 4>(a, stream);
+  else if (kib <= 8) layer_norm_in<T, P, 64, 4, 2>(a, stream);
+  else if (kib <= 16) layer_norm_in<T, P, 64, 4, 4>(a, stream);
+  else if (kib <= 32) layer_norm_in<T, P, 64, 8, 4>(a, stream);
   else if (kib <= kHeldKib<T, P>) {
-    if constexpr (kHeldKib<T, P> > 32) layer_norm_in<T, P, 16, 4>(a, stream);
+    if constexpr (kHeldKib<T, P> > 32) layer_norm_in<T, P, 64, 16, 4>(a, stream);
   } else {
     const uint64_t most = (uint64_t)cus() * 2;
     hipLaunchKernelGGL((layer_norm_wide_kernel<T, P>), dim3((uint32_t)(a.tokens < most ? a.tokens : most)), dim3(1024),
@@ -614,14 +650,14 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   }
 }
 
-template <typename T, typename P, int W, int U>
+template <typename T, typename P, int L, int W, int U>
 void layer_norm_backward_in(const LayerNormBackwardArgs& a, const LayerNormShape& s, hipStream_t stream) {
-  hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, W, U>), dim3(s.blocks), dim3(64 * kGradWaves), 0, stream, a);
+  hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U>), dim3(s.blocks), dim3(64 * kGradWaves), 0, stream, a);
 }
 
 template <typename T, typename P>
 void layer_norm_backward_any(const LayerNormBackwardArgs& a, const LayerNormShape& s, hipStream_t stream) {
-  const uint64_t kib = ((uint64_t)a.width * T::kSize + 1023) / 1024;
+  const uint64_t bytes = (uint64_t)a.width * T::kSize, kib = (bytes + 1023) / 1024;
   if (s.row_sums) {
     const uint64_t most = (uint64_t)cus() * 2;
     hipLaunchKernelGGL((layer_norm_row_sums_kernel<T, P>), dim3((uint32_t)(a.tokens < most ? a.tokens : most)),
@@ -629,12 +665,14 @@ void layer_norm_backward_any(const LayerNormBackwardArgs& a, const LayerNormShap
     const uint32_t y = s.blocks < 32768 ? s.blocks : 32768;
     hipLaunchKernelGGL((layer_norm_columns_kernel<T, P>), dim3((uint32_t)((kib + 3) / 4), y), dim3(256), 0, stream, a,
                        s.per);
-  } else if (kib <= 1) layer_norm_backward_in<T, P, 1, 1>(a, s, stream);
-  else if (kib <= 2) layer_norm_backward_in<T, P, 1, 2>(a, s, stream);
-  else if (kib <= 4) layer_norm_backward_in<T, P, 2, 2>(a, s, stream);
-  else if (kib <= 8) layer_norm_backward_in<T, P, 4, 2>(a, s, stream);
-  else if (kib <= 16) layer_norm_backward_in<T, P, 8, 2>(a, s, stream);
-  else layer_norm_backward_in<T, P, 16, 2>(a, s, stream);
+  } else if (bytes <= 256) layer_norm_backward_in<T, P, 16, 1, 1>(a, s, stream);
+  else if (bytes <= 512) layer_norm_backward_in<T, P, 32, 1, 1>(a, s, stream);
+  else if (kib <= 1) layer_norm_backward_in<T, P, 64, 1, 1>(a, s, stream);
+  else if (kib <= 2) layer_norm_backward_in<T, P, 64, 1, 2>(a, s, stream);
+  else if (kib <= 4) layer_norm_backward_in<T, P, 64, 2, 2>(a, s, stream);
+  else if (kib <= 8) layer_norm_backward_in<T, P, 64, 4, 2>(a, s, stream);
+  else if (kib <= 16) layer_norm_backward_in<T, P, 64, 8, 2>(a, s, stream);
+  else layer_norm_backward_in<T, P, 64, 16, 2>(a, s, stream);
 }
 
 }  // namespace
@@ -654,7 +692,7 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
   const uint64_t kib = (bytes + 1023) / 1024;
   uint64_t rows = 1, most = kGradBlocks;
   if (s.row_sums) most = kGradBlocks * 16 / kib + 1;
-  else rows = kib <= 2 ? 16 : kib <= 4 ? 8 : kib <= 8 ? 4 : kib <= 16 ? 2 : 1;
+  else rows = bytes <= 256 ? 64 : bytes <= 512 ? 32 : kib <= 2 ? 16 : kib <= 4 ? 8 : kib <= 8 ? 4 : kib <= 16 ? 2 : 1;
   uint64_t turns = (tokens + rows * most - 1) / (rows * most);
   if (turns > kSumTokens) turns = kSumTokens;
   s.per = (uint32_t)(rows * turns);

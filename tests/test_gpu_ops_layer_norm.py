@@ -11,9 +11,9 @@ Bounds, u = 2^-24, h = (x - mean) rstd, half = half a step of the output's type:
           g h 14 u of the terms' mean sizes (sums of a unit 7, rounding,
           1 / width, product), three operations more:
           u rstd (4 |g| + 14 mean|g| + 20 |h| mean|g h|) + half |dx|
-  dweight 32 fused multiply-adds, 3 joinings and a rounding, h 2: 40 u of the
-          terms' sizes + half |dweight|; dbias likewise; accumulated ones with
-          what was there among the sizes
+  dweight 32 fused multiply-adds, 6 joinings of 64 rows side by side and a
+          rounding, h 2: 41 u of the terms' sizes + half |dweight|; dbias likewise;
+          accumulated ones with what was there among the sizes
 """
 from __future__ import annotations
 
@@ -89,7 +89,7 @@ def out_bound(h, w, out, dtype):
 
 
 # every shape that is compiled, whole and not, and rows that go to the wide kernels
-WIDTHS = [1, 2, 3, 7, 8, 64, 100, 255, 256, 257, 511, 512, 513, 1000, 1024, 1030, 2047, 2048, 2049, 4096, 5003, 8192, 8200, 12001,
+WIDTHS = [1, 2, 3, 7, 8, 63, 64, 65, 100, 128, 129, 250, 255, 256, 257, 511, 512, 513, 1000, 1024, 1030, 2047, 2048, 2049, 4096, 5003, 8192, 8200, 12001,
           16384, 16385, 30000, 33000]
 
 
@@ -132,11 +132,11 @@ def test_both_ways(torch, ops, handle, dtype, params, width):
         near(dx, want_dx, U * hs[:, 1:] * (4 * np.abs(up) + 14 * mg + 20 * np.abs(h) * mgh) + HALF[dtype] * np.abs(want_dx) + TINY, "dx")
         old = 3.0 if accumulate else 0.0
         for got, sums, size in ((dw, want_dw, np.abs(hg * h).sum(axis=0)), (db, want_db, np.abs(hg).sum(axis=0))):
-            near(got[1:-1], sums + old, 40 * U * (size + old) + HALF[grad] * np.abs(sums + old), (grad, accumulate))
+            near(got[1:-1], sums + old, 41 * U * (size + old) + HALF[grad] * np.abs(sums + old), (grad, accumulate))
 
 
 @pytest.mark.parametrize("tokens", [1, 2, 31, 4096, 4097, 16500, 40001])
-@pytest.mark.parametrize("dtype,width", [("bf16", 40), ("f32", 260), ("bf16", 2050)])
+@pytest.mark.parametrize("dtype,width", [("bf16", 40), ("bf16", 200), ("f32", 260), ("bf16", 2050)])
 def test_many_tokens(torch, ops, handle, dtype, width, tokens):
     """Sums over many tokens are not off by more than over few; whole numbers come out whole."""
     if tokens * width > 1 << 25:
