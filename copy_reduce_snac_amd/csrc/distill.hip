@@ -136,8 +136,8 @@ __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(con
     u32x4 next[kUnits] = {};
     auto load = [&](uint32_t p) {
       const char* at = row + (uint64_t)p * kPiece * T::kSize;
-      if (lines) ld_held<T, kUnits, true>(at, a.width - p * kPiece, next);
-      else ld_held<T, kUnits, false>(at, a.width - p * kPiece, next);
+      if (lines) ld_held<T, kUnits, true, true>(at, a.width - p * kPiece, a.width, next);
+      else ld_held<T, kUnits, false, true>(at, a.width - p * kPiece, a.width, next);
     };
     if (w < pieces) load(w);
     Choices<C> k;
@@ -159,11 +159,12 @@ __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(con
     r.start();
     for (uint32_t p = w; p < pieces; p += W) {
       float f[kUnits][N];
+      const uint32_t left = a.width - p * kPiece;
 #pragma unroll
       for (int j = 0; j < kUnits; ++j) unpack<T>(next[j], f[j]);
-      const uint32_t left = a.width - p * kPiece;
       if (pieces - p > W) load(p + W);
       if (left < kPiece) {
+        settle_held<T, kUnits>(left, a.width, f);
 #pragma unroll
         for (int j = 0; j < kUnits; ++j)
 #pragma unroll
@@ -266,8 +267,8 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
     u32x4 next[kBackUnits];
     auto load = [&](uint32_t p) {
       const char* at = row + (uint64_t)p * kPiece * T::kSize;
-      if (lines) ld_held<T, kBackUnits, true>(at, a.width - p * kPiece, next);
-      else ld_held<T, kBackUnits, false>(at, a.width - p * kPiece, next);
+      if (lines) ld_held<T, kBackUnits, true, true>(at, a.width - p * kPiece, a.width, next);
+      else ld_held<T, kBackUnits, false, true>(at, a.width - p * kPiece, a.width, next);
     };
     if (p0 + w < p1) load(p0 + w);
     const float top = a.stats[2 * t], total = a.stats[2 * t + 1];
@@ -297,6 +298,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
       float f[kBackUnits][N];
 #pragma unroll
       for (int j = 0; j < kBackUnits; ++j) unpack<T>(next[j], f[j]);
+      if (left < kPiece) settle_held<T, kBackUnits>(left, a.width, f);
       if (p1 - p > kBackWaves) load(p + kBackWaves);
 #pragma unroll
       for (int j = 0; j < kBackUnits; ++j)
@@ -326,7 +328,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
       u32x4 v[kBackUnits];
 #pragma unroll
       for (int j = 0; j < kBackUnits; ++j) v[j] = part ? pack<T>(f[j]) : u32x4{0, 0, 0, 0};
-      st_held<T, kBackUnits, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
+      st_held<T, kBackUnits, true, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
     }
     if (items - it > gridDim.x) __syncthreads();  // the choices are read
   }

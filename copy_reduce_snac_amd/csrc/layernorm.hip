@@ -9,8 +9,8 @@ namespace snac {
 namespace {
 
 // The widest rows that a workgroup holds in registers: 16 waves of 64 lanes of 4
-// units, or 2 where wider parameters or the gradient's sums over tokens are held
-// too.
+// units (rows of whole units), or 2 where wider parameters or the gradient's sums
+// over tokens are held too.
 template <typename T, typename P>
 constexpr uint64_t kHeldKib = P::kSize > T::kSize ? 32 : 64;
 constexpr uint64_t kHeldBackwardKib = 32;
@@ -23,32 +23,53 @@ struct Params {
   uint32_t w[kWords];
 };
 
-// Parameters of the kUnit<T> elements from `e` on; those past `width` read as 0.
+// Parameters of the kUnit<T> elements from `e` on; those past `width` are 0 (or
+// what follows, where a lane has none).  A part of a unit is loaded as the
+// elements that end where the row does and moved down: element by element, each
+// waiting for the one before, it took 10 us of 46 for 8192 rows of 5003 bf16.
 template <typename T, typename P>
 __device__ __forceinline__ void ld_params(const char* p, uint32_t e, uint32_t width, Params<T, P>& r) {
   constexpr uint32_t N = kUnit<T>;
-  const char* at = p + (uint64_t)e * P::kSize;
+  constexpr int K = Params<T, P>::kWords;
 #pragma unroll
-  for (int c = 0; c < Params<T, P>::kWords; ++c) r.w[c] = 0;
-  if (e + N <= width) {
-    if constexpr (Params<T, P>::kWords == 2) {
-      const u32x2_a2 v = *(global_ptr<const u32x2_a2>)(at);
-      r.w[0] = v[0], r.w[1] = v[1];
-    } else {
-#pragma unroll
-      for (int u = 0; u < Params<T, P>::kWords / 4; ++u) {
-        const u32x4 v = ld_unit<false>(at + 16 * u);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) r.w[4 * u + c] = v[c];
-      }
-    }
-  } else {
+  for (int c = 0; c < K; ++c) r.w[c] = 0;
+  if (e >= width) return;
+  if (width < N) {
 #pragma unroll
     for (uint32_t i = 0; i < N; ++i) {
       if (e + i >= width) continue;
-      if constexpr (P::kSize == 4) r.w[i] = *(global_ptr<const uint32_t>)(at + 4 * i);
-      else r.w[i / 2] |= (uint32_t)*(global_ptr<const uint16_t>)(at + 2 * i) << (16 * (i & 1));
+      const char* at = p + (uint64_t)(e + i) * P::kSize;
+      if constexpr (P::kSize == 4) r.w[i] = *(global_ptr<const uint32_t>)(at);
+      else r.w[i / 2] |= (uint32_t)*(global_ptr<const uint16_t>)(at) << (16 * (i & 1));
     }
+    return;
+  }
+  const uint32_t first = e + N <= width ? 0 : e + N - width;
+  const char* at = p + (uint64_t)(e - first) * P::kSize;
+  if constexpr (K == 2) {
+    const u32x2_a2 v = *(global_ptr<const u32x2_a2>)(at);
+    r.w[0] = v[0], r.w[1] = v[1];
+  } else {
+#pragma unroll
+    for (int u = 0; u < K / 4; ++u) {
+      const u32x4 v = ld_unit<false>(at + 16 * u);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) r.w[4 * u + c] = v[c];
+    }
+  }
+  if (first != 0) {
+    const uint32_t words = first * P::kSize / 4;
+    uint32_t t[K];
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
+      t[c] = r.w[c];
+#pragma unroll
+      for (int q = 1; q < K; ++q)
+        if (words == (uint32_t)q) t[c] = c + q < K ? r.w[(c + q) % K] : 0u;
+    }
+    const bool half = P::kSize == 2 && (first & 1);
+#pragma unroll
+    for (int c = 0; c < K; ++c) r.w[c] = half ? t[c] >> 16 | (c + 1 < K ? t[(c + 1) % K] << 16 : 0u) : t[c];
   }
 }
 // All of them 1 (absent weights) or -0 (absent biases: x + -0 is x, also for -0).
@@ -131,18 +152,28 @@ __device__ __forceinline__ float unit_dot(const float (&x)[N], const float (&y)[
   return s;
 }
 
-// Unit `l` of a row of `width` elements, which may have a part of it or none.
-template <typename T>
+// Unit `l` of a row of `width` elements, which may have a part of it (REST, and
+// settled as in settle_held) or none.
+template <typename T, bool REST>
 __device__ __forceinline__ u32x4 ld_lane(const char* row, uint32_t l, uint32_t width) {
-  const uint32_t units = width / kUnit<T>, rest = width % kUnit<T>;
+  constexpr uint32_t N = kUnit<T>;
+  const uint32_t units = width / N, rest = REST ? width % N : 0;
   u32x4 v = {0, 0, 0, 0};
-  if (l < units) v = ld_unit<false>(row + l * 16u);
-  if (rest != 0 && l == units) v = ld_rest<T>(row + units * 16u, rest);
+  if (l < units + (rest != 0 && width >= N ? 1 : 0))
+    v = ld_unit<false>(l < units ? row + l * 16u : row + (uint64_t)width * T::kSize - 16);
+  if (REST && width < N && l == 0) v = ld_rest<T>(row, rest);
   return v;
 }
 template <typename T>
+__device__ __forceinline__ void settle_lane(uint32_t l, uint32_t width, u32x4& v) {
+  constexpr uint32_t N = kUnit<T>;
+  if (width % N == 0 || width < N) return;
+  const u32x4 r = later_elems<T>(v, N - width % N);
+  if (l == width / N) v = r;
+}
+template <typename T, bool REST>
 __device__ __forceinline__ void st_lane(char* row, uint32_t l, uint32_t width, u32x4 v) {
-  const uint32_t units = width / kUnit<T>, rest = width % kUnit<T>;
+  const uint32_t units = width / kUnit<T>, rest = REST ? width % kUnit<T> : 0;
   if (l < units) st_unit<true>(row + l * 16u, v);
   if (rest != 0 && l == units) st_rest<T>(row + units * 16u, v, rest);
 }
@@ -168,7 +199,7 @@ constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 // L lanes of one wave a row (L < 64: W and U are 1), or W waves of U units a lane:
 // the row stays in registers, so that it is read once although its mean is needed
 // before its variance and that before the result.
-template <typename T, typename P, int L, int W, int U>
+template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_norm_kernel(const LayerNormArgs a,
                                                                                                      const uint32_t per) {
   constexpr int NW = W > kNormWaves ? W : kNormWaves, G = NW / W * (64 / L);
@@ -206,9 +237,9 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
   auto load = [&](uint64_t row) {
     if (row >= end) return;
     const char* x = a.x + row * a.ld_x + (uint64_t)first * T::kSize;
-    if constexpr (L < 64) next[0] = ld_lane<T>(x, l, a.width);
-    else if (lines) ld_held<T, U, true>(x, left, next);
-    else ld_held<T, U, false>(x, left, next);
+    if constexpr (L < 64) next[0] = ld_lane<T, REST>(x, l, a.width);
+    else if (lines) ld_held<T, U, true, REST>(x, left, a.width, next);
+    else ld_held<T, U, false, REST>(x, left, a.width, next);
   };
   if constexpr (kAhead) load(t0 + g);
   // every wave of the workgroup goes round as often as its first
@@ -218,13 +249,16 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
     u32x4 v[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) v[j] = next[j];
+    if (REST && !whole) {
+      if constexpr (L < 64) settle_lane<T>(l, a.width, v[0]);
+      else settle_held<T, U>(left, a.width, v);
+    }
     if constexpr (kAhead) load(t + G);
     float f[U][N], sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      unpack<T>(v[j], f[j]);
-      sum += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
-    }
+    for (int j = 0; j < U; ++j) unpack<T>(v[j], f[j]);
+#pragma unroll
+    for (int j = 0; j < U; ++j) sum += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
     const float near = row_sum<L, W>(sum, first_sums) * inv_f;
 #pragma unroll
     for (int j = 0; j < U; ++j)
@@ -258,8 +292,8 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
         v[j] = pack<T>(f[j]);
       }
       char* out = a.out + t * a.ld_out + (uint64_t)first * T::kSize;
-      if constexpr (L < 64) st_lane<T>(out, l, a.width, v[0]);
-      else st_held<T, U, true>(out, left, v);
+      if constexpr (L < 64) st_lane<T, REST>(out, l, a.width, v[0]);
+      else st_held<T, U, true, REST>(out, left, v);
       if (a.stats && w % W == 0 && l == 0) {
         a.stats[2 * t] = m.mean;
         a.stats[2 * t + 1] = m.rstd;
@@ -341,7 +375,7 @@ __device__ __forceinline__ void st_sums(float* p, uint32_t left, const float (&f
 
 // L lanes of one wave a row (L < 64: W and U are 1), or W waves of U units a lane; the sums over tokens stay in
 // registers and leave as one partial sum a workgroup.
-template <typename T, typename P, int L, int W, int U>
+template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     const LayerNormBackwardArgs a) {
   constexpr int NW = kGradWaves, Q = NW / W, G = Q * (64 / L);
@@ -371,14 +405,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   auto load = [&](uint64_t t) {
     if (t >= a.tokens) return;
     if constexpr (L < 64) {
-      next_x[0] = ld_lane<T>(a.x + t * a.ld_x, l, a.width);
-      next_g[0] = ld_lane<T>(a.dout + t * a.ld_dout, l, a.width);
+      next_x[0] = ld_lane<T, REST>(a.x + t * a.ld_x, l, a.width);
+      next_g[0] = ld_lane<T, REST>(a.dout + t * a.ld_dout, l, a.width);
     } else if (lines) {
-      ld_held<T, U, true>(a.x + t * a.ld_x + off, left, next_x);
-      ld_held<T, U, true>(a.dout + t * a.ld_dout + off, left, next_g);
+      ld_held<T, U, true, REST>(a.x + t * a.ld_x + off, left, a.width, next_x);
+      ld_held<T, U, true, REST>(a.dout + t * a.ld_dout + off, left, a.width, next_g);
     } else {
-      ld_held<T, U, false>(a.x + t * a.ld_x + off, left, next_x);
-      ld_held<T, U, false>(a.dout + t * a.ld_dout + off, left, next_g);
+      ld_held<T, U, false, REST>(a.x + t * a.ld_x + off, left, a.width, next_x);
+      ld_held<T, U, false, REST>(a.dout + t * a.ld_dout + off, left, a.width, next_g);
     }
   };
   // rows of all workgroups' same turn lie side by side
@@ -389,6 +423,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     const uint64_t t = s + g;
     const bool live = t < a.tokens;
     float h[U][N], up[U][N];
+    if (REST && !whole) {
+      if constexpr (L < 64) settle_lane<T>(l, a.width, next_x[0]), settle_lane<T>(l, a.width, next_g[0]);
+      else settle_held<T, U>(left, a.width, next_x), settle_held<T, U>(left, a.width, next_g);
+    }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       unpack<T>(next_x[j], h[j]);
@@ -433,8 +471,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
       v[j] = pack<T>(h[j]);
     }
     if (live) {
-      if constexpr (L < 64) st_lane<T>(a.dx + t * a.ld_dx, l, a.width, v[0]);
-      else st_held<T, U, true>(a.dx + t * a.ld_dx + off, left, v);
+      if constexpr (L < 64) st_lane<T, REST>(a.dx + t * a.ld_dx, l, a.width, v[0]);
+      else st_held<T, U, true, REST>(a.dx + t * a.ld_dx + off, left, v);
     }
   }
   if (!a.partial) return;
@@ -577,30 +615,35 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(const LayerNorm
 }
 
 // dweight and dbias from the partial sums: 64 columns a workgroup, its waves
-// taking every 16th partial sum.
+// taking every 16th partial sum.  256 of 4096 columns each (8.4 MB) 4.2 us.
 constexpr int kJoinWaves = 16;
+constexpr uint64_t kJoinGrid = 1u << 20;
 template <typename GT>
 __global__ __launch_bounds__(64 * kJoinWaves) void layer_norm_join_kernel(const LayerNormBackwardArgs a, const uint32_t blocks) {
   __shared__ double lds[kJoinWaves][64];
   const uint32_t lane = threadIdx.x & 63u, w = wave_id();
-  const uint64_t col = (uint64_t)blockIdx.x * 64 + lane;
   const bool second = blockIdx.y != 0;
   char* out = static_cast<char*>(second ? a.dbias : a.dweight);
   if (!out) return;
-  double sum = 0.0;
-  if (col < a.width) {
-    const float* p = a.partial + (second ? a.width : 0) + col;
+  for (uint64_t c0 = (uint64_t)blockIdx.x * 64; c0 < a.width; c0 += (uint64_t)gridDim.x * 64) {
+    const uint64_t col = c0 + lane;
+    double sum = 0.0;
+    if (col < a.width) {
+      const float* p = a.partial + (second ? a.width : 0) + col;
 #pragma unroll 8
-    for (uint32_t b = w; b < blocks; b += kJoinWaves) sum += p[(uint64_t)b * 2 * a.width];
-  }
-  lds[w][lane] = sum;
-  __syncthreads();
-  if (w != 0 || col >= a.width) return;
+      for (uint32_t b = w; b < blocks; b += kJoinWaves) sum += p[(uint64_t)b * 2 * a.width];
+    }
+    lds[w][lane] = sum;
+    __syncthreads();
+    if (w == 0 && col < a.width) {
 #pragma unroll
-  for (int i = 1; i < kJoinWaves; ++i) sum += lds[i][lane];
-  char* at = out + col * GT::kSize;
-  if (a.accumulate) sum += load_elem<GT>(at);
-  store_elem<GT>(at, (float)sum);
+      for (int i = 1; i < kJoinWaves; ++i) sum += lds[i][lane];
+      char* at = out + col * GT::kSize;
+      if (a.accumulate) sum += load_elem<GT>(at);
+      store_elem<GT>(at, (float)sum);
+    }
+    __syncthreads();  // lds is free
+  }
 }
 
 uint32_t cus() {
@@ -624,8 +667,9 @@ void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
     c.x = a.x + t * a.ld_x;
     c.out = a.out + t * a.ld_out;
     c.stats = a.stats ? a.stats + 2 * t : nullptr;
-    hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U>), dim3((uint32_t)((c.tokens + per - 1) / per)), dim3(64 * NW), 0,
-                       stream, c, per);
+    const dim3 grid((uint32_t)((c.tokens + per - 1) / per)), block(64 * NW);
+    if (a.width % kUnit<T> == 0) hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U, false>), grid, block, 0, stream, c, per);
+    else if constexpr (W * U < 64) hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U, true>), grid, block, 0, stream, c, per);
   }
 }
 
@@ -641,7 +685,7 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   else if (kib <= 8) layer_norm_in<T, P, 64, 4, 2>(a, stream);
   else if (kib <= 16) layer_norm_in<T, P, 64, 4, 4>(a, stream);
   else if (kib <= 32) layer_norm_in<T, P, 64, 8, 4>(a, stream);
-  else if (kib <= kHeldKib<T, P>) {
+  else if (kib <= kHeldKib<T, P> && a.width % kUnit<T> == 0) {
     if constexpr (kHeldKib<T, P> > 32) layer_norm_in<T, P, 64, 16, 4>(a, stream);
   } else {
     const uint64_t most = (uint64_t)cus() * 2;
@@ -652,7 +696,9 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
 
 template <typename T, typename P, int L, int W, int U>
 void layer_norm_backward_in(const LayerNormBackwardArgs& a, const LayerNormShape& s, hipStream_t stream) {
-  hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U>), dim3(s.blocks), dim3(64 * kGradWaves), 0, stream, a);
+  const dim3 grid((uint32_t)s.blocks), block(64 * kGradWaves);
+  if (a.width % kUnit<T> == 0) hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U, false>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U, true>), grid, block, 0, stream, a);
 }
 
 template <typename T, typename P>
@@ -662,7 +708,7 @@ void layer_norm_backward_any(const LayerNormBackwardArgs& a, const LayerNormShap
     const uint64_t most = (uint64_t)cus() * 2;
     hipLaunchKernelGGL((layer_norm_row_sums_kernel<T, P>), dim3((uint32_t)(a.tokens < most ? a.tokens : most)),
                        dim3(1024), 0, stream, a);
-    const uint32_t y = s.blocks < 32768 ? s.blocks : 32768;
+    const uint32_t y = s.blocks < 32768 ? (uint32_t)s.blocks : 32768u;
     hipLaunchKernelGGL((layer_norm_columns_kernel<T, P>), dim3((uint32_t)((kib + 3) / 4), y), dim3(256), 0, stream, a,
                        s.per);
   } else if (bytes <= 256) layer_norm_backward_in<T, P, 16, 1, 1>(a, s, stream);
@@ -696,7 +742,7 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
   uint64_t turns = (tokens + rows * most - 1) / (rows * most);
   if (turns > kSumTokens) turns = kSumTokens;
   s.per = (uint32_t)(rows * turns);
-  s.blocks = (uint32_t)((tokens + s.per - 1) / s.per);
+  s.blocks = (tokens + s.per - 1) / s.per;
   return s;
 }
 
@@ -709,9 +755,10 @@ hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const Laye
     if (e != hipSuccess) return e;
   }
   if (a.dweight || a.dbias) {
-    const dim3 grid((uint32_t)(((uint64_t)a.width + 63) / 64), 2), block(64 * kJoinWaves);
-    if (grad_bf16) hipLaunchKernelGGL((layer_norm_join_kernel<BF16>), grid, block, 0, stream, a, s.blocks);
-    else hipLaunchKernelGGL((layer_norm_join_kernel<F32>), grid, block, 0, stream, a, s.blocks);
+    const uint64_t cols = ((uint64_t)a.width + 63) / 64;
+    const dim3 grid((uint32_t)(cols < kJoinGrid ? cols : kJoinGrid), 2), block(64 * kJoinWaves);
+    if (grad_bf16) hipLaunchKernelGGL((layer_norm_join_kernel<BF16>), grid, block, 0, stream, a, (uint32_t)s.blocks);
+    else hipLaunchKernelGGL((layer_norm_join_kernel<F32>), grid, block, 0, stream, a, (uint32_t)s.blocks);
   }
   return hipGetLastError();
 }

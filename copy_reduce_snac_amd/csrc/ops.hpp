@@ -220,9 +220,11 @@ hipError_t launch_layer_norm(const LayerNormArgs& a, bool bf16, bool param_bf16,
 // workgroups, which leave one partial sum each.  row_sums: rows too wide for a
 // workgroup's registers, whose own sums are made by a launch before.
 struct LayerNormShape {
-  uint32_t blocks, per;
+  uint64_t blocks;
+  uint32_t per;
   bool row_sums;
 };
+constexpr uint32_t kLayerNormMaxBlocks = 1u << 22;  // a launch has fewer than 2^32 threads
 LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize);
 struct LayerNormBackwardArgs {
   const char* dout;

@@ -110,6 +110,7 @@ snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, cons
 size_t snac_layer_norm_scratch(size_t tokens, size_t width, snac_dtype dtype) {
   if (!is_float(dtype) || tokens > SNAC_MAX_BYTES || width >= kMaxWidth || tokens == 0 || width == 0) return 0;
   const LayerNormShape s = layer_norm_shape(tokens, width, esize(dtype));
+  if (s.blocks >= kLayerNormMaxBlocks) return 0;
   return up256((uint64_t)s.blocks * 2 * width * 4) + (s.row_sums ? tokens * 8 : 0);
 }
 
@@ -137,6 +138,7 @@ snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_
   TRY(check_spans(s, al, dx, dout));
   if (width == 0) return ok();
   const LayerNormShape shape = layer_norm_shape(tokens, width, es);
+  if (shape.blocks >= kLayerNormMaxBlocks) return fail(SNAC_E_ARG, "%zu tokens: more than one call takes", tokens);
   const uint64_t partial = dweight || dbias ? up256((uint64_t)shape.blocks * 2 * width * 4) : 0;
   const uint64_t bytes = partial + (shape.row_sums ? tokens * 8 : 0);
   char* scratch = nullptr;

@@ -249,10 +249,12 @@ snac_status snac_clip_grad_norm(snac_grads* grads, float max_norm, float* norm, 
  *   rstd = 1 / sqrt(var + eps),  out = (x - mean) * rstd * weight + bias
  * weight and bias: `width` values of param_dtype, or NULL (1 and 0; they may be
  * given one without the other).  stats: NULL, or [tokens][2] binary32 that
- * receive mean and rstd for the gradient.  The sums are binary32 within 16 bytes
- * of a row and binary64 over them, the mean is subtracted in more than binary32's
- * precision, each output is rounded once.  eps finite and >= 0 (with 0 a constant
- * row gives NaN, by the formula).  out may be x itself (same ld).
+ * receive mean and rstd for the gradient.  A mean near the row's is made in
+ * binary32; the distances from it and their squares are summed in binary32 within
+ * 16 bytes of a row and in binary64 over them, which gives the mean and the
+ * variance of rows far from 0 too.  (Sums and squares that pass binary32's range
+ * are infinite.)  Each output is rounded once.  eps finite and >= 0 (with 0 a
+ * constant row gives NaN, by the formula).  out may be x itself (same ld).
  */
 snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, const void* bias, snac_dtype param_dtype,
                             size_t tokens, size_t width, float eps, snac_dtype dtype, void* out, size_t ld_out,
@@ -273,6 +275,7 @@ snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, cons
  * dx may be dout itself (same ld).  Scratch is the context's staging rings:
  * snac_layer_norm_scratch bytes (SNAC_E_ARG if the rings together are smaller);
  * without dweight and dbias rows of up to 32 KiB need none, and ctx may be NULL.
+ * Calls of 2^27 tokens and more may be refused (SNAC_E_ARG).
  */
 snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_dout, const void* x, size_t ld_x,
                                      const void* weight, snac_dtype param_dtype, const float* stats, size_t tokens,

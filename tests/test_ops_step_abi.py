@@ -73,12 +73,14 @@ def test_layer_norm_backward():
     refused(*f(), says="ctx")  # the sums over tokens need scratch
     refused(*f(dx=A), says="ctx")  # in place is right
     refused(*f(dw=0), says="ctx")
+    refused(*f(n=1, ld=1, ld_g=1, ld_dx=1, t=1 << 34, g=FAR, x=2 * FAR, stats=3 * FAR, dx=4 * FAR, w=0), says="tokens")
     n = 20000  # rows too wide for a workgroup's registers need scratch for their sums too
     refused(*f(ld=n, ld_g=n, ld_dx=n, n=n, dw=0, db=0), says="ctx")
     snac.snac_layer_norm_backward(None, 0, 32, 0, 32, 0, "f32", 0, 0, 32, "f32", 0, 32, 0, 0, "f32")
     snac.snac_layer_norm_backward(None, 0, 0, 0, 0, 0, "f32", 0, 4, 0, "f32", 0, 0, G, H, "f32")
     s = snac.snac_layer_norm_scratch
     assert s(0, 32, "f32") == s(8, 0, "f32") == s(8, 1 << 31, "f32") == s(8, 32, "u32") == 0
+    assert s(1 << 34, 1, "f32") == 0
     assert s(1, 32, "f32") >= 2 * 32 * 4
     assert s(1 << 20, 4096, "bf16") <= (1 << 20) * 4096 // 4  # an eighth of the rows
 
