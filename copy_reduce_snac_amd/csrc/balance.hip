@@ -224,10 +224,15 @@ __global__ __launch_bounds__(kLoadThreads) void balance_load_kernel(const Balanc
       R other(r.E);
       other.l = i % L;
       const uint32_t e = other.at((int)(j0 + i / L));
-      if (e < r.E) out[e] = s;
+      if (e >= r.E) continue;
+      if (gridDim.x == 1) a.load[r.E + e] = (float)s;  // nothing to join
+      else out[e] = s;
     }
   }
-  for (uint32_t e = threadIdx.x; e < r.E; e += kLoadThreads) a.counts[(uint64_t)blockIdx.x * r.E + e] = hist[e];
+  for (uint32_t e = threadIdx.x; e < r.E; e += kLoadThreads) {
+    if (gridDim.x == 1) a.load[e] = (float)hist[e];
+    else a.counts[(uint64_t)blockIdx.x * r.E + e] = hist[e];
+  }
 }
 
 // load from the workgroups' sums and counts: 16 experts a workgroup, a lane
@@ -398,6 +403,8 @@ struct BackwardLauncher {
 
 uint32_t balance_blocks(uint64_t tokens, int experts) {
   const uint64_t rows = kLoadWaves * (experts <= 256 ? 4 : experts <= 512 ? 2 : 1);
+  // one workgroup has no other's sums to wait for: the join's launch is saved
+  if (tokens != 0 && tokens <= 2 * rows) return 1;
   const uint64_t want = (tokens + rows - 1) / rows;
   return (uint32_t)(want < kBalanceMaxBlocks ? want : kBalanceMaxBlocks);
 }
@@ -407,7 +414,7 @@ hipError_t launch_balance_load(const BalanceArgs& a, bool bf16, hipStream_t stre
     if (bf16) by_experts<BF16>(a.experts, LoadLauncher{a, stream});
     else by_experts<F32>(a.experts, LoadLauncher{a, stream});
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.blocks == 1) return e;
   }
   hipLaunchKernelGGL(balance_join_kernel, dim3((a.experts + 15) / 16), dim3(64 * kJoinWaves), 0, stream, a);
   return hipGetLastError();

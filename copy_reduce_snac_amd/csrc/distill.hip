@@ -348,17 +348,27 @@ void distill_any(const DistillArgs& a, hipStream_t stream) {
     const uint64_t want = (a.tokens + rows - 1) / rows;
     return dim3((uint32_t)(want < kMaxGrid ? want : kMaxGrid));
   };
-  if (bytes <= 16384) hipLaunchKernelGGL((distill_kernel<T, 1, C>), grid(kWaves), dim3(kThreads), 0, stream, a);
-  else if (a.tokens >= cus() * 2) hipLaunchKernelGGL((distill_kernel<T, 4, C>), grid(1), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((distill_kernel<T, 16, C>), grid(1), dim3(1024), 0, stream, a);
+  // Waves a row: one has its sums without a barrier, more have it sooner.  us, 1 / 4
+  // waves: 8192 x 9001 bf16 40 / 58, 2000 x 16384 15.9 / 19.5, 700 x 16384 10.4 /
+  // 9.0, 8192 x 32768 96 / 97, f32 92 / 84 at 8192 x 16384; 4 / 16: 500 x 9001 bf16
+  // 8.2 / 10.2.
+  const uint64_t cu = cus();
+  if (bytes <= 16384 || (bytes <= 32768 && a.tokens >= cu * 4))
+    hipLaunchKernelGGL((distill_kernel<T, 1, C>), grid(kWaves), dim3(kThreads), 0, stream, a);
+  else if (bytes <= 65536 || a.tokens >= cu * 2)
+    hipLaunchKernelGGL((distill_kernel<T, 4, C>), grid(1), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((distill_kernel<T, 16, C>), grid(1), dim3(1024), 0, stream, a);
 }
 
 template <typename T, int C>
 void distill_backward_any(const DistillArgs& a, hipStream_t stream) {
   constexpr uint32_t kPiece = 64u * kBackUnits * kUnit<T>;
   const uint32_t pieces = (uint32_t)(((uint64_t)a.width + kPiece - 1) / kPiece);
-  const uint32_t per = kBackWaves * kBackTurns;
-  const uint32_t runs = (pieces + per - 1) / per;
+  // runs of about kBackWaves * kBackTurns pieces, of equal lengths
+  constexpr uint32_t kRun = kBackWaves * kBackTurns;
+  const uint32_t about = pieces < kRun ? 1 : (pieces + kRun / 2) / kRun;
+  const uint32_t per = (pieces + about - 1) / about, runs = (pieces + per - 1) / per;
   const uint64_t items = a.tokens * runs;
   hipLaunchKernelGGL((distill_backward_kernel<T, C>), dim3((uint32_t)(items < kMaxGrid ? items : kMaxGrid)),
                      dim3(64 * kBackWaves), 0, stream, a, pieces, per, runs, items);

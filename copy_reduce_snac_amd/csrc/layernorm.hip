@@ -360,6 +360,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
 
 constexpr int kGradWaves = 16;  // of a workgroup
 constexpr uint32_t kGradBlocks = 256;
+constexpr uint32_t kAloneTurns = 2;
 
 // N binary32 values to `p`, the first `left` of them.
 template <uint32_t N>
@@ -370,6 +371,18 @@ __device__ __forceinline__ void st_sums(float* p, uint32_t left, const float (&f
     const u32x4 v = {__float_as_uint(f[c]), __float_as_uint(f[c + 1]), __float_as_uint(f[c + 2]), __float_as_uint(f[c + 3])};
     if (c + 4 <= left) st_unit<false>(at + 4 * c, v);
     else if (c < left) st_part<F32>(at + 4 * c, v, left - c);
+  }
+}
+
+// A sum over the tokens into a gradient.
+__device__ __forceinline__ void put_grad(void* grad, bool bf16, bool accumulate, uint64_t i, double sum) {
+  char* p = static_cast<char*>(grad);
+  if (bf16) {
+    if (accumulate) sum += load_elem<BF16>(p + i * 2);
+    store_elem<BF16>(p + i * 2, (float)sum);
+  } else {
+    if (accumulate) sum += load_elem<F32>(p + i * 4);
+    store_elem<F32>(p + i * 4, (float)sum);
   }
 }
 
@@ -475,7 +488,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
       else st_held<T, U, true, REST>(a.dx + t * a.ld_dx + off, left, v);
     }
   }
-  if (!a.partial) return;
+  if (!a.dweight && !a.dbias) return;
   // the rows that went side by side: those of a wave, then the upper half of the
   // waves to the lower
   if constexpr (L < 64) {
@@ -522,6 +535,19 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     }
   }
   if (q != 0 || l != lane) return;
+  if (gridDim.x == 1) {  // nothing to join
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t e = first + (j * L + l) * N;
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) {
+        if (e + c >= a.width) continue;
+        if (a.dweight) put_grad(a.dweight, a.grad_bf16, a.accumulate, e + c, dw[j][c]);
+        if (a.dbias) put_grad(a.dbias, a.grad_bf16, a.accumulate, e + c, db[j][c]);
+      }
+    }
+    return;
+  }
   float* part = a.partial + (uint64_t)blockIdx.x * 2 * a.width;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
@@ -618,12 +644,11 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(const LayerNorm
 // taking every 16th partial sum.  256 of 4096 columns each (8.4 MB) 4.2 us.
 constexpr int kJoinWaves = 16;
 constexpr uint64_t kJoinGrid = 1u << 20;
-template <typename GT>
 __global__ __launch_bounds__(64 * kJoinWaves) void layer_norm_join_kernel(const LayerNormBackwardArgs a, const uint32_t blocks) {
   __shared__ double lds[kJoinWaves][64];
   const uint32_t lane = threadIdx.x & 63u, w = wave_id();
   const bool second = blockIdx.y != 0;
-  char* out = static_cast<char*>(second ? a.dbias : a.dweight);
+  void* out = second ? a.dbias : a.dweight;
   if (!out) return;
   for (uint64_t c0 = (uint64_t)blockIdx.x * 64; c0 < a.width; c0 += (uint64_t)gridDim.x * 64) {
     const uint64_t col = c0 + lane;
@@ -638,9 +663,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void layer_norm_join_kernel(const 
     if (w == 0 && col < a.width) {
 #pragma unroll
       for (int i = 1; i < kJoinWaves; ++i) sum += lds[i][lane];
-      char* at = out + col * GT::kSize;
-      if (a.accumulate) sum += load_elem<GT>(at);
-      store_elem<GT>(at, (float)sum);
+      put_grad(out, a.grad_bf16, a.accumulate, col, sum);
     }
     __syncthreads();  // lds is free
   }
@@ -740,6 +763,8 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
   if (s.row_sums) most = kGradBlocks * 16 / kib + 1;
   else rows = bytes <= 256 ? 64 : bytes <= 512 ? 32 : kib <= 2 ? 16 : kib <= 4 ? 8 : kib <= 8 ? 4 : kib <= 16 ? 2 : 1;
   uint64_t turns = (tokens + rows * most - 1) / (rows * most);
+  // one workgroup has no other's sums to wait for: the join's launch is saved
+  if (tokens <= rows * kAloneTurns) turns = (tokens + rows - 1) / rows;
   if (turns > kSumTokens) turns = kSumTokens;
   s.per = (uint32_t)(rows * turns);
   s.blocks = (tokens + s.per - 1) / s.per;
@@ -747,18 +772,17 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const LayerNormShape& s, bool bf16,
-                                      bool param_bf16, bool grad_bf16, hipStream_t stream) {
+                                      bool param_bf16, hipStream_t stream) {
   if (a.tokens) {
     if (bf16) param_bf16 ? layer_norm_backward_any<BF16, BF16>(a, s, stream) : layer_norm_backward_any<BF16, F32>(a, s, stream);
     else param_bf16 ? layer_norm_backward_any<F32, BF16>(a, s, stream) : layer_norm_backward_any<F32, F32>(a, s, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dweight || a.dbias) {
+  if ((a.dweight || a.dbias) && (s.blocks != 1 || s.row_sums)) {
     const uint64_t cols = ((uint64_t)a.width + 63) / 64;
-    const dim3 grid((uint32_t)(cols < kJoinGrid ? cols : kJoinGrid), 2), block(64 * kJoinWaves);
-    if (grad_bf16) hipLaunchKernelGGL((layer_norm_join_kernel<BF16>), grid, block, 0, stream, a, (uint32_t)s.blocks);
-    else hipLaunchKernelGGL((layer_norm_join_kernel<F32>), grid, block, 0, stream, a, (uint32_t)s.blocks);
+    hipLaunchKernelGGL(layer_norm_join_kernel, dim3((uint32_t)(cols < kJoinGrid ? cols : kJoinGrid), 2),
+                       dim3(64 * kJoinWaves), 0, stream, a, (uint32_t)s.blocks);
   }
   return hipGetLastError();
 }

@@ -239,12 +239,12 @@ struct LayerNormBackwardArgs {
   uint64_t ld_dx;  // bytes
   void* dweight;   // nullptr: not wanted
   void* dbias;
-  int32_t accumulate;
+  bool grad_bf16, accumulate;
   float* partial;   // [blocks][2][width], nullptr: neither is wanted
   float* row_sums;  // [tokens][2], see LayerNormShape
 };
 hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const LayerNormShape& s, bool bf16,
-                                      bool param_bf16, bool grad_bf16, hipStream_t stream);
+                                      bool param_bf16, hipStream_t stream);
 
 // --------------------------------------------------------- balance loss
 struct BalanceArgs {

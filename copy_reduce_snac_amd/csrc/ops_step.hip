@@ -157,11 +157,12 @@ snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_
   a.ld_dx = ld_dx * es;
   a.dweight = dweight;
   a.dbias = dbias;
-  a.accumulate = accumulate;
+  a.grad_bf16 = grad_dtype == SNAC_BF16;
+  a.accumulate = accumulate != 0;
   a.partial = partial ? reinterpret_cast<float*>(scratch) : nullptr;
   a.row_sums = shape.row_sums ? reinterpret_cast<float*>(scratch + partial) : nullptr;
-  const hipError_t e = launch_layer_norm_backward(a, shape, dtype == SNAC_BF16, param_dtype == SNAC_BF16,
-                                                  grad_dtype == SNAC_BF16, (hipStream_t)stream);
+  const hipError_t e =
+      launch_layer_norm_backward(a, shape, dtype == SNAC_BF16, param_dtype == SNAC_BF16, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_layer_norm_backward launch");
 }
 
