@@ -23,29 +23,11 @@ struct Params {
   uint32_t w[kWords];
 };
 
-// Parameters of the kUnit<T> elements from `e` on; those past `width` are 0 (or
-// what follows, where a lane has none).  A part of a unit is loaded as the
-// elements that end where the row does and moved down: element by element, each
-// waiting for the one before, it took 10 us of 46 for 8192 rows of 5003 bf16.
+// Parameters of the kUnit<T> elements from `e` on.
 template <typename T, typename P>
-__device__ __forceinline__ void ld_params(const char* p, uint32_t e, uint32_t width, Params<T, P>& r) {
-  constexpr uint32_t N = kUnit<T>;
+__device__ __forceinline__ void ld_params(const char* p, uint32_t e, Params<T, P>& r) {
   constexpr int K = Params<T, P>::kWords;
-#pragma unroll
-  for (int c = 0; c < K; ++c) r.w[c] = 0;
-  if (e >= width) return;
-  if (width < N) {
-#pragma unroll
-    for (uint32_t i = 0; i < N; ++i) {
-      if (e + i >= width) continue;
-      const char* at = p + (uint64_t)(e + i) * P::kSize;
-      if constexpr (P::kSize == 4) r.w[i] = *(global_ptr<const uint32_t>)(at);
-      else r.w[i / 2] |= (uint32_t)*(global_ptr<const uint16_t>)(at) << (16 * (i & 1));
-    }
-    return;
-  }
-  const uint32_t first = e + N <= width ? 0 : e + N - width;
-  const char* at = p + (uint64_t)(e - first) * P::kSize;
+  const char* at = p + (uint64_t)e * P::kSize;
   if constexpr (K == 2) {
     const u32x2_a2 v = *(global_ptr<const u32x2_a2>)(at);
     r.w[0] = v[0], r.w[1] = v[1];
@@ -57,19 +39,20 @@ __device__ __forceinline__ void ld_params(const char* p, uint32_t e, uint32_t wi
       for (int c = 0; c < 4; ++c) r.w[4 * u + c] = v[c];
     }
   }
-  if (first != 0) {
-    const uint32_t words = first * P::kSize / 4;
-    uint32_t t[K];
+}
+// The same at the end of a row; those past `width` are 0.
+template <typename T, typename P>
+__device__ __forceinline__ void ld_params(const char* p, uint32_t e, uint32_t width, Params<T, P>& r) {
+  constexpr uint32_t N = kUnit<T>;
+  if (e + N <= width) return ld_params<T, P>(p, e, r);
 #pragma unroll
-    for (int c = 0; c < K; ++c) {
-      t[c] = r.w[c];
+  for (int c = 0; c < Params<T, P>::kWords; ++c) r.w[c] = 0;
 #pragma unroll
-      for (int q = 1; q < K; ++q)
-        if (words == (uint32_t)q) t[c] = c + q < K ? r.w[(c + q) % K] : 0u;
-    }
-    const bool half = P::kSize == 2 && (first & 1);
-#pragma unroll
-    for (int c = 0; c < K; ++c) r.w[c] = half ? t[c] >> 16 | (c + 1 < K ? t[(c + 1) % K] << 16 : 0u) : t[c];
+  for (uint32_t i = 0; i < N; ++i) {
+    if (e + i >= width) continue;
+    const char* at = p + (uint64_t)(e + i) * P::kSize;
+    if constexpr (P::kSize == 4) r.w[i] = *(global_ptr<const uint32_t>)(at);
+    else r.w[i / 2] |= (uint32_t)*(global_ptr<const uint16_t>)(at) << (16 * (i & 1));
   }
 }
 // All of them 1 (absent weights) or -0 (absent biases: x + -0 is x, also for -0).
@@ -152,31 +135,93 @@ __device__ __forceinline__ float unit_dot(const float (&x)[N], const float (&y)[
   return s;
 }
 
-// Unit `l` of a row of `width` elements, which may have a part of it (REST, and
-// settled as in settle_held) or none.
-template <typename T, bool REST>
-__device__ __forceinline__ u32x4 ld_lane(const char* row, uint32_t l, uint32_t width) {
-  constexpr uint32_t N = kUnit<T>;
-  const uint32_t units = width / N, rest = REST ? width % N : 0;
-  u32x4 v = {0, 0, 0, 0};
-  if (l < units + (rest != 0 && width >= N ? 1 : 0))
-    v = ld_unit<false>(l < units ? row + l * 16u : row + (uint64_t)width * T::kSize - 16);
-  if (REST && width < N && l == 0) v = ld_rest<T>(row, rest);
-  return v;
+// A 16-bit element's place in its word.
+__device__ __forceinline__ uint32_t with_half(uint32_t w, uint32_t c, uint16_t half) {
+  return (c & 1) ? (w & 0xffffu) | (uint32_t)half << 16 : (w & 0xffff0000u) | half;
 }
-template <typename T>
-__device__ __forceinline__ void settle_lane(uint32_t l, uint32_t width, u32x4& v) {
-  constexpr uint32_t N = kUnit<T>;
-  if (width % N == 0 || width < N) return;
-  const u32x4 r = later_elems<T>(v, N - width % N);
-  if (l == width / N) v = r;
-}
-template <typename T, bool REST>
-__device__ __forceinline__ void st_lane(char* row, uint32_t l, uint32_t width, u32x4 v) {
-  const uint32_t units = width / kUnit<T>, rest = REST ? width % kUnit<T> : 0;
-  if (l < units) st_unit<true>(row + l * 16u, v);
-  if (rest != 0 && l == units) st_rest<T>(row + units * 16u, v, rest);
-}
+
+// A wave's piece of a row that stays in registers: U units of each of a row's L
+// lanes, unit j of lane l being the piece's unit j L + l; `left` elements of the row
+// from the piece on.  REST: a row may end in a part of a unit.  Its lane takes the
+// unit that ends where the row does instead, whose first `skip` elements are another
+// lane's too: both make the same results of them, and sums leave them out.  A row of
+// less than a unit (16 lanes only) is the last elements of one.  (Parts loaded and stored in pieces of their own, and moved
+// to their places: 8192 rows of 5003 bf16 42 us, this way 33.)
+template <typename T, int L, int U, bool REST>
+struct Piece {
+  static constexpr uint32_t N = kUnit<T>;
+  const uint32_t left;
+  const bool whole;
+  __device__ __forceinline__ Piece(uint32_t left) : left(left), whole(left >= L * U * N) {}
+  __device__ __forceinline__ static uint32_t own(int j) { return (j * L + threadIdx.x % L) * N; }
+  __device__ __forceinline__ bool has(int j) const { return REST ? own(j) < left : own(j) + N <= left; }
+  // the unit's first element, counted from the piece
+  __device__ __forceinline__ int32_t at(int j) const {
+    const int32_t e = (int32_t)own(j), last = (int32_t)(left - N);
+    return REST && e > last ? last : e;
+  }
+  __device__ __forceinline__ uint32_t skip(int j) const { return own(j) - (uint32_t)at(j); }
+  __device__ __forceinline__ bool small() const { return REST && L == 16 && left < N && has(0); }
+  template <typename P>
+  __device__ __forceinline__ void params(const char* p, uint32_t first, int j, Params<T, P>& r) const {
+    if (!p || !has(j)) return;
+    const char* from = p + (int64_t)(int32_t)(first + (uint32_t)at(j)) * P::kSize;
+    if (small()) {
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) {
+        if (c < skip(j)) continue;
+        if constexpr (P::kSize == 4) r.w[c] = *(global_ptr<const uint32_t>)(from + 4 * c);
+        else r.w[c / 2] = with_half(r.w[c / 2], c, *(global_ptr<const uint16_t>)(from + 2 * c));
+      }
+    } else {
+      ld_params<T, P>(from, 0, r);
+    }
+  }
+  template <bool NT>
+  __device__ __forceinline__ void load(const char* piece, u32x4 (&v)[U]) const {
+    const uint32_t l = threadIdx.x % L;
+    if (small()) {
+      v[0] = u32x4{0, 0, 0, 0};
+      const char* from = piece + (int64_t)at(0) * T::kSize;
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) {
+        if (c < skip(0)) continue;
+        if constexpr (T::kSize == 4) v[0][c] = *(global_ptr<const uint32_t>)(from + 4 * c);
+        else v[0][c / 2] = with_half(v[0][c / 2], c, *(global_ptr<const uint16_t>)(from + 2 * c));
+      }
+    } else if (whole) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) v[j] = ld_unit<NT>(piece + (j * L + l) * 16u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        v[j] = u32x4{0, 0, 0, 0};
+        if (has(j)) v[j] = ld_unit<NT>(piece + (int64_t)at(j) * T::kSize);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* piece, const u32x4 (&v)[U]) const {
+    const uint32_t l = threadIdx.x % L;
+    if (small()) {
+      char* from = piece + (int64_t)at(0) * T::kSize;
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) {
+        if (c < skip(0)) continue;
+        if constexpr (T::kSize == 4) *(global_ptr<uint32_t>)(from + 4 * c) = v[0][c];
+        else *(global_ptr<uint16_t>)(from + 2 * c) = (uint16_t)(v[0][c / 2] >> (16 * (c & 1)));
+      }
+    } else if (whole) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) st_unit<true>(piece + (j * L + l) * 16u, v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (has(j)) st_unit<true>(piece + (int64_t)at(j) * T::kSize, v[j]);
+    }
+  }
+  // an element as sums take it
+  __device__ __forceinline__ float counted(int j, uint32_t c, float f) const { return !REST || c >= skip(j) ? f : 0.0f; }
+};
 
 // ------------------------------------------------------------------ forward
 
@@ -209,21 +254,19 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
   const uint32_t l = threadIdx.x % L, w = wave_id();
   const uint32_t g = L < 64 ? threadIdx.x / L : w / W;  // the row of those side by side
   const uint32_t first = (w % W) * 64u * U * N * (L == 64);  // the wave's piece of it
-  const uint32_t left = first < a.width ? a.width - first : 0;
-  const bool whole = left >= L * U * N;
+  const Piece<T, L, U, REST> piece(first < a.width ? a.width - first : 0);
   // the parameters are kept, and the next row is loaded while this one is worked
   // on, where registers allow it
   constexpr bool kAhead = W * U < 64;
   Params<T, P> weight[U], bias[U];
   auto params = [&](int j) {
-    const uint32_t e = first + (j * L + l) * N;
     const char *pw = a.weight, *pb = a.bias;
     // opaque here, so that they are not loaded before the loop after all
     if constexpr (!kAhead) asm volatile("" : "+s"(pw), "+s"(pb));
-    if (pw) ld_params<T, P>(pw, e, a.width, weight[j]);
-    else fill_params<T, P>(1.0f, weight[j]);
-    if (pb) ld_params<T, P>(pb, e, a.width, bias[j]);
-    else fill_params<T, P>(-0.0f, bias[j]);
+    fill_params<T, P>(1.0f, weight[j]);
+    fill_params<T, P>(-0.0f, bias[j]);
+    piece.params(pw, first, j, weight[j]);
+    piece.params(pb, first, j, bias[j]);
   };
   if constexpr (kAhead) {
 #pragma unroll
@@ -237,9 +280,8 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
   auto load = [&](uint64_t row) {
     if (row >= end) return;
     const char* x = a.x + row * a.ld_x + (uint64_t)first * T::kSize;
-    if constexpr (L < 64) next[0] = ld_lane<T, REST>(x, l, a.width);
-    else if (lines) ld_held<T, U, true, REST>(x, left, a.width, next);
-    else ld_held<T, U, false, REST>(x, left, a.width, next);
+    if (L == 64 && lines) piece.template load<true>(x, next);
+    else piece.template load<false>(x, next);
   };
   if constexpr (kAhead) load(t0 + g);
   // every wave of the workgroup goes round as often as its first
@@ -249,33 +291,26 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
     u32x4 v[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) v[j] = next[j];
-    if (REST && !whole) {
-      if constexpr (L < 64) settle_lane<T>(l, a.width, v[0]);
-      else settle_held<T, U>(left, a.width, v);
-    }
     if constexpr (kAhead) load(t + G);
     float f[U][N], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < U; ++j) unpack<T>(v[j], f[j]);
 #pragma unroll
-    for (int j = 0; j < U; ++j) sum += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
+    for (int j = 0; j < U; ++j) sum += unit_sum<N>([&](uint32_t c) { return piece.counted(j, c, f[j][c]); });
     const float near = row_sum<L, W>(sum, first_sums) * inv_f;
 #pragma unroll
     for (int j = 0; j < U; ++j)
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c) f[j][c] = f[j][c] - near;
-    if (!whole) {
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (uint32_t c = 0; c < N; ++c)
-          if ((j * L + l) * N + c >= left) f[j][c] = 0.0f;
-    }
     double sd = 0.0, sq = 0.0;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      sd += unit_sum<N>([&](uint32_t c) { return f[j][c]; });
-      sq += unit_dot<N>(f[j], f[j]);
+      if (!piece.whole && !piece.has(j)) continue;
+      float d[N];
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) d[c] = piece.counted(j, c, f[j][c]);
+      sd += unit_sum<N>([&](uint32_t c) { return d[c]; });
+      sq += unit_dot<N>(d, d);
     }
     row_sum<L, W>(sd, sq, lds);
     const Moments m(near, sd * inv, sq * inv, a.eps);
@@ -291,9 +326,7 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
           f[j][c] = __builtin_fmaf(__builtin_fmaf(f[j][c], m.rstd, m.shift), param<T, P>(weight[j], c), param<T, P>(bias[j], c));
         v[j] = pack<T>(f[j]);
       }
-      char* out = a.out + t * a.ld_out + (uint64_t)first * T::kSize;
-      if constexpr (L < 64) st_lane<T, REST>(out, l, a.width, v[0]);
-      else st_held<T, U, true, REST>(out, left, v);
+      piece.store(a.out + t * a.ld_out + (uint64_t)first * T::kSize, v);
       if (a.stats && w % W == 0 && l == 0) {
         a.stats[2 * t] = m.mean;
         a.stats[2 * t + 1] = m.rstd;
@@ -362,15 +395,18 @@ constexpr int kGradWaves = 16;  // of a workgroup
 constexpr uint32_t kGradBlocks = 256;
 constexpr uint32_t kAloneTurns = 2;
 
-// N binary32 values to `p`, the first `left` of them.
+// N binary32 values to `p`, but the first `skip`.
 template <uint32_t N>
-__device__ __forceinline__ void st_sums(float* p, uint32_t left, const float (&f)[N]) {
-  char* at = reinterpret_cast<char*>(p);
+__device__ __forceinline__ void st_sums(float* p, uint32_t skip, const float (&f)[N]) {
+  if (skip == 0) {
 #pragma unroll
-  for (uint32_t c = 0; c < N; c += 4) {
-    const u32x4 v = {__float_as_uint(f[c]), __float_as_uint(f[c + 1]), __float_as_uint(f[c + 2]), __float_as_uint(f[c + 3])};
-    if (c + 4 <= left) st_unit<false>(at + 4 * c, v);
-    else if (c < left) st_part<F32>(at + 4 * c, v, left - c);
+    for (uint32_t c = 0; c < N; c += 4)
+      st_unit<false>(reinterpret_cast<char*>(p + c), u32x4{__float_as_uint(f[c]), __float_as_uint(f[c + 1]),
+                                                           __float_as_uint(f[c + 2]), __float_as_uint(f[c + 3])});
+  } else {
+#pragma unroll
+    for (uint32_t c = 0; c < N; ++c)
+      if (c >= skip) *(global_ptr<float>)(reinterpret_cast<char*>(p + c)) = f[c];
   }
 }
 
@@ -399,13 +435,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   const uint32_t g = L < 64 ? threadIdx.x / L : q;  // the row of those side by side
   const uint32_t first = (w % W) * kPiece * (L == 64);
   const uint32_t left = first < a.width ? a.width - first : 0;
+  const Piece<T, L, U, REST> piece(left);
   const uint64_t off = (uint64_t)first * T::kSize;
-  const bool whole = left >= L * U * N;
   Params<T, P> weight[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    if (a.weight) ld_params<T, P>(a.weight, first + (j * L + l) * N, a.width, weight[j]);
-    else fill_params<T, P>(1.0f, weight[j]);
+    fill_params<T, P>(1.0f, weight[j]);
+    piece.params(a.weight, first, j, weight[j]);
   }
   float dw[U][N], db[U][N];
 #pragma unroll
@@ -415,51 +451,44 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   const float inv = (float)(1.0 / (double)a.width);
   const bool lines = whole_lines(a.x, a.ld_x) && whole_lines(a.dout, a.ld_dout);
   u32x4 next_x[U] = {}, next_g[U] = {};
-  auto load = [&](uint64_t t) {
+  auto load = [&](uint64_t t, const Piece<T, L, U, REST>& piece) {
     if (t >= a.tokens) return;
-    if constexpr (L < 64) {
-      next_x[0] = ld_lane<T, REST>(a.x + t * a.ld_x, l, a.width);
-      next_g[0] = ld_lane<T, REST>(a.dout + t * a.ld_dout, l, a.width);
-    } else if (lines) {
-      ld_held<T, U, true, REST>(a.x + t * a.ld_x + off, left, a.width, next_x);
-      ld_held<T, U, true, REST>(a.dout + t * a.ld_dout + off, left, a.width, next_g);
+    if (L == 64 && lines) {
+      piece.template load<true>(a.x + t * a.ld_x + off, next_x);
+      piece.template load<true>(a.dout + t * a.ld_dout + off, next_g);
     } else {
-      ld_held<T, U, false, REST>(a.x + t * a.ld_x + off, left, a.width, next_x);
-      ld_held<T, U, false, REST>(a.dout + t * a.ld_dout + off, left, a.width, next_g);
+      piece.template load<false>(a.x + t * a.ld_x + off, next_x);
+      piece.template load<false>(a.dout + t * a.ld_dout + off, next_g);
     }
   };
   // rows of all workgroups' same turn lie side by side
   const uint64_t step = (uint64_t)gridDim.x * G;
-  load((uint64_t)blockIdx.x * G + g);
+  load((uint64_t)blockIdx.x * G + g, piece);
   uint32_t turn = 0;
   for (uint64_t s = (uint64_t)blockIdx.x * G; s < a.tokens; s += step, turn ^= 1) {
     const uint64_t t = s + g;
     const bool live = t < a.tokens;
-    float h[U][N], up[U][N];
-    if (REST && !whole) {
-      if constexpr (L < 64) settle_lane<T>(l, a.width, next_x[0]), settle_lane<T>(l, a.width, next_g[0]);
-      else settle_held<T, U>(left, a.width, next_x), settle_held<T, U>(left, a.width, next_g);
+    // its places and masks are worked out again for every row: kept, they spill
+    uint32_t left_here = left;
+    if constexpr (REST) {
+      left_here = __builtin_amdgcn_readfirstlane(left);
+      asm volatile("" : "+s"(left_here));
     }
+    const Piece<T, L, U, REST> piece(left_here);
+    float h[U][N], up[U][N];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       unpack<T>(next_x[j], h[j]);
       unpack<T>(next_g[j], up[j]);
     }
     const float mean = live ? a.stats[2 * t] : 0.0f, rstd = live ? a.stats[2 * t + 1] : 0.0f;
-    load(t + step);
+    load(t + step, piece);
     double c1 = 0.0, c2 = 0.0;
     if (live) {
 #pragma unroll
       for (int j = 0; j < U; ++j)
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c) h[j][c] = (h[j][c] - mean) * rstd;
-      if (!whole) {
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-          for (uint32_t c = 0; c < N; ++c)
-            if ((j * L + l) * N + c >= left) h[j][c] = 0.0f;
-      }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
 #pragma unroll
@@ -470,8 +499,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
           db[j][c] += up[j][c];
           up[j][c] = up[j][c] * param<T, P>(weight[j], c);
         }
-        c1 += unit_sum<N>([&](uint32_t c) { return up[j][c]; });
-        c2 += unit_dot<N>(up[j], h[j]);
+        float d[N];
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c) d[c] = piece.counted(j, c, up[j][c]);
+        c1 += unit_sum<N>([&](uint32_t c) { return d[c]; });
+        c2 += unit_dot<N>(d, h[j]);
       }
     }
     row_sum<L, W>(c1, c2, lds[turn]);
@@ -483,10 +515,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
       for (uint32_t c = 0; c < N; ++c) h[j][c] = rstd * __builtin_fmaf(-h[j][c], m2, up[j][c] - m1);
       v[j] = pack<T>(h[j]);
     }
-    if (live) {
-      if constexpr (L < 64) st_lane<T, REST>(a.dx + t * a.ld_dx, l, a.width, v[0]);
-      else st_held<T, U, true, REST>(a.dx + t * a.ld_dx + off, left, v);
-    }
+    if (live) piece.store(a.dx + t * a.ld_dx + off, v);
   }
   if (!a.dweight && !a.dbias) return;
   // the rows that went side by side: those of a wave, then the upper half of the
@@ -535,26 +564,22 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     }
   }
   if (q != 0 || l != lane) return;
-  if (gridDim.x == 1) {  // nothing to join
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const uint32_t e = first + (j * L + l) * N;
-#pragma unroll
-      for (uint32_t c = 0; c < N; ++c) {
-        if (e + c >= a.width) continue;
-        if (a.dweight) put_grad(a.dweight, a.grad_bf16, a.accumulate, e + c, dw[j][c]);
-        if (a.dbias) put_grad(a.dbias, a.grad_bf16, a.accumulate, e + c, db[j][c]);
-      }
-    }
-    return;
-  }
   float* part = a.partial + (uint64_t)blockIdx.x * 2 * a.width;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    const uint32_t e = first + (j * L + l) * N;
-    if (e >= a.width) continue;
-    st_sums<N>(part + e, a.width - e, dw[j]);
-    st_sums<N>(part + a.width + e, a.width - e, db[j]);
+    if (!piece.has(j)) continue;
+    const int64_t e = (int32_t)(first + (uint32_t)piece.at(j));
+    if (gridDim.x == 1) {  // nothing to join
+#pragma unroll
+      for (uint32_t c = 0; c < N; ++c) {
+        if (c < piece.skip(j)) continue;
+        if (a.dweight) put_grad(a.dweight, a.grad_bf16, a.accumulate, e + c, dw[j][c]);
+        if (a.dbias) put_grad(a.dbias, a.grad_bf16, a.accumulate, e + c, db[j][c]);
+      }
+    } else {
+      st_sums<N>(part + e, piece.skip(j), dw[j]);
+      st_sums<N>(part + a.width + e, piece.skip(j), db[j]);
+    }
   }
 }
 
@@ -634,9 +659,12 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(const LayerNorm
     }
     if (!a.partial) continue;
     float* part = a.partial + b * 2 * a.width;
-    if (e >= a.width) continue;
-    st_sums<N>(part + e, a.width - e, dw);
-    st_sums<N>(part + a.width + e, a.width - e, db);
+#pragma unroll
+    for (uint32_t c = 0; c < N; ++c) {
+      if (e + c >= a.width) continue;
+      part[e + c] = dw[c];
+      part[(uint64_t)a.width + e + c] = db[c];
+    }
   }
 }
 
@@ -765,7 +793,13 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
   uint64_t turns = (tokens + rows * most - 1) / (rows * most);
   // one workgroup has no other's sums to wait for: the join's launch is saved
   if (tokens <= rows * kAloneTurns) turns = (tokens + rows - 1) / rows;
-  if (turns > kSumTokens) turns = kSumTokens;
+  // more tokens than those have turns for: as many workgroups again, and as even
+  // (20000 rows of 6000 bf16 in turns of 32, 313 workgroups of one a CU, 180 us;
+  // evenly 137)
+  if (turns > kSumTokens) {
+    most *= (turns + kSumTokens - 1) / kSumTokens;
+    turns = (tokens + rows * most - 1) / (rows * most);
+  }
   s.per = (uint32_t)(rows * turns);
   s.blocks = (tokens + s.per - 1) / s.per;
   return s;
