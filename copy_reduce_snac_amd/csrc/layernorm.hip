@@ -9,8 +9,8 @@ namespace snac {
 namespace {
 
 // The widest rows that a workgroup holds in registers: 16 waves of 64 lanes of 4
-// units (rows of whole units), or 2 where wider parameters or the gradient's sums
-// over tokens are held too.
+// units, or 2 where wider parameters (with 4 they spill) or the gradient's sums over
+// tokens are held too.
 template <typename T, typename P>
 constexpr uint64_t kHeldKib = P::kSize > T::kSize ? 32 : 64;
 constexpr uint64_t kHeldBackwardKib = 32;
@@ -145,8 +145,9 @@ __device__ __forceinline__ uint32_t with_half(uint32_t w, uint32_t c, uint16_t h
 // from the piece on.  REST: a row may end in a part of a unit.  Its lane takes the
 // unit that ends where the row does instead, whose first `skip` elements are another
 // lane's too: both make the same results of them, and sums leave them out.  A row of
-// less than a unit (16 lanes only) is the last elements of one.  (Parts loaded and stored in pieces of their own, and moved
-// to their places: 8192 rows of 5003 bf16 42 us, this way 33.)
+// less than a unit (16 lanes only) is the last elements of one.  (Parts loaded and
+// stored in pieces of their own, and moved to their places: 8192 rows of 5003 bf16
+// 42 us, this way 33.)
 template <typename T, int L, int U, bool REST>
 struct Piece {
   static constexpr uint32_t N = kUnit<T>;
@@ -241,9 +242,19 @@ struct Moments {
 
 constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 
-// L lanes of one wave a row (L < 64: W and U are 1), or W waves of U units a lane:
-// the row stays in registers, so that it is read once although its mean is needed
-// before its variance and that before the result.
+// out = (x - mean) rstd weight + bias, mean and variance those of the row, rstd =
+// (variance + eps)^-1/2.  L lanes of one wave a row (L < 64: W and U are 1), or W
+// waves of U units a lane: the row stays in registers, so that it is read once
+// although its mean is needed before its variance and that before the result.  Sums
+// go over a unit in binary32 and on in binary64.
+//
+// Bound by HBM: each element is read and written once.  A workgroup takes `per` rows
+// one after another, so that its parameters are loaded once for them.  TB/s read and
+// written: 32768 x 4096 bf16 90 us, 6.0; 16384 x 4096 f32 84 us, 6.4; 65536 x 1024
+// bf16 43 us, 6.3; 262144 x 128 bf16 (16 lanes a row; with 64, 3 of 4 of them idle)
+// 23 us, 5.9; 8192 x 16384 f32 194 us, 5.5: one workgroup a CU there, whose waves load
+// and store at the same times.  One row of 8192 takes 3.2 us, two joins of four
+// waves' sums through LDS after its load.
 template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_norm_kernel(const LayerNormArgs a,
                                                                                                      const uint32_t per) {
@@ -254,44 +265,51 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
   const uint32_t l = threadIdx.x % L, w = wave_id();
   const uint32_t g = L < 64 ? threadIdx.x / L : w / W;  // the row of those side by side
   const uint32_t first = (w % W) * 64u * U * N * (L == 64);  // the wave's piece of it
-  const Piece<T, L, U, REST> piece(first < a.width ? a.width - first : 0);
-  // the parameters are kept, and the next row is loaded while this one is worked
-  // on, where registers allow it
-  constexpr bool kAhead = W * U < 64;
+  const uint32_t left = first < a.width ? a.width - first : 0;
+  const Piece<T, L, U, REST> piece(left);
+  // the next row is loaded while this one is worked on (4096 rows of 32768 bf16 111 us
+  // without, 100 with it), and the parameters are kept where registers allow it
+  constexpr bool kKeep = W * U < 64;
   Params<T, P> weight[U], bias[U];
-  auto params = [&](int j) {
+  auto params = [&](int j, const Piece<T, L, U, REST>& piece) {
     const char *pw = a.weight, *pb = a.bias;
     // opaque here, so that they are not loaded before the loop after all
-    if constexpr (!kAhead) asm volatile("" : "+s"(pw), "+s"(pb));
+    if constexpr (!kKeep) asm volatile("" : "+s"(pw), "+s"(pb));
     fill_params<T, P>(1.0f, weight[j]);
     fill_params<T, P>(-0.0f, bias[j]);
     piece.params(pw, first, j, weight[j]);
     piece.params(pb, first, j, bias[j]);
   };
-  if constexpr (kAhead) {
+  if constexpr (kKeep) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) params(j);
+    for (int j = 0; j < U; ++j) params(j, piece);
   }
   const double inv = 1.0 / (double)a.width;
   const float inv_f = (float)inv;
   const uint64_t t0 = (uint64_t)blockIdx.x * per, end = a.tokens - t0 < per ? a.tokens : t0 + per;
   u32x4 next[U] = {};
   const bool lines = whole_lines(a.x, a.ld_x);
-  auto load = [&](uint64_t row) {
+  auto load = [&](uint64_t row, const Piece<T, L, U, REST>& piece) {
     if (row >= end) return;
     const char* x = a.x + row * a.ld_x + (uint64_t)first * T::kSize;
     if (L == 64 && lines) piece.template load<true>(x, next);
     else piece.template load<false>(x, next);
   };
-  if constexpr (kAhead) load(t0 + g);
+  load(t0 + g, piece);
   // every wave of the workgroup goes round as often as its first
   for (uint64_t s = t0; s < end; s += G) {
     const uint64_t t = s + g;
-    if constexpr (!kAhead) load(t);
+    // places and masks worked out again for every row: kept, they spill
+    uint32_t left_here = left;
+    if constexpr (REST && !kKeep) {
+      left_here = __builtin_amdgcn_readfirstlane(left);
+      asm volatile("" : "+s"(left_here));
+    }
+    const Piece<T, L, U, REST> piece(left_here);
     u32x4 v[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) v[j] = next[j];
-    if constexpr (kAhead) load(t + G);
+    load(t + G, piece);
     float f[U][N], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < U; ++j) unpack<T>(v[j], f[j]);
@@ -317,9 +335,9 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
     if (t < end) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        if constexpr (!kAhead) {
+        if constexpr (!kKeep) {
           __builtin_amdgcn_sched_barrier(0);  // not all of them at once
-          params(j);
+          params(j, piece);
         }
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c)
@@ -335,7 +353,9 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
   }
 }
 
-// Rows of any width by one workgroup of 16 waves, which reads them three times.
+// Rows of any width by one workgroup of 16 waves, which reads them three times, the
+// later times from the caches where they hold it: 4096 x 32768 f32 305 us, 3.5 TB/s
+// of what it cannot do without.
 template <typename T, typename P>
 __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormArgs a) {
   constexpr int NW = 16;
@@ -422,8 +442,17 @@ __device__ __forceinline__ void put_grad(void* grad, bool bf16, bool accumulate,
   }
 }
 
-// L lanes of one wave a row (L < 64: W and U are 1), or W waves of U units a lane; the sums over tokens stay in
-// registers and leave as one partial sum a workgroup.
+// With h = (x - mean) rstd and g = dout weight: dx = rstd (g - mean(g) - h mean(g h)),
+// dweight = sum over the tokens of dout h, dbias of dout.  L lanes of one wave a row
+// (L < 64: W and U are 1), or W waves of U units a lane; x and dout are read once, for
+// dx and for the sums over tokens, which stay in registers in binary32 for up to
+// kSumTokens rows and leave as one partial sum a workgroup.
+//
+// Bound by HBM: two streams read, one written, 16384 x 4096 bf16 63 us, 6.5 TB/s
+// (8192 x 8192 66), the join 4.  One workgroup of 16 waves a CU leaves the fewest
+// partial sums (8.4 MB there), and its waves' registers are what one CU has: the row
+// after this one is on its way meanwhile.  131072 x 128 bf16 21 us, 4.7 TB/s; 2049 x
+// 1030 f32 10.7 and the join 3.9, launches and ramps.
 template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     const LayerNormBackwardArgs a) {
@@ -583,8 +612,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   }
 }
 
-// Sums of one row of any width, by one workgroup: sum g / width and
-// sum g h / width.
+// Rows wider than the above holds: the two sums of each first, sum g / width and sum
+// g h / width, a row a workgroup, and then dx and the sums over tokens by columns,
+// which reads both streams again: 2048 x 16384 f32 115 us, half of what reading them
+// once would allow.
 template <typename T, typename P>
 __global__ __launch_bounds__(1024) void layer_norm_row_sums_kernel(const LayerNormBackwardArgs a) {
   constexpr int NW = 16;
@@ -720,7 +751,7 @@ void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
     c.stats = a.stats ? a.stats + 2 * t : nullptr;
     const dim3 grid((uint32_t)((c.tokens + per - 1) / per)), block(64 * NW);
     if (a.width % kUnit<T> == 0) hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U, false>), grid, block, 0, stream, c, per);
-    else if constexpr (W * U < 64) hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U, true>), grid, block, 0, stream, c, per);
+    else hipLaunchKernelGGL((layer_norm_kernel<T, P, L, W, U, true>), grid, block, 0, stream, c, per);
   }
 }
 
@@ -736,7 +767,7 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   else if (kib <= 8) layer_norm_in<T, P, 64, 4, 2>(a, stream);
   else if (kib <= 16) layer_norm_in<T, P, 64, 4, 4>(a, stream);
   else if (kib <= 32) layer_norm_in<T, P, 64, 8, 4>(a, stream);
-  else if (kib <= kHeldKib<T, P> && a.width % kUnit<T> == 0) {
+  else if (kib <= kHeldKib<T, P>) {
     if constexpr (kHeldKib<T, P> > 32) layer_norm_in<T, P, 64, 16, 4>(a, stream);
   } else {
     const uint64_t most = (uint64_t)cus() * 2;
