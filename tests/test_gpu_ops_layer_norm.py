@@ -191,6 +191,38 @@ def test_in_place_and_without_parameters(torch, ops, handle, dtype, width):
         assert torch.equal(same, dx) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [3, 27, 131, 300, 505, 1999, 5003, 9999, 25001])
+def test_rows_with_a_part_of_a_unit(torch, ops, handle, dtype, width):
+    """The shared end of a row: in place, over the rows of a workgroup, as if each row came alone."""
+    rows = min(20001, (1 << 23) // width)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(width)
+    x, dout = (torch.randn(rows, width, generator=g, device="cuda").to(getattr(torch, DT[dtype])) for _ in "xd")
+    w, b = torch.randn(2, width, generator=g, device="cuda")
+    out, dx, stats = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, 2, device="cuda")
+    dw, db = torch.empty(2, width, device="cuda")
+    ops.layer_norm(x, w, b, out, stats=stats)
+    ops.layer_norm_backward(dout, x, w, stats, dx, dw, db, handle)
+    same = x.clone()
+    ops.layer_norm(same, w, b, same)
+    assert torch.equal(same, out)
+    same, dw2, db2 = dout.clone(), torch.empty_like(dw), torch.empty_like(db)
+    ops.layer_norm_backward(same, x, w, stats, same, dw2, db2, handle)
+    assert torch.equal(same, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+    for t in (0, 1, rows // 2, rows - 2, rows - 1):
+        one = torch.empty_like(x[:1])
+        ops.layer_norm(x[t:t + 1], w, b, one)
+        assert torch.equal(one[0], out[t]), t
+        ops.layer_norm_backward(dout[t:t + 1], x[t:t + 1], w, stats[t:t + 1], one, None, None, handle)
+        assert torch.equal(one[0], dx[t]), t
+    h = (x.double() - stats[:, :1].double()) * stats[:, 1:].double()
+    hg = dout.double()
+    # as dweight above: a workgroup's turns are at most 32 for any number of tokens
+    for got, terms in ((dw, hg * h), (db, hg)):
+        assert ((got.double() - terms.sum(0)).abs() <= 41 * U * terms.abs().sum(0) + TINY).all()
+
+
 @pytest.mark.parametrize("width", [5, 640, 3000, 9001, 40000])
 def test_rows_far_from_zero(torch, ops, width):
     """A constant row is 0 with any eps, and a row far from 0 is as good as the same row near it."""
