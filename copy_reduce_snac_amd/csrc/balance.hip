@@ -419,8 +419,12 @@ struct BackwardLauncher {
 
 uint32_t balance_blocks(uint64_t tokens, int experts) {
   const uint64_t rows = kLoadWaves * (experts <= 256 ? 4 : experts <= 512 ? 2 : 1);
-  // one workgroup has no other's sums to wait for: the join's launch is saved
-  if (tokens != 0 && tokens <= 2 * rows) return 1;
+  // one workgroup has no other's sums to wait for: the join's launch is saved.  Load
+  // and loss of 200 x 60 bf16 11.3 us a call among others and 6.6 in a graph, with the
+  // join 14.4 and 7.2; 509 x 60, which takes 8 turns, 11.2 and 10.3 or 14.4 and 7.1;
+  // 250 x 256 f32, 4 turns of 16 logits a lane, 14.8 and 14.7 or 14.3 and 10.8.
+  const uint64_t alone = experts <= 64 ? 4 : 2;  // turns
+  if (tokens != 0 && tokens <= alone * rows) return 1;
   const uint64_t want = (tokens + rows - 1) / rows;
   return (uint32_t)(want < kBalanceMaxBlocks ? want : kBalanceMaxBlocks);
 }

@@ -152,7 +152,7 @@ def test_gradient_without_dloss(torch, ops, handle):
     assert torch.equal(a, b) and float(a.abs().sum()) > 0
 
 
-@pytest.mark.parametrize("tokens", [0, 1, 16, 17, 8192, 8193, 131072])
+@pytest.mark.parametrize("tokens", [0, 1, 16, 17, 256, 257, 8192, 8193, 131072])
 def test_many_tokens(torch, ops, handle, tokens):
     """Equal shares add up exactly, over however many tokens."""
     e = 32
