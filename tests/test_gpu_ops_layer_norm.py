@@ -165,6 +165,25 @@ def test_many_tokens(torch, ops, handle, dtype, width, tokens):
     assert torch.equal(again, dx)
 
 
+@pytest.mark.parametrize("dtype,width,tokens", [("f32", 4100, 8193), ("bf16", 8300, 16400), ("f32", 9000, 3700), ("bf16", 20001, 3300)])
+def test_more_tokens_than_turns(torch, ops, handle, dtype, width, tokens):
+    """More than 32 turns of the workgroups that fill the chip, held rows and wide ones: whole numbers come out whole."""
+    dt = getattr(torch, DT[dtype])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(tokens)
+    x = torch.randint(-2, 3, (tokens, width), generator=g, device="cuda", dtype=torch.int8).to(dt)
+    dout = torch.randint(-2, 3, (tokens, width), generator=g, device="cuda", dtype=torch.int8).to(dt)
+    stats = torch.tensor([0.0, 1.0], device="cuda").repeat(tokens, 1)
+    dx = torch.empty_like(x)
+    dw, db = torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+    ops.layer_norm_backward(dout, x, None, stats, dx, dw, db, handle)
+    assert torch.equal(dw, (x * dout).sum(0, dtype=torch.float32)) and torch.equal(db, dout.sum(0, dtype=torch.float32))
+    for t in (0, tokens // 2, tokens - 1):
+        one = torch.empty_like(dx[:1])
+        ops.layer_norm_backward(dout[t:t + 1], x[t:t + 1], None, stats[t:t + 1], one, None, None, handle)
+        assert torch.equal(one[0], dx[t]), t
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("width", [300, 5000, 40000])
 def test_in_place_and_without_parameters(torch, ops, handle, dtype, width):
