@@ -250,7 +250,7 @@ constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 //
 // Bound by HBM: each element is read and written once.  A workgroup takes `per` rows
 // one after another, so that its parameters are loaded once for them.  TB/s read and
-// written: 32768 x 4096 bf16 90 us, 6.0; 16384 x 4096 f32 84 us, 6.4; 65536 x 1024
+// written: 32768 x 4096 bf16 84 us, 6.4; 16384 x 4096 f32 84 us, 6.4; 65536 x 1024
 // bf16 43 us, 6.3; 262144 x 128 bf16 (16 lanes a row; with 64, 3 of 4 of them idle)
 // 23 us, 5.9; 8192 x 16384 f32 194 us, 5.5: one workgroup a CU there, whose waves load
 // and store at the same times.  One row of 8192 takes 3.2 us, two joins of four
@@ -755,7 +755,10 @@ void layer_norm_in(const LayerNormArgs& a, hipStream_t stream) {
   }
 }
 
-// The narrowest shape that holds a row, in units of 1 KiB (64 lanes).
+// The narrowest shape that holds a row, in units of 1 KiB (64 lanes), and of those of
+// one size the one with the fewest waves whose registers leave 3 of them a SIMD: 32768
+// x 4096 bf16 by 2 waves of 4 units 84 us, 4 of 2 90, 8 of 1 98, 1 of 8 94; 16384 x
+// 8192 by 4 of 4 84, 2 of 8 97, 8 of 2 94.
 template <typename T, typename P>
 void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   const uint64_t bytes = (uint64_t)a.width * T::kSize, kib = (bytes + 1023) / 1024;
@@ -764,7 +767,7 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   else if (kib <= 1) layer_norm_in<T, P, 64, 1, 1>(a, stream);
   else if (kib <= 2) layer_norm_in<T, P, 64, 1, 2>(a, stream);
   else if (kib <= 4) layer_norm_in<T, P, 64, 1, 4>(a, stream);
-  else if (kib <= 8) layer_norm_in<T, P, 64, 4, 2>(a, stream);
+  else if (kib <= 8) layer_norm_in<T, P, 64, 2, 4>(a, stream);
   else if (kib <= 16) layer_norm_in<T, P, 64, 4, 4>(a, stream);
   else if (kib <= 32) layer_norm_in<T, P, 64, 8, 4>(a, stream);
   else if (kib <= kHeldKib<T, P>) {
