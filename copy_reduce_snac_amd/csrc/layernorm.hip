@@ -520,6 +520,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
         for (uint32_t c = 0; c < N; ++c) h[j][c] = (h[j][c] - mean) * rstd;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
+        // what is not of the row has no part: its h is -mean rstd, which may be infinite
+        if (!piece.whole && !piece.has(j)) continue;
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c) {
           if (c % (N / Params<T, P>::kWords ? N / Params<T, P>::kWords : 1) == 0)  // kept as it is stored
@@ -532,7 +534,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
 #pragma unroll
         for (uint32_t c = 0; c < N; ++c) d[c] = piece.counted(j, c, up[j][c]);
         c1 += unit_sum<N>([&](uint32_t c) { return d[c]; });
-        c2 += unit_dot<N>(d, h[j]);
+        if constexpr (L == 16) {  // nor have the elements before a row of less than a unit
+          float dh[N];
+#pragma unroll
+          for (uint32_t c = 0; c < N; ++c) dh[c] = piece.counted(j, c, h[j][c]);
+          c2 += unit_dot<N>(d, dh);
+        } else {
+          c2 += unit_dot<N>(d, h[j]);
+        }
       }
     }
     row_sum<L, W>(c1, c2, lds[turn]);

@@ -1,0 +1,77 @@
+"""Layer norm's gradient of rows whose mean times 1 / deviation passes binary32's
+range: lanes without an element of the row have no part in its sums.
+
+Bounds as in test_gpu_ops_layer_norm.py (u = 2^-24, h = (x - mean) rstd):
+  dx      u rstd (4 |g| + 14 mean|g| + 20 |h| mean|g h|) + half |dx|
+  dweight 41 u of the terms' sizes + half |dweight|; dbias likewise
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import ops_step_reference as ref
+from gpu_helpers import gpu_available
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+U = 2.0 ** -24
+DT = {"f32": "float32", "bf16": "bfloat16"}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+TINY = 1e-37
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+
+    torch.cuda.set_device(0)
+    return torch
+
+
+@pytest.fixture(scope="module")
+def ops(torch):
+    from copy_reduce_snac_amd import operators
+
+    return operators
+
+
+@pytest.fixture(scope="module")
+def handle(torch):
+    import copy_reduce_snac_amd as snac
+
+    h = snac.snac_init(1)
+    yield h
+    snac.snac_finalize(h)
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+# rows of less than a unit, and rows that fill a part of every shape
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [1, 3, 5, 7, 9, 32, 100, 130, 300, 1000, 1027, 3000, 5000, 5003, 9000, 17000, 20001])
+def test_gradient_of_large_rows(torch, ops, handle, dtype, width):
+    rows = 40
+    g = np.random.default_rng(width)
+    x = torch.from_numpy(g.normal(size=(rows, width)).astype(np.float32)).to(getattr(torch, DT[dtype])).cuda()
+    stats = np.concatenate(ref.moments(host(x), 1e-5), axis=1)
+    for r, (size, rstd) in enumerate([(2.0 ** 121, 1e-5 ** -0.5), (-2.0 ** 121, 1e-5 ** -0.5), (2.0 ** 64, 2.0 ** 70)]):
+        x[r] = size  # constant rows
+        stats[r] = size, rstd
+    stats = torch.from_numpy(stats.astype(np.float32)).cuda()
+    dout = torch.from_numpy(g.normal(size=(rows, width)).astype(np.float32)).to(x.dtype).cuda()
+    w = torch.from_numpy((1 + 0.2 * g.normal(size=width)).astype(np.float32)).cuda()
+    dx, dw, db = torch.empty_like(x), torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+    ops.layer_norm_backward(dout, x, w, stats, dx, dw, db, handle)
+    hx, hg, hw, hs = host(x), host(dout), host(w), host(stats)
+    want_dx, want_dw, want_db = ref.layer_norm_backward(hg, hx, hw, hs)
+    h, up = (hx - hs[:, :1]) * hs[:, 1:], hg * hw
+    mg, mgh = np.abs(up).mean(axis=1, keepdims=True), np.abs(up * h).mean(axis=1, keepdims=True)
+    bound = U * hs[:, 1:] * (4 * np.abs(up) + 14 * mg + 20 * np.abs(h) * mgh) + HALF[dtype] * np.abs(want_dx) + TINY
+    got = host(dx)
+    assert not np.isnan(got).any(), np.isnan(got).any(axis=1).nonzero()
+    assert (np.abs(got - want_dx) <= bound).all()
+    for got, sums, size in ((dw, want_dw, np.abs(hg * h).sum(axis=0)), (db, want_db, np.abs(hg).sum(axis=0))):
+        assert (np.abs(host(got) - sums) <= 41 * U * size + U * np.abs(sums) + TINY).all()
