@@ -240,6 +240,14 @@ struct Moments {
   }
 };
 
+// A row's sum over its width, rounded once (`inv`: 1 / width): the product is
+// corrected by its remainder, so that equal numbers have themselves as their mean,
+// and a constant row has no variance at all.
+__device__ __forceinline__ double mean_of(double sum, double width, double inv) {
+  const double q = sum * inv, rest = __builtin_fma(-q, width, sum);
+  return rest == rest ? __builtin_fma(rest, inv, q) : q;  // (infinite ones stay so)
+}
+
 constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 
 // out = (x - mean) rstd weight + bias, mean and variance those of the row, rstd =
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
 #pragma unroll
     for (int j = 0; j < U; ++j) params(j, piece);
   }
-  const double inv = 1.0 / (double)a.width;
+  const double width = (double)a.width, inv = 1.0 / width;
   const float inv_f = (float)inv;
   const uint64_t t0 = (uint64_t)blockIdx.x * per, end = a.tokens - t0 < per ? a.tokens : t0 + per;
   u32x4 next[U] = {};
@@ -331,7 +339,7 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
       sq += unit_dot<N>(d, d);
     }
     row_sum<L, W>(sd, sq, lds);
-    const Moments m(near, sd * inv, sq * inv, a.eps);
+    const Moments m(near, mean_of(sd, width, inv), mean_of(sq, width, inv), a.eps);
     if (t < end) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -363,7 +371,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
   __shared__ float first_sums[NW];
   __shared__ double lds[NW][2];
   const uint32_t lane = threadIdx.x & 63u, w = wave_id();
-  const double inv = 1.0 / (double)a.width;
+  const double width = (double)a.width, inv = 1.0 / width;
   for (uint64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const char* x = a.x + t * a.ld_x;
     char* out = a.out + t * a.ld_out;
@@ -387,7 +395,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
       sq += unit_dot<N>(u, u);
     });
     row_sum<64, NW>(sd, sq, lds);
-    const Moments m(near, sd * inv, sq * inv, a.eps);
+    const Moments m(near, mean_of(sd, width, inv), mean_of(sq, width, inv), a.eps);
     row([&](uint32_t e0, uint32_t left, float (&u)[N]) {
       Params<T, P> weight, bias;
       const uint32_t e = e0 + lane * N;

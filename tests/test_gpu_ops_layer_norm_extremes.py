@@ -75,3 +75,19 @@ def test_gradient_of_large_rows(torch, ops, handle, dtype, width):
     assert (np.abs(got - want_dx) <= bound).all()
     for got, sums, size in ((dw, want_dw, np.abs(hg * h).sum(axis=0)), (db, want_db, np.abs(hg).sum(axis=0))):
         assert (np.abs(host(got) - sums) <= 41 * U * size + U * np.abs(sums) + TINY).all()
+
+
+# widths whose reciprocal is exact or rounded down or up, in the shapes that hold a row and the wide one
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [1, 3, 49, 64, 237, 479, 1000, 1700, 1871, 3001, 5003, 7101, 7798, 13001, 33001, 41003])
+def test_constant_rows_without_eps(torch, ops, dtype, width):
+    """0 over 0: NaN whatever the constant, as the formula has it; with the smallest eps 0."""
+    g = np.random.default_rng(width)
+    values = (g.normal(size=64) * 10.0 ** g.uniform(-3, 5, size=64)).astype(np.float32)
+    x = torch.from_numpy(values).to(getattr(torch, DT[dtype])).cuda().unsqueeze(1).repeat(1, width)
+    out, stats = torch.empty_like(x), torch.empty(64, 2, device="cuda")
+    ops.layer_norm(x, None, None, out, eps=0.0, stats=stats)
+    assert bool(out.isnan().all()), out.isnan().all(dim=1).logical_not().nonzero().flatten().tolist()
+    assert torch.equal(stats[:, 0], x[:, 0].float())
+    ops.layer_norm(x, None, None, out, eps=2.0 ** -149, stats=stats)
+    assert bool((out == 0).all()) and torch.equal(stats[:, 0], x[:, 0].float())
