@@ -229,24 +229,26 @@ struct Piece {
 // What a row's sums give.  The mean `near` of the first pass is binary32
 // throughout and off by its sum's roundings, which matter where the row is far
 // from 0 and hardly varies: so the second pass sums the distances d from it as
-// well as their squares, and (d - rest) rstd is as good as with the exact mean.
+// well as their squares, and takes their mean off, in a fused product with rstd.
+// Where that is more than a deviation, its roundings would show: then its binary32
+// `rest` goes off first, exactly so from such d.
 struct Moments {
-  float mean, rstd, shift;  // h = d * rstd + shift
-  __device__ __forceinline__ Moments(float near, double mean_d, double mean_dd, float eps) {
-    const double var = mean_dd - mean_d * mean_d;
+  float mean, rstd, rest, shift;  // h = (d - rest) * rstd + shift
+  // the sums of the d's and of their squares; `inv`: 1 / width
+  __device__ __forceinline__ Moments(float near, double sum_d, double sum_dd, double width, double inv, float eps) {
+    // The quotient is rounded once, by its remainder, and the squares lose it in one
+    // rounding: of equal d's it is d, and their variance is 0.
+    const double q = sum_d * inv, mean_d = __builtin_fma(__builtin_fma(-q, width, sum_d), inv, q);
+    const double var = __builtin_fma(-sum_d, mean_d, sum_dd) * inv;
     mean = (float)((double)near + mean_d);
     rstd = inverse_root((var < 0.0 ? 0.0 : var) + (double)eps);
-    shift = (float)(-mean_d * (double)rstd);
+    rest = __builtin_fabs(mean_d) * (double)rstd > 1.0 ? (float)mean_d : 0.0f;
+    shift = (float)(((double)rest - mean_d) * (double)rstd);
   }
+  // whether a row of this wave has one: taken off in a branch, since it costs 8192
+  // rows of 5003 bf16 2 us of 33
+  __device__ __forceinline__ bool any_rest() const { return __any(rest != 0.0f); }
 };
-
-// A row's sum over its width, rounded once (`inv`: 1 / width): the product is
-// corrected by its remainder, so that equal numbers have themselves as their mean,
-// and a constant row has no variance at all.
-__device__ __forceinline__ double mean_of(double sum, double width, double inv) {
-  const double q = sum * inv, rest = __builtin_fma(-q, width, sum);
-  return rest == rest ? __builtin_fma(rest, inv, q) : q;  // (infinite ones stay so)
-}
 
 constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 
@@ -339,7 +341,14 @@ __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_
       sq += unit_dot<N>(d, d);
     }
     row_sum<L, W>(sd, sq, lds);
-    const Moments m(near, mean_of(sd, width, inv), mean_of(sq, width, inv), a.eps);
+    const Moments m(near, sd, sq, width, inv, a.eps);
+    if (m.any_rest()) {
+      asm volatile("");  // a branch, and not always
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (uint32_t c = 0; c < N; ++c) f[j][c] = f[j][c] - m.rest;
+    }
     if (t < end) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -395,7 +404,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
       sq += unit_dot<N>(u, u);
     });
     row_sum<64, NW>(sd, sq, lds);
-    const Moments m(near, mean_of(sd, width, inv), mean_of(sq, width, inv), a.eps);
+    const Moments m(near, sd, sq, width, inv, a.eps);
     row([&](uint32_t e0, uint32_t left, float (&u)[N]) {
       Params<T, P> weight, bias;
       const uint32_t e = e0 + lane * N;
@@ -405,7 +414,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
       else fill_params<T, P>(-0.0f, bias);
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c)
-        u[c] = __builtin_fmaf(__builtin_fmaf(u[c] - near, m.rstd, m.shift), param<T, P>(weight, c), param<T, P>(bias, c));
+        u[c] = __builtin_fmaf(__builtin_fmaf((u[c] - near) - m.rest, m.rstd, m.shift), param<T, P>(weight, c), param<T, P>(bias, c));
       const u32x4 v[1] = {pack<T>(u)};
       st_piece<T, 1, true>(out + (uint64_t)e0 * T::kSize, left, v);
     });

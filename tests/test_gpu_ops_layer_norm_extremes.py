@@ -91,3 +91,23 @@ def test_constant_rows_without_eps(torch, ops, dtype, width):
     assert torch.equal(stats[:, 0], x[:, 0].float())
     ops.layer_norm(x, None, None, out, eps=2.0 ** -149, stats=stats)
     assert bool((out == 0).all()) and torch.equal(stats[:, 0], x[:, 0].float())
+
+
+@pytest.mark.parametrize("width", [60, 130, 700, 1671, 2927, 4532, 5990, 16001, 40001])
+def test_rows_that_hardly_vary(torch, ops, width):
+    """Rows far from 0 that differ by a unit in the last place here and there, as good as any row near 0: distances from
+    a binary32 number near the mean are exact there, so the bound of test_gpu_ops_layer_norm.py stays
+    u (10 |h| + 8) + 2 u |out|, however far that number is from the mean in deviations."""
+    g = np.random.default_rng(width)
+    x = np.repeat((g.uniform(1, 2, size=(50, 1)) * 2.0 ** 24).astype(np.float32), width, axis=1)
+    for row in x:
+        at = g.integers(0, width, g.integers(1, max(2, width // 50)))
+        row[at] = np.nextafter(row[at], np.float32(np.inf))
+    t = torch.from_numpy(x).cuda()
+    out, stats = torch.empty_like(t), torch.empty(50, 2, device="cuda")
+    ops.layer_norm(t, None, None, out, stats=stats)
+    mean, rstd = ref.moments(x, np.float32(1e-5))
+    h = (x.astype(np.float64) - mean) * rstd
+    assert (np.abs(host(out) - h) <= U * (12 * np.abs(h) + 8) + TINY).all(), (np.abs(host(out) - h) / (U * (12 * np.abs(h) + 8))).max()
+    assert (np.abs(host(stats[:, :1]) - mean) <= U * np.abs(mean) + 8 * U / rstd).all()
+    assert (np.abs(host(stats[:, 1:]) - rstd) <= 8 * U * rstd).all()
