@@ -463,7 +463,8 @@ __device__ __forceinline__ void put_grad(void* grad, bool bf16, bool accumulate,
 // dweight = sum over the tokens of dout h, dbias of dout.  L lanes of one wave a row
 // (L < 64: W and U are 1), or W waves of U units a lane; x and dout are read once, for
 // dx and for the sums over tokens, which stay in registers in binary32 for up to
-// kSumTokens rows and leave as one partial sum a workgroup.
+// kSumTokens rows; those of the rows that went side by side are added up in binary64
+// and leave as one partial sum a workgroup, rounded to binary32.
 //
 // Bound by HBM: two streams read, one written, 16384 x 4096 bf16 63 us, 6.5 TB/s
 // (8192 x 8192 66), the join 4.  One workgroup of 16 waves a CU leaves the fewest
@@ -476,7 +477,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   constexpr int NW = kGradWaves, Q = NW / W, G = Q * (64 / L);
   constexpr uint32_t N = kUnit<T>, kPiece = 64u * U * N;
   __shared__ double lds[2][NW][2];
-  __shared__ __align__(16) float join[Q > 1 ? Q / 2 * W : 1][2][Q > 1 ? kPiece : 1];
+  // of the rows side by side: of a wave, and of all waves of a row; columns of a thread
+  // at a time, and whether weight's and bias's sums are joined at once
+  constexpr uint32_t kRow = L * U * N, kCols = W * kRow;
+  constexpr bool kBoth = 2 * kCols <= 64 * NW;
+  constexpr uint32_t V = kBoth ? 1 : 4;
+  __shared__ __align__(16) float join[kBoth ? 2 : 1][Q > 1 ? NW : 1][Q > 1 ? kPiece : 4];
   const uint32_t lane = threadIdx.x & 63u, l = lane % L, w = wave_id(), q = w / W;
   const uint32_t g = L < 64 ? threadIdx.x / L : q;  // the row of those side by side
   const uint32_t first = (w % W) * kPiece * (L == 64);
@@ -573,58 +579,81 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     if (live) piece.store(a.dx + t * a.ld_dx + off, v);
   }
   if (!a.dweight && !a.dbias) return;
-  // the rows that went side by side: those of a wave, then the upper half of the
-  // waves to the lower
-  if constexpr (L < 64) {
-#pragma unroll
-    for (uint32_t c = 0; c < N; ++c) {
-      if constexpr (L == 16) dw[0][c] = exchange_sum<16>(dw[0][c]), db[0][c] = exchange_sum<16>(db[0][c]);
-      dw[0][c] = exchange_sum<32>(dw[0][c]), db[0][c] = exchange_sum<32>(db[0][c]);
-    }
-  }
-  if constexpr (Q > 1) {
-#pragma unroll
-    for (uint32_t half = Q / 2; half > 0; half /= 2) {
-      __syncthreads();
-      if (q >= half && q < 2 * half) {
-        float(&to)[2][kPiece] = join[w - half * W];
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-          for (uint32_t c = 0; c < N; c += 4) {
-            *reinterpret_cast<u32x4*>(&to[0][(j * N + c) * 64 + lane * 4]) =
-                u32x4{__float_as_uint(dw[j][c]), __float_as_uint(dw[j][c + 1]), __float_as_uint(dw[j][c + 2]),
-                      __float_as_uint(dw[j][c + 3])};
-            *reinterpret_cast<u32x4*>(&to[1][(j * N + c) * 64 + lane * 4]) =
-                u32x4{__float_as_uint(db[j][c]), __float_as_uint(db[j][c + 1]), __float_as_uint(db[j][c + 2]),
-                      __float_as_uint(db[j][c + 3])};
-          }
-      }
-      __syncthreads();
-      if (q < half) {
-        const float(&from)[2][kPiece] = join[w];
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-          for (uint32_t c = 0; c < N; c += 4) {
-            const u32x4 vw = *reinterpret_cast<const u32x4*>(&from[0][(j * N + c) * 64 + lane * 4]);
-            const u32x4 vb = *reinterpret_cast<const u32x4*>(&from[1][(j * N + c) * 64 + lane * 4]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dw[j][c + i] += __uint_as_float(vw[i]);
-              db[j][c + i] += __uint_as_float(vb[i]);
-            }
-          }
-      }
-    }
-  }
-  if (q != 0 || l != lane) return;
   float* part = a.partial + (uint64_t)blockIdx.x * 2 * a.width;
+  const bool alone = gridDim.x == 1;  // nothing to join
+  if constexpr (Q > 1) {
+    // The sums of the rows that went side by side, in the order of a row's elements:
+    // a thread adds up a column's in binary64.
+    auto put = [&](const float (&f)[U][N], float (&to)[kPiece]) {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (uint32_t c = 0; c < N; c += 4)
+          *reinterpret_cast<u32x4*>(&to[(j * 64 + lane) * N + c]) =
+              u32x4{__float_as_uint(f[j][c]), __float_as_uint(f[j][c + 1]), __float_as_uint(f[j][c + 2]), __float_as_uint(f[j][c + 3])};
+    };
+    auto columns = [&](const float (&from)[NW][kPiece], uint32_t col, void* grad, float* part) {
+      const uint32_t own = col / N * N;
+      if (own >= a.width) return;
+      double sum[V];
+#pragma unroll
+      for (uint32_t c = 0; c < V; ++c) sum[c] = 0.0;
+#pragma unroll
+      for (uint32_t k = 0; k < Q; ++k)
+#pragma unroll
+        for (uint32_t sub = 0; sub < 64 / L; ++sub) {
+          const float* f = &from[k * W + col / kRow][sub * kRow + col % kRow];
+          if constexpr (V == 4) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(f);
+#pragma unroll
+            for (uint32_t c = 0; c < V; ++c) sum[c] += __uint_as_float(v[c]);
+          } else {
+            sum[0] += *f;
+          }
+        }
+      // of the unit that ends where the row does another has the first elements
+      const int32_t e = (int32_t)(REST && own + N > a.width ? col + a.width - N - own : col);
+      if (V == 4 && !alone && e >= (int32_t)own) {
+        u32x4 v;
+#pragma unroll
+        for (uint32_t c = 0; c < V; ++c) v[c] = __float_as_uint((float)sum[c]);
+        return st_unit<false>(reinterpret_cast<char*>(part + e), v);
+      }
+#pragma unroll
+      for (uint32_t c = 0; c < V; ++c) {
+        const int32_t at = e + (int32_t)c;
+        if (at < (int32_t)own) continue;
+        if (!alone) part[at] = (float)sum[c];
+        else if (grad) put_grad(grad, a.grad_bf16, a.accumulate, at, sum[c]);
+      }
+    };
+    if constexpr (kBoth) {
+      put(dw, join[0][w]);
+      put(db, join[1][w]);
+      __syncthreads();
+      const uint32_t i = threadIdx.x;
+      if (i < kCols) columns(join[0], i, a.dweight, part);
+      else if (i < 2 * kCols) columns(join[1], i - kCols, a.dbias, part + a.width);
+    } else {
+      // one after the other, four columns at a time (both at once and by single columns
+      // took 128 KiB of LDS and 8192 rows of 5003 bf16 4 us more of 60)
+      put(dw, join[0][w]);
+      __syncthreads();
+#pragma unroll
+      for (uint32_t i = V * threadIdx.x; i < kCols; i += V * 64 * NW) columns(join[0], i, a.dweight, part);
+      __syncthreads();
+      put(db, join[0][w]);
+      __syncthreads();
+#pragma unroll
+      for (uint32_t i = V * threadIdx.x; i < kCols; i += V * 64 * NW) columns(join[0], i, a.dbias, part + a.width);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     if (!piece.has(j)) continue;
     const int64_t e = (int32_t)(first + (uint32_t)piece.at(j));
-    if (gridDim.x == 1) {  // nothing to join
+    if (alone) {
 #pragma unroll
       for (uint32_t c = 0; c < N; ++c) {
         if (c < piece.skip(j)) continue;

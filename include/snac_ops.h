@@ -268,8 +268,9 @@ snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, cons
  *   dbias   = sum over the tokens of dout       (NULL: not wanted)
  * stats: what snac_layer_norm left for these rows.  A row's sums are binary32
  * within 16 bytes and binary64 over them; the sums over tokens are binary32 over
- * at most 32 tokens, binary64 over those, rounded to binary32 and that to
- * grad_dtype.
+ * at most 32 tokens and binary64 over those.  On the way a workgroup's sum (of 32
+ * tokens, of rows of up to 16 KiB 64 to 2048) is rounded to binary32, the whole to
+ * binary32 and that to grad_dtype.
  *   accumulate  0: dweight and dbias are written; 1: the sums are added to them
  *               before the rounding
  * dx may be dout itself (same ld).  Scratch is the context's staging rings:
