@@ -430,6 +430,8 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(const LayerNormAr
 
 constexpr int kGradWaves = 16;  // of a workgroup
 constexpr uint32_t kGradBlocks = 256;
+constexpr uint64_t kGradPartial = 32ull << 20;  // bytes of partial sums
+constexpr uint64_t kGradAgain = 256;            // times kGradBlocks in a launch at most
 constexpr uint32_t kAloneTurns = 2;
 
 // N binary32 values to `p`, but the first `skip`.
@@ -464,7 +466,9 @@ __device__ __forceinline__ void put_grad(void* grad, bool bf16, bool accumulate,
 // (L < 64: W and U are 1), or W waves of U units a lane; x and dout are read once, for
 // dx and for the sums over tokens, which stay in registers in binary32 for up to
 // kSumTokens rows; those of the rows that went side by side are added up in binary64
-// and leave as one partial sum a workgroup, rounded to binary32.
+// and leave as one partial sum a workgroup, rounded to binary32.  More tokens than
+// kGradPartial bytes of partial sums serve take several launches, each with a join
+// into the call's sums.
 //
 // Bound by HBM: two streams read, one written, 16384 x 4096 bf16 63 us, 6.5 TB/s
 // (8192 x 8192 66), the join 4.  One workgroup of 16 waves a CU leaves the fewest
@@ -473,7 +477,7 @@ __device__ __forceinline__ void put_grad(void* grad, bool bf16, bool accumulate,
 // 1030 f32 10.7 and the join 3.9, launches and ramps.
 template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
-    const LayerNormBackwardArgs a) {
+    const LayerNormBackwardArgs a, const uint32_t per) {
   constexpr int NW = kGradWaves, Q = NW / W, G = Q * (64 / L);
   constexpr uint32_t N = kUnit<T>, kPiece = 64u * U * N;
   __shared__ double lds[2][NW][2];
@@ -502,9 +506,16 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     for (uint32_t c = 0; c < N; ++c) dw[j][c] = db[j][c] = 0.0f;
   const float inv = (float)(1.0 / (double)a.width);
   const bool lines = whole_lines(a.x, a.ld_x) && whole_lines(a.dout, a.ld_dout);
+  // kGradBlocks workgroups go at once, the rows of their same turn side by side; as many
+  // again take the rows after theirs
+  const uint32_t before = blockIdx.x / kGradBlocks * kGradBlocks;
+  const uint32_t at_once = gridDim.x - before < kGradBlocks ? gridDim.x - before : kGradBlocks;
+  const uint64_t step = (uint64_t)at_once * G, first_row = (uint64_t)before * per;
+  const uint64_t start = first_row + (blockIdx.x - before) * G;
+  const uint64_t end = a.tokens - first_row < (uint64_t)at_once * per ? a.tokens : first_row + (uint64_t)at_once * per;
   u32x4 next_x[U] = {}, next_g[U] = {};
   auto load = [&](uint64_t t, const Piece<T, L, U, REST>& piece) {
-    if (t >= a.tokens) return;
+    if (t >= end) return;
     if (L == 64 && lines) {
       piece.template load<true>(a.x + t * a.ld_x + off, next_x);
       piece.template load<true>(a.dout + t * a.ld_dout + off, next_g);
@@ -513,13 +524,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
       piece.template load<false>(a.dout + t * a.ld_dout + off, next_g);
     }
   };
-  // rows of all workgroups' same turn lie side by side
-  const uint64_t step = (uint64_t)gridDim.x * G;
-  load((uint64_t)blockIdx.x * G + g, piece);
+  load(start + g, piece);
   uint32_t turn = 0;
-  for (uint64_t s = (uint64_t)blockIdx.x * G; s < a.tokens; s += step, turn ^= 1) {
+  for (uint64_t s = start; s < end; s += step, turn ^= 1) {
     const uint64_t t = s + g;
-    const bool live = t < a.tokens;
+    const bool live = t < end;
     // its places and masks are worked out again for every row: kept, they spill
     uint32_t left_here = left;
     if constexpr (REST) {
@@ -580,7 +589,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   }
   if (!a.dweight && !a.dbias) return;
   float* part = a.partial + (uint64_t)blockIdx.x * 2 * a.width;
-  const bool alone = gridDim.x == 1;  // nothing to join
+  const bool alone = gridDim.x == 1 && !a.whole;  // nothing to join
   if constexpr (Q > 1) {
     // The sums of the rows that went side by side, in the order of a row's elements:
     // a thread adds up a column's in binary64.
@@ -717,13 +726,16 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(const LayerNorm
   const uint32_t left = a.width - (uint32_t)e0, e = (uint32_t)e0 + lane * N;
   Params<T, P> weight;
   if (a.weight && e < a.width) ld_params<T, P>(a.weight, e, a.width, weight);
-  const uint64_t blocks = (a.tokens + per - 1) / per;
-  for (uint64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
-    const uint64_t t0 = b * per, end = a.tokens - t0 < per ? a.tokens : t0 + per;
+  const uint64_t t0 = (uint64_t)blockIdx.y * per, end = a.tokens - t0 < per ? a.tokens : t0 + per;
+  double sum_w[N], sum_b[N];
+#pragma unroll
+  for (uint32_t c = 0; c < N; ++c) sum_w[c] = sum_b[c] = 0.0;
+  for (uint64_t r0 = t0; r0 < end; r0 += kSumTokens) {
+    const uint64_t r1 = end - r0 < kSumTokens ? end : r0 + kSumTokens;
     float dw[N], db[N];
 #pragma unroll
     for (uint32_t c = 0; c < N; ++c) dw[c] = db[c] = 0.0f;
-    for (uint64_t t = t0; t < end; ++t) {
+    for (uint64_t t = r0; t < r1; ++t) {
       u32x4 vx[1], vg[1];
       ld_piece<T, 1, true>(a.x + t * a.ld_x + e0 * T::kSize, left, vx);
       ld_piece<T, 1, true>(a.dout + t * a.ld_dout + e0 * T::kSize, left, vg);
@@ -743,32 +755,36 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(const LayerNorm
       vx[0] = pack<T>(h);
       st_piece<T, 1, true>(a.dx + t * a.ld_dx + e0 * T::kSize, left, vx);
     }
-    if (!a.partial) continue;
-    float* part = a.partial + b * 2 * a.width;
 #pragma unroll
-    for (uint32_t c = 0; c < N; ++c) {
-      if (e + c >= a.width) continue;
-      part[e + c] = dw[c];
-      part[(uint64_t)a.width + e + c] = db[c];
-    }
+    for (uint32_t c = 0; c < N; ++c) sum_w[c] += dw[c], sum_b[c] += db[c];
+  }
+  if (!a.partial) return;
+  float* part = a.partial + (uint64_t)blockIdx.y * 2 * a.width;
+#pragma unroll
+  for (uint32_t c = 0; c < N; ++c) {
+    if (e + c >= a.width) continue;
+    part[e + c] = (float)sum_w[c];
+    part[(uint64_t)a.width + e + c] = (float)sum_b[c];
   }
 }
 
 // dweight and dbias from the partial sums: 64 columns a workgroup, its waves
-// taking every 16th partial sum.  256 of 4096 columns each (8.4 MB) 4.2 us.
+// taking every 16th partial sum.  256 of 4096 columns each (8.4 MB) 4.2 us.  Those of
+// a call's several launches go through its sums in binary64.
 constexpr int kJoinWaves = 16;
 constexpr uint64_t kJoinGrid = 1u << 20;
-__global__ __launch_bounds__(64 * kJoinWaves) void layer_norm_join_kernel(const LayerNormBackwardArgs a, const uint32_t blocks) {
+__global__ __launch_bounds__(64 * kJoinWaves) void layer_norm_join_kernel(const LayerNormBackwardArgs a, const uint32_t blocks,
+                                                                          const bool later, const bool last) {
   __shared__ double lds[kJoinWaves][64];
   const uint32_t lane = threadIdx.x & 63u, w = wave_id();
   const bool second = blockIdx.y != 0;
   void* out = second ? a.dbias : a.dweight;
   if (!out) return;
   for (uint64_t c0 = (uint64_t)blockIdx.x * 64; c0 < a.width; c0 += (uint64_t)gridDim.x * 64) {
-    const uint64_t col = c0 + lane;
+    const uint64_t col = c0 + lane, at = (second ? a.width : 0) + col;
     double sum = 0.0;
     if (col < a.width) {
-      const float* p = a.partial + (second ? a.width : 0) + col;
+      const float* p = a.partial + at;
 #pragma unroll 8
       for (uint32_t b = w; b < blocks; b += kJoinWaves) sum += p[(uint64_t)b * 2 * a.width];
     }
@@ -777,7 +793,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void layer_norm_join_kernel(const 
     if (w == 0 && col < a.width) {
 #pragma unroll
       for (int i = 1; i < kJoinWaves; ++i) sum += lds[i][lane];
-      put_grad(out, a.grad_bf16, a.accumulate, col, sum);
+      if (later) sum += a.whole[at];
+      if (last) put_grad(out, a.grad_bf16, a.accumulate, col, sum);
+      else a.whole[at] = sum;
     }
     __syncthreads();  // lds is free
   }
@@ -834,11 +852,29 @@ void layer_norm_any(const LayerNormArgs& a, hipStream_t stream) {
   }
 }
 
+void layer_norm_join(const LayerNormBackwardArgs& a, uint64_t blocks, bool later, bool last, hipStream_t stream) {
+  const uint64_t cols = ((uint64_t)a.width + 63) / 64;
+  hipLaunchKernelGGL(layer_norm_join_kernel, dim3((uint32_t)(cols < kJoinGrid ? cols : kJoinGrid), 2), dim3(64 * kJoinWaves),
+                     0, stream, a, (uint32_t)blocks, later, last);
+}
+
 template <typename T, typename P, int L, int W, int U>
 void layer_norm_backward_in(const LayerNormBackwardArgs& a, const LayerNormShape& s, hipStream_t stream) {
-  const dim3 grid((uint32_t)s.blocks), block(64 * kGradWaves);
-  if (a.width % kUnit<T> == 0) hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U, false>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U, true>), grid, block, 0, stream, a);
+  const uint64_t most = s.blocks * s.per;  // tokens of a launch
+  LayerNormBackwardArgs c = a;
+  for (uint64_t t = 0; t < a.tokens; t += most) {
+    c.tokens = a.tokens - t < most ? a.tokens - t : most;
+    c.dout = a.dout + t * a.ld_dout;
+    c.x = a.x + t * a.ld_x;
+    c.stats = a.stats + 2 * t;
+    c.dx = a.dx + t * a.ld_dx;
+    const uint64_t blocks = (c.tokens + s.per - 1) / s.per;
+    const dim3 grid((uint32_t)blocks), block(64 * kGradWaves);
+    if (a.width % kUnit<T> == 0) hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U, false>), grid, block, 0, stream, c, s.per);
+    else hipLaunchKernelGGL((layer_norm_backward_kernel<T, P, L, W, U, true>), grid, block, 0, stream, c, s.per);
+    if ((a.dweight || a.dbias) && (blocks != 1 || a.whole))
+      layer_norm_join(c, blocks, t != 0, a.tokens - t <= most, stream);
+  }
 }
 
 template <typename T, typename P>
@@ -848,9 +884,9 @@ void layer_norm_backward_any(const LayerNormBackwardArgs& a, const LayerNormShap
     const uint64_t most = (uint64_t)cus() * 2;
     hipLaunchKernelGGL((layer_norm_row_sums_kernel<T, P>), dim3((uint32_t)(a.tokens < most ? a.tokens : most)),
                        dim3(1024), 0, stream, a);
-    const uint32_t y = s.blocks < 32768 ? (uint32_t)s.blocks : 32768u;
-    hipLaunchKernelGGL((layer_norm_columns_kernel<T, P>), dim3((uint32_t)((kib + 3) / 4), y), dim3(256), 0, stream, a,
-                       s.per);
+    hipLaunchKernelGGL((layer_norm_columns_kernel<T, P>), dim3((uint32_t)((kib + 3) / 4), (uint32_t)s.blocks), dim3(256), 0,
+                       stream, a, s.per);
+    if (a.dweight || a.dbias) layer_norm_join(a, s.blocks, false, true, stream);
   } else if (bytes <= 256) layer_norm_backward_in<T, P, 16, 1, 1>(a, s, stream);
   else if (bytes <= 512) layer_norm_backward_in<T, P, 32, 1, 1>(a, s, stream);
   else if (kib <= 1) layer_norm_backward_in<T, P, 64, 1, 1>(a, s, stream);
@@ -871,7 +907,7 @@ hipError_t launch_layer_norm(const LayerNormArgs& a, bool bf16, bool param_bf16,
 
 LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize) {
   const uint64_t bytes = width * esize;
-  LayerNormShape s{0, kSumTokens, bytes > kHeldBackwardKib * 1024};
+  LayerNormShape s{0, kSumTokens, bytes > kHeldBackwardKib * 1024, false};
   if (tokens == 0) return s;
   // rows side by side in a workgroup of layer_norm_backward_kernel, and how many
   // workgroups they are dealt out to
@@ -884,29 +920,31 @@ LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize)
   if (tokens <= rows * kAloneTurns) turns = (tokens + rows - 1) / rows;
   // more tokens than those have turns for: as many workgroups again, and as even
   // (20000 rows of 6000 bf16 in turns of 32, 313 workgroups of one a CU, 180 us;
-  // evenly 137)
-  if (turns > kSumTokens) {
-    most *= (turns + kSumTokens - 1) / kSumTokens;
-    turns = (tokens + rows * most - 1) / (rows * most);
+  // evenly 137), while their partial sums are few; then several launches, so that the
+  // scratch does not grow with the tokens (131072 rows of 8192 bf16 in one 1150 us and
+  // 134 MB of partial sums, in four 1075; 20000 of 5999 in two 155, in one 147).  A
+  // workgroup of layer_norm_columns_kernel takes any number of tokens.
+  uint64_t launches = 1;
+  if (turns > kSumTokens && !s.row_sums) {
+    const uint64_t groups = (turns + kSumTokens - 1) / kSumTokens;
+    uint64_t again = kGradPartial / (most * 2 * width * 4);
+    again = again < 1 ? 1 : again > kGradAgain ? kGradAgain : again;
+    again = again < groups ? again : groups;
+    launches = (groups + again - 1) / again;
+    most *= again;
+    turns = (tokens + rows * most * launches - 1) / (rows * most * launches);
   }
+  s.runs = launches > 1;
   s.per = (uint32_t)(rows * turns);
-  s.blocks = (tokens + s.per - 1) / s.per;
+  s.blocks = s.runs ? most : (tokens + s.per - 1) / s.per;
   return s;
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const LayerNormShape& s, bool bf16,
                                       bool param_bf16, hipStream_t stream) {
-  if (a.tokens) {
-    if (bf16) param_bf16 ? layer_norm_backward_any<BF16, BF16>(a, s, stream) : layer_norm_backward_any<BF16, F32>(a, s, stream);
-    else param_bf16 ? layer_norm_backward_any<F32, BF16>(a, s, stream) : layer_norm_backward_any<F32, F32>(a, s, stream);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if ((a.dweight || a.dbias) && (s.blocks != 1 || s.row_sums)) {
-    const uint64_t cols = ((uint64_t)a.width + 63) / 64;
-    hipLaunchKernelGGL(layer_norm_join_kernel, dim3((uint32_t)(cols < kJoinGrid ? cols : kJoinGrid), 2),
-                       dim3(64 * kJoinWaves), 0, stream, a, (uint32_t)s.blocks);
-  }
+  if (a.tokens == 0) layer_norm_join(a, 0, false, true, stream);  // zeros
+  else if (bf16) param_bf16 ? layer_norm_backward_any<BF16, BF16>(a, s, stream) : layer_norm_backward_any<BF16, F32>(a, s, stream);
+  else param_bf16 ? layer_norm_backward_any<F32, BF16>(a, s, stream) : layer_norm_backward_any<F32, F32>(a, s, stream);
   return hipGetLastError();
 }
 

@@ -218,13 +218,14 @@ hipError_t launch_layer_norm(const LayerNormArgs& a, bool bf16, bool param_bf16,
 
 // How the rows of a gradient are dealt out: `per` rows to each of the `blocks`
 // workgroups, which leave one partial sum each.  row_sums: rows too wide for a
-// workgroup's registers, whose own sums are made by a launch before.
+// workgroup's registers, whose own sums are made by a launch before.  runs: more
+// tokens than those, in launches of which each is joined into the call's sums.
 struct LayerNormShape {
   uint64_t blocks;
   uint32_t per;
-  bool row_sums;
+  bool row_sums, runs;
 };
-constexpr uint32_t kLayerNormMaxBlocks = 1u << 22;  // a launch has fewer than 2^32 threads
+constexpr uint64_t kLayerNormMaxTokens = 1ull << 33;  // of a gradient
 LayerNormShape layer_norm_shape(uint64_t tokens, uint64_t width, uint64_t esize);
 struct LayerNormBackwardArgs {
   const char* dout;
@@ -241,6 +242,7 @@ struct LayerNormBackwardArgs {
   void* dbias;
   bool grad_bf16, accumulate;
   float* partial;   // [blocks][2][width], nullptr: neither is wanted
+  double* whole;    // [2][width] with runs, else nullptr
   float* row_sums;  // [tokens][2], see LayerNormShape
 };
 hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, const LayerNormShape& s, bool bf16,

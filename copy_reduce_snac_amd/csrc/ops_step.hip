@@ -109,9 +109,9 @@ snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, cons
 
 size_t snac_layer_norm_scratch(size_t tokens, size_t width, snac_dtype dtype) {
   if (!is_float(dtype) || tokens > SNAC_MAX_BYTES || width >= kMaxWidth || tokens == 0 || width == 0) return 0;
+  if (tokens >= kLayerNormMaxTokens) return 0;
   const LayerNormShape s = layer_norm_shape(tokens, width, esize(dtype));
-  if (s.blocks >= kLayerNormMaxBlocks) return 0;
-  return up256((uint64_t)s.blocks * 2 * width * 4) + (s.row_sums ? tokens * 8 : 0);
+  return up256(s.blocks * 2 * width * 4) + (s.runs ? up256(2 * width * 8) : 0) + (s.row_sums ? tokens * 8 : 0);
 }
 
 snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_dout, const void* x, size_t ld_x,
@@ -137,10 +137,11 @@ snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_
   const uint64_t al[] = {es, es, ps, 4, es, gs, gs};
   TRY(check_spans(s, al, dx, dout));
   if (width == 0) return ok();
+  if (tokens >= kLayerNormMaxTokens) return fail(SNAC_E_ARG, "%zu tokens: more than one call takes", tokens);
   const LayerNormShape shape = layer_norm_shape(tokens, width, es);
-  if (shape.blocks >= kLayerNormMaxBlocks) return fail(SNAC_E_ARG, "%zu tokens: more than one call takes", tokens);
-  const uint64_t partial = dweight || dbias ? up256((uint64_t)shape.blocks * 2 * width * 4) : 0;
-  const uint64_t bytes = partial + (shape.row_sums ? tokens * 8 : 0);
+  const uint64_t partial = dweight || dbias ? up256(shape.blocks * 2 * width * 4) : 0;
+  const uint64_t whole = partial && shape.runs ? up256(2 * width * 8) : 0;
+  const uint64_t bytes = partial + whole + (shape.row_sums ? tokens * 8 : 0);
   char* scratch = nullptr;
   if (bytes) TRY(ctx_scratch(ctx, bytes, "snac_layer_norm_backward", &scratch));
   if (tokens == 0 && (accumulate || !(dweight || dbias))) return ok();
@@ -160,7 +161,8 @@ snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_
   a.grad_bf16 = grad_dtype == SNAC_BF16;
   a.accumulate = accumulate != 0;
   a.partial = partial ? reinterpret_cast<float*>(scratch) : nullptr;
-  a.row_sums = shape.row_sums ? reinterpret_cast<float*>(scratch + partial) : nullptr;
+  a.whole = whole ? reinterpret_cast<double*>(scratch + partial) : nullptr;
+  a.row_sums = shape.row_sums ? reinterpret_cast<float*>(scratch + partial + whole) : nullptr;
   const hipError_t e =
       launch_layer_norm_backward(a, shape, dtype == SNAC_BF16, param_dtype == SNAC_BF16, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "snac_layer_norm_backward launch");

@@ -276,7 +276,7 @@ snac_status snac_layer_norm(const void* x, size_t ld_x, const void* weight, cons
  * dx may be dout itself (same ld).  Scratch is the context's staging rings:
  * snac_layer_norm_scratch bytes (SNAC_E_ARG if the rings together are smaller);
  * without dweight and dbias rows of up to 32 KiB need none, and ctx may be NULL.
- * Calls of 2^27 tokens and more may be refused (SNAC_E_ARG).
+ * Calls of 2^33 tokens and more are refused (SNAC_E_ARG).
  */
 snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_dout, const void* x, size_t ld_x,
                                      const void* weight, snac_dtype param_dtype, const float* stats, size_t tokens,
@@ -285,7 +285,10 @@ snac_status snac_layer_norm_backward(snac_ctx* ctx, const void* dout, size_t ld_
 
 /* Scratch of snac_layer_norm_backward with dweight or dbias, rows of `dtype`:
  * staging bytes per rank times ranks must be at least this (0 for arguments that
- * the call refuses). */
+ * the call refuses).  For rows of up to 32 KiB at most 32 MiB, 16 bytes an element
+ * of the width and 512, whatever the tokens; for wider ones at most 32 MiB and 8
+ * bytes an element of the width, and 8 bytes a token.  (A context of one rank has 64
+ * MiB by default.) */
 size_t snac_layer_norm_scratch(size_t tokens, size_t width, snac_dtype dtype);
 
 /* --------------------------------------------------------- balance loss */

@@ -66,3 +66,46 @@ def test_rows_side_by_side(torch, ops, handle, dtype, width, side, groups):
     assert torch.equal(dw, want * x[0].float())
     ops.layer_norm_backward(dout, x, None, stats, dx, dw, db, handle, accumulate=True)
     assert torch.equal(db, 2 * want) and torch.equal(dw, 2 * want * x[0].float())
+
+
+# rows that a workgroup takes one at a time, rows side by side, and (36 KiB) those of which a workgroup takes columns
+@pytest.mark.parametrize("dtype,width,side,groups", [("bf16", 16384, 1, 256), ("f32", 5003, 1, 256), ("bf16", 3000, 4, 256),
+                                                     ("f32", 64, 64, 256), ("f32", 9216, 0, 114)])
+def test_more_than_32_turns(torch, ops, handle, dtype, width, side, groups):
+    """2^24, then nothing, after 32 turns ones and at the end -2^24: 40 turns of the workgroups that fill the chip."""
+    v = torch.zeros(40, groups * max(side, 1), device="cuda")
+    v[0], v[32:39], v[39] = BIG, 1.0, -BIG
+    if side == 0:  # the rows of a workgroup follow one another there
+        v = v.t()
+    tokens = v.numel()
+    dout = v.reshape(tokens, 1).repeat(1, width).to(getattr(torch, DT[dtype]))
+    x = torch.ones_like(dout)
+    stats = torch.tensor([0.0, 1.0], device="cuda").repeat(tokens, 1)
+    dx, dw, db = torch.empty_like(x), torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+    want = torch.full((width,), 7.0 * tokens / 40, device="cuda")
+    for _ in range(2):  # the scratch of one call does not matter to the next
+        ops.layer_norm_backward(dout, x, None, stats, dx, dw, db, handle)
+        assert torch.equal(db, want) and torch.equal(dw, want), (db.min(), db.max(), want[0])
+    ops.layer_norm_backward(dout, x, None, stats, dx, dw, None, handle, accumulate=True)
+    assert torch.equal(dw, 2 * want)
+
+
+@pytest.mark.parametrize("dtype,width,tokens", [("bf16", 16384, 32768), ("bf16", 12288, 40001), ("bf16", 8192, 131072), ("f32", 16384, 16384)])
+def test_many_tokens_on_a_default_context(torch, ops, handle, dtype, width, tokens):
+    """The partial sums' scratch does not grow with the tokens: whole numbers come out whole."""
+    dt = getattr(torch, DT[dtype])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(tokens)
+    x, dout = (torch.randint(-2, 3, (tokens, width), generator=g, device="cuda", dtype=torch.int8).to(dt) for _ in "xd")
+    stats = torch.tensor([0.0, 1.0], device="cuda").repeat(tokens, 1)
+    dx, dw, db = torch.empty_like(x), torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+    ops.layer_norm_backward(dout, x, None, stats, dx, dw, db, handle)
+    want_w, want_b = torch.zeros(width, device="cuda"), torch.zeros(width, device="cuda")
+    for t in range(0, tokens, 4096):  # sums below 2^24, exact
+        want_b += dout[t:t + 4096].sum(0, dtype=torch.float32)
+        want_w += (dout[t:t + 4096] * x[t:t + 4096]).sum(0, dtype=torch.float32)
+    assert torch.equal(dw, want_w) and torch.equal(db, want_b)
+    for t in (0, tokens // 2, tokens - 1):
+        one = torch.empty_like(dx[:1])
+        ops.layer_norm_backward(dout[t:t + 1], x[t:t + 1], None, stats[t:t + 1], one, None, None, handle)
+        assert torch.equal(one[0], dx[t]), t
