@@ -515,15 +515,18 @@ def distill_backward(logits, ids, teacher, stats, dlogits, *, dloss=None, scale:
                      vocab: int | None = None, temperature: float = 1.0, stream=None) -> None:
     """``dlogits`` (may be ``logits``): the gradient of scale * sum of dloss *
     loss with respect to ``logits``, the whole vocabulary's or (with ``first``
-    and ``vocab``) a shard's.  ``stats`` is ``distill``'s or ``distill_join``'s;
-    ``dloss`` [tokens] (float32) may be None for all 1."""
+    and ``vocab``, also of the first and last one) a shard's.  ``stats`` is
+    ``distill``'s or ``distill_join``'s; ``dloss`` [tokens] (float32) may be None
+    for all 1."""
+    if first != 0 and vocab is None:  # the teacher's distribution is over all of its choices
+        raise ValueError("distill_backward: a shard (first) needs the whole vocabulary's size (vocab)")
     ld, ld_d = _matrix(logits, "distill_backward: logits"), _matrix(dlogits, "distill_backward: dlogits")
     dt = _float(logits, "distill_backward: logits")
     _pair(logits, dlogits, "distill_backward: logits and dlogits")
     t, w = logits.shape
     if dlogits.shape != logits.shape:
         raise ValueError("distill_backward: dlogits must have the shape of logits")
-    h = _teacher(ids, teacher, t, first + w if vocab is None else vocab, temperature, "distill_backward")
+    h = _teacher(ids, teacher, t, w if vocab is None else vocab, temperature, "distill_backward")
     _packed(stats, (t, 2), torch.float32, "distill_backward: stats")
     if dloss is not None:
         _packed(dloss, (t,), torch.float32, "distill_backward: dloss")

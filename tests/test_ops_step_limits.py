@@ -1,4 +1,5 @@
-"""Layer norm's scratch, on the CPU."""
+"""Layer norm's scratch, and calls of distillation that name a shard without its
+vocabulary, on the CPU."""
 from __future__ import annotations
 
 import pytest
@@ -22,3 +23,20 @@ def test_layer_norm_scratch_fits_a_default_context(dtype, size):
                 assert 0 < got <= (32 << 20) + 8 * width + 256 + 8 * tokens, (tokens, width)
     for tokens, width in ((32768, 16384), (65536, 12288), (131072, 8192), (16384, 16384)):
         assert snac.snac_layer_norm_scratch(tokens, width, dtype) <= DEFAULT, (tokens, width)
+
+
+def test_a_shard_needs_its_vocabulary():
+    """Without it every column above the shard would be no choice, and the teacher's distribution another."""
+    import torch
+
+    from copy_reduce_snac_amd import operators as ops
+
+    x, st = torch.zeros(4, 16), torch.zeros(4, 2)
+    ids, t = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for first in (16, -16):
+        with pytest.raises(ValueError, match="vocab"):
+            ops.distill_backward(x, ids, t, st, x, first=first)
+    with pytest.raises(ValueError, match="current device"):
+        ops.distill_backward(x, ids, t, st, x, first=16, vocab=64)
+    with pytest.raises(ValueError, match="current device"):
+        ops.distill_backward(x, ids, t, st, x)
