@@ -44,6 +44,8 @@ ROUTER = dict(score="softmax", renorm=True)
 class DistillStep:
     def __init__(self, ranks=4, tokens=256, width=256, vocab=4096, experts=8, topk=2, choices=16, temperature=2.0,
                  balance=0.05, seed=0):
+        if vocab % ranks:  # a column that no rank held would be a choice without a logit
+            raise ValueError(f"vocab {vocab} is not a multiple of ranks {ranks}: the shards are equal")
         self.n, self.tokens, self.width, self.topk, self.experts = ranks, tokens, width, topk, experts
         self.local, self.vocab, self.temperature, self.balance = vocab // ranks, vocab, temperature, balance
         g = torch.Generator(device="cuda")

@@ -1,11 +1,15 @@
-"""Layer norm's scratch, and calls of distillation that name a shard without its
-vocabulary, on the CPU."""
+"""Layer norm's scratch, calls of distillation that name a shard without its
+vocabulary, and a vocabulary that the example cannot cut, on the CPU."""
 from __future__ import annotations
+
+import os
+import sys
 
 import pytest
 
 import copy_reduce_snac_amd as snac
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DEFAULT = 64 << 20  # staging bytes per rank of a context that names no size
 
 
@@ -40,3 +44,14 @@ def test_a_shard_needs_its_vocabulary():
         ops.distill_backward(x, ids, t, st, x, first=16, vocab=64)
     with pytest.raises(ValueError, match="current device"):
         ops.distill_backward(x, ids, t, st, x)
+
+
+def test_example_refuses_a_vocabulary_in_uneven_shards():
+    """The example's shards are equal: a column that no rank held would be a choice without logits."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import distill_step
+    finally:
+        sys.path.pop(0)
+    with pytest.raises(ValueError, match="vocab"):
+        distill_step.DistillStep(ranks=4, tokens=16, width=64, vocab=513)
