@@ -1,0 +1,130 @@
+"""The loss against a teacher's top logits at the ends of the accepted
+temperatures, whole and in shards, values against tests/ops_step_reference.py.
+
+Bounds, u = 2^-24, as test_gpu_ops_distill.py derives them: an exponential of
+arg = (x - top) / temperature is off by (2 + 2.5 |arg|) u of itself.
+  S     the terms' errors, and 8 u of the sum; a rounding more for a shard's part
+        and one for the joint sum
+  q     q (r + sum q r + 2) u with r = 2 + 2.5 |arg|
+  loss  sum of q's errors times |log q - log p| + 1, S's and the teacher's sum's
+        relative errors, a rounding; joined from shards a rounding of each
+        part's D (its size) and Q (times the distance of the shard's maximum)
+  dz    |factor| u (p (r + 4) + q's error + 3 q) and half a step
+An exponential below binary32's normal numbers, 2^-126, is 0: 2^-126 of a share.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import ops_step_reference as ref
+from gpu_helpers import gpu_available
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+U = 2.0 ** -24
+HALF = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8}
+TINY = 1e-37
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+
+    torch.cuda.set_device(0)
+    return torch
+
+
+@pytest.fixture(scope="module")
+def ops(torch):
+    from copy_reduce_snac_amd import operators
+
+    return operators
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def error(arg):
+    return 2 + 2.5 * np.abs(arg)
+
+
+def inputs(torch, dtype, seed, tokens=16, vocab=700, topk=9):
+    """Logits with ties at the top in some rows, padding and masked ones."""
+    g = np.random.default_rng(seed)
+    z, t = g.normal(size=(tokens, vocab)), 2.0 + 2 * g.normal(size=(tokens, topk))
+    ids = np.argsort(g.random((tokens, vocab)), axis=1)[:, :topk].astype(np.int64)
+    for r in range(tokens):
+        z[r, ids[r]] = t[r] + 0.5 * g.normal(size=topk)
+    z[1, [3, 400]] = z[1].max() + 1   # two largest logits
+    t[2, [0, 5]] = t[2].max() + 1     # two largest of the teacher
+    ids[3], ids[4, 0], t[5, 1] = -1, vocab, -np.inf
+    z[6, 50:60] = np.where(np.isin(np.arange(50, 60), ids[6]), z[6, 50:60], -np.inf)
+    z = torch.from_numpy(z.astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    return z, torch.from_numpy(ids).cuda(), torch.from_numpy(t.astype(np.float32)).cuda()
+
+
+def bounds(z, ids, t, tau, loss):
+    """Bounds of loss and S and, for the gradient, the teacher's part."""
+    q, logq, ok = ref.choices(ids, t, z.shape[1], tau)
+    r = error(np.where(q > 0, logq - logq.max(axis=1, keepdims=True, where=ok, initial=-1e30), 0.0))
+    rel = (q * r).sum(axis=1, keepdims=True)
+    m = z.max(axis=1, keepdims=True)
+    with np.errstate(all="ignore"):
+        arg = np.where(z == -np.inf, 0.0, (z - m) / tau)
+        e = np.where(z == -np.inf, 0.0, np.exp(arg))
+        s = e.sum(axis=1, keepdims=True)
+        s_rel = (e * error(arg)).sum(axis=1, keepdims=True) / s + 8
+        logp = np.take_along_axis((z - m) / tau - np.log(s), np.where(ok, ids, 0), axis=1)
+        gap = np.where(q > 0, np.abs(logq - logp), 0.0)
+    q_off = q * (r + rel + 2)
+    return U * ((q_off * (gap + 1)).sum(axis=1) + s_rel[:, 0] + rel[:, 0] + np.abs(loss)) + TINY, U * (s_rel[:, 0] + 1) * s[:, 0], q, q_off, ok
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("tau", [2.0 ** -64, 2.0 ** -30, 1e-4, 0.01, 30.0, 2.0 ** 30, 2.0 ** 64])
+def test_values(torch, ops, tau, dtype):
+    z, ids, t = inputs(torch, dtype, 5)
+    tokens, vocab = z.shape
+    loss, stats, dz = torch.empty(tokens, device="cuda"), torch.empty(tokens, 2, device="cuda"), torch.empty_like(z)
+    ops.distill(z, ids, t, loss, stats, temperature=tau)
+    ops.distill_backward(z, ids, t, stats, dz, temperature=tau, scale=tau)
+    tau32 = float(np.float32(tau))
+    hz, hi, ht = host(z), ids.cpu().numpy(), host(t)
+    want, m, s = ref.distill(hz, hi, ht, tau32)
+    off, s_off, q, q_off, ok = bounds(hz, hi, ht, tau32, want)
+    assert np.array_equal(host(stats[:, 0]), m)
+    assert (np.abs(host(stats[:, 1]) - s) <= s_off).all()
+    assert (np.abs(host(loss) - want) <= off).all(), (host(loss), want)
+    if tau < 1e-3:  # what the loss is made of: the distance of the teacher's choice from the top
+        assert want.max() > 1000 and (host(stats[:, 1]) >= 1).all()
+
+    hs = host(stats)
+    back = ref.distill_backward(hz, hi, ht, tau32, hs, np.full(tokens, tau32))
+    with np.errstate(all="ignore"):
+        arg = np.where(np.isinf(hz), 0.0, (hz - hs[:, :1]) / tau32)
+        err = np.where(np.isinf(hz), 0.0, np.exp(arg) / hs[:, 1:]) * (error(arg) + 2)
+    for row in range(tokens):
+        np.add.at(err[row], hi[row][ok[row]], (q_off + 3 * q)[row][ok[row]])
+    assert (np.abs(host(dz) - back) <= U * err + (U + HALF[dtype]) * np.abs(back) + TINY).all()
+
+    # two shards, the first without row 1's largest logits' second
+    cut = 300
+    parts = torch.empty(2, tokens, 4, device="cuda")
+    ops.distill_shard(z[:, :cut], ids, t, parts[0], first=0, vocab=vocab, temperature=tau)
+    ops.distill_shard(z[:, cut:], ids, t, parts[1], first=cut, vocab=vocab, temperature=tau)
+    loss2, stats2, dz2 = torch.empty_like(loss), torch.empty_like(stats), torch.empty(tokens, vocab - cut, dtype=z.dtype, device="cuda")
+    ops.distill_join(parts, ids, t, loss2, stats2, vocab=vocab, temperature=tau)
+    assert torch.equal(stats2[:, 0], stats[:, 0])
+    assert (np.abs(host(stats2[:, 1]) - s) <= s_off + U * s).all()
+    at = np.where(ok, hi, 0)
+    sizes = np.zeros(tokens)
+    for a, b in ((0, cut), (cut, vocab)):
+        here = ok & (hi >= a) & (hi < b)
+        ms = hz[:, a:b].max(axis=1)
+        gap = np.where(here & (q > 0), np.abs(np.take_along_axis(hz, at, axis=1) - ms[:, None]) / tau32, 0.0)
+        sizes += (q * gap).sum(axis=1) + (q * here).sum(axis=1) * np.abs(ms - m) / tau32
+    assert (np.abs(host(loss2) - want) <= off + U * (sizes + 2)).all(), (host(loss2), want)
+    ops.distill_backward(z[:, cut:], ids, t, stats, dz2, temperature=tau, scale=tau, first=cut, vocab=vocab)
+    assert torch.equal(dz2, dz[:, cut:])
