@@ -348,7 +348,14 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
-// x + the x of the lane's partner at distance D
+// x + the x of the lane's partner at distance D (both types here: an overload in an
+// inner namespace would hide the other and take its arguments)
+template <int D>
+__device__ __forceinline__ float exchange_sum(float x) {
+  return __uint_as_float(exchange<D>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
 template <int D>
 __device__ __forceinline__ double exchange_sum(double x) {
   const uint64_t b = (uint64_t)__double_as_longlong(x);

@@ -109,3 +109,26 @@ def test_many_tokens_on_a_default_context(torch, ops, handle, dtype, width, toke
         one = torch.empty_like(dx[:1])
         ops.layer_norm_backward(dout[t:t + 1], x[t:t + 1], None, stats[t:t + 1], one, None, None, handle)
         assert torch.equal(one[0], dx[t]), t
+
+
+# rows that 2, 4, 8 and 16 waves hold, and one that a workgroup reads several times
+@pytest.mark.parametrize("dtype,width", [("f32", 1024), ("f32", 2048), ("f32", 4096), ("f32", 8192), ("f32", 16384), ("bf16", 2048),
+                                         ("bf16", 4096), ("bf16", 8192), ("bf16", 16384), ("bf16", 32768)])
+def test_a_rows_sums_over_its_waves(torch, ops, handle, dtype, width):
+    """A row's sums are binary64 over its units, those of different waves as well: 2^30 in one unit, ones in the others and
+    -2^30 in a unit of the last wave have their exact sum.  h is 0 and 1 / deviation 1, so dx is dout less its mean,
+    exact in binary32 where dout is 1."""
+    n = 16 // (4 if dtype == "f32" else 2)  # a unit's elements
+    dout = torch.ones(6, width, device="cuda")
+    for r, (a, b) in enumerate([(0, width // n - 1), (3, width // n - 2), (width // n // 2, width // n - 5)]):
+        for row, first in ((r, 2.0 ** 30), (r + 3, -2.0 ** 30)):
+            dout[row, a * n:(a + 1) * n] = 0
+            dout[row, b * n:(b + 1) * n] = 0
+            dout[row, a * n], dout[row, b * n] = first, -first
+    dout = dout.to(getattr(torch, DT[dtype]))
+    x, stats = torch.full_like(dout, 3.0), torch.tensor([3.0, 1.0], device="cuda").repeat(6, 1)
+    dx = torch.empty_like(dout)
+    ops.layer_norm_backward(dout, x, None, stats, dx, None, None, handle)
+    g = dout.double()
+    want = (g - g.mean(dim=1, keepdim=True)).float().to(dout.dtype)
+    assert torch.equal(dx, want), (dx.float()[:, 100], want.float()[:, 100])
