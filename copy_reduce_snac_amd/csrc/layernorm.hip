@@ -505,7 +505,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
   for (int j = 0; j < U; ++j)
 #pragma unroll
     for (uint32_t c = 0; c < N; ++c) dw[j][c] = db[j][c] = 0.0f;
-  const float inv = (float)(1.0 / (double)a.width);
+  const double inv = 1.0 / (double)a.width;
   const bool lines = whole_lines(a.x, a.ld_x) && whole_lines(a.dout, a.ld_dout);
   // kGradBlocks workgroups go at once, the rows of their same turn side by side; as many
   // again take the rows after theirs
@@ -578,7 +578,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
       }
     }
     row_sum<L, W>(c1, c2, lds[turn]);
-    const float m1 = (float)c1 * inv, m2 = (float)c2 * inv;
+    const float m1 = (float)(c1 * inv), m2 = (float)(c2 * inv);
     u32x4 v[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {

@@ -1,5 +1,5 @@
-"""Layer norm's gradient of rows whose mean times 1 / deviation passes binary32's
-range: lanes without an element of the row have no part in its sums.
+"""Layer norm's gradient of rows whose mean times 1 / deviation or whose sums pass
+binary32's range, and rows that do not vary, or hardly.
 
 Bounds as in test_gpu_ops_layer_norm.py (u = 2^-24, h = (x - mean) rstd):
   dx      u rstd (4 |g| + 14 mean|g| + 20 |h| mean|g h|) + half |dx|
@@ -111,3 +111,24 @@ def test_rows_that_hardly_vary(torch, ops, width):
     assert (np.abs(host(out) - h) <= U * (12 * np.abs(h) + 8) + TINY).all(), (np.abs(host(out) - h) / (U * (12 * np.abs(h) + 8))).max()
     assert (np.abs(host(stats[:, :1]) - mean) <= U * np.abs(mean) + 8 * U / rstd).all()
     assert (np.abs(host(stats[:, 1:]) - rstd) <= 8 * U * rstd).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [5000, 5003, 8192, 9000, 16001, 20001])
+def test_gradient_of_large_gradients(torch, ops, handle, dtype, width):
+    """Sums of a row that pass binary32's range, of terms and with means far below it."""
+    rows = 20
+    g = np.random.default_rng(width)
+    x = torch.from_numpy(g.normal(size=(rows, width)).astype(np.float32)).to(getattr(torch, DT[dtype])).cuda()
+    stats = torch.from_numpy(np.concatenate(ref.moments(host(x), 1e-5), axis=1).astype(np.float32)).cuda()
+    dout = torch.full_like(x, 2.0 ** 116)  # sum g passes it
+    dout[::2] = dout[::2] * torch.where(x[::2] > 0, 1.0, -1.0)  # sum g h does, sum g does not
+    dx = torch.empty_like(x)
+    ops.layer_norm_backward(dout, x, None, stats, dx, None, None, handle)
+    hx, hg, hs = host(x), host(dout), host(stats)
+    want, _, _ = ref.layer_norm_backward(hg, hx, None, hs)
+    h = (hx - hs[:, :1]) * hs[:, 1:]
+    mg, mgh = np.abs(hg).mean(axis=1, keepdims=True), np.abs(hg * h).mean(axis=1, keepdims=True)
+    bound = U * hs[:, 1:] * (4 * np.abs(hg) + 14 * mg + 20 * np.abs(h) * mgh) + HALF[dtype] * np.abs(want)
+    got = host(dx)
+    assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all()
