@@ -336,6 +336,10 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Balanc
   s = wave_sum(s);
   const double scale = c == 0.0 || s == 0.0 ? 0.0
                                             : (a.dloss ? (double)a.dloss[0] : 1.0) * (double)a.coefficient * (double)r.E / (c * s);
+  // A scale that binary32 holds not at all, or with few bits, is taken by a power of two
+  // that the products get back.
+  const int power = scale != 0.0 && isfinite(scale) && !(fabs(scale) > 0x1p-60 && fabs(scale) < 0x1p60) ? ilogb(scale) : 0;
+  const double scale_f = ldexp(scale, -power);
   for (uint64_t t0 = t - sub; t0 < a.tokens; t0 += step, t += step) {
     float x[V], far[V];
     r.take(next, -inf, x);
@@ -352,11 +356,15 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Balanc
 #pragma unroll
     for (int j = 0; j < V; ++j) dot[j % 4] = __builtin_fmaf(x[j], count[j] - best, dot[j % 4]);
     const float mean = (float)((double)lanes_sum<L>((dot[0] + dot[1]) + (dot[2] + dot[3])) * inv);
-    const float f = (float)(inv * scale);
+    const float f = (float)(inv * scale_f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       x[j] = x[j] * f * ((count[j] - best) - mean);
       if (!softmax) x[j] = x[j] * far[j];
+    }
+    if (power != 0) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = ldexpf(x[j], power);
     }
     char* out = static_cast<char*>(a.dlogits) + (t < a.tokens ? t : a.tokens - 1) * a.ld_d * T::kSize;
     if (a.accumulate) {
