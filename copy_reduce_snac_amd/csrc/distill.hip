@@ -290,7 +290,10 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
     };
     if (p0 + w < p1) load(p0 + w);
     const float top = a.stats[2 * t], total = a.stats[2 * t + 1];
-    const float factor = (float)((double)a.scale / (double)a.teacher.temperature * (a.dloss ? (double)a.dloss[t] : 1.0));
+    const double whole = (double)a.scale / (double)a.teacher.temperature * (a.dloss ? (double)a.dloss[t] : 1.0);
+    // beyond binary32 by a power of two that the differences get back
+    const int power = (int)uniform(fabs(whole) >= 0x1p126 && isfinite(whole) ? (uint32_t)ilogb(whole) : 0u);
+    const float factor = (float)ldexp(whole, -power);
     const float f0 = (float)((double)factor / (double)total);
     if (w == 0) {
       Choices<C> k;
@@ -346,6 +349,16 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
       u32x4 v[kBackUnits];
 #pragma unroll
       for (int j = 0; j < kBackUnits; ++j) v[j] = part ? pack<T>(f[j]) : u32x4{0, 0, 0, 0};
+      if (power != 0) {  // exact, also after the rounding; before it it costs 20 registers
+#pragma unroll
+        for (int j = 0; j < kBackUnits; ++j) {
+          float g[N];
+          unpack<T>(v[j], g);
+#pragma unroll
+          for (uint32_t c = 0; c < N; ++c) g[c] = ldexpf(g[c], power);
+          v[j] = pack<T>(g);
+        }
+      }
       st_held<T, kBackUnits, true, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
     }
     if (items - it > gridDim.x) __syncthreads();  // the choices are read

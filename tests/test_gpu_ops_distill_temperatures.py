@@ -128,3 +128,44 @@ def test_values(torch, ops, tau, dtype):
     assert (np.abs(host(loss2) - want) <= off + U * (sizes + 2)).all(), (host(loss2), want)
     ops.distill_backward(z[:, cut:], ids, t, stats, dz2, temperature=tau, scale=tau, first=cut, vocab=vocab)
     assert torch.equal(dz2, dz[:, cut:])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("up,tau", [(2.0 ** 100, 2.0 ** -40), (-2.0 ** 127, 2.0 ** -10), (2.0 ** 120, 2.0 ** -64)])
+def test_factors_beyond_binary32(torch, ops, up, tau, dtype):
+    """dloss * scale / temperature is, the gradient of shares far below 1 is not: masked columns have gradient 0, and one
+    whose share and choice are nearly the same has their difference."""
+    tokens, vocab = 12, 600
+    g = np.random.default_rng(3)
+    # distances from the top in units of the temperature, exact in both types
+    z = -(40 + np.floor(g.uniform(0, 60, (tokens, vocab)))) * tau
+    z[:, 7], z[:, 11], z[:, 599] = 0.0, -np.inf, -np.inf
+    ids = np.tile(np.array([[7, 20, 300]]), (tokens, 1))
+    t = np.tile(np.array([[0.0, -45.0, -64.0]]) * tau, (tokens, 1))
+    ids[3] = -1
+    logits = torch.from_numpy(z.astype(np.float32)).to(getattr(torch, dtype)).cuda()
+    teacher = torch.from_numpy(t.astype(np.float32)).cuda()
+    hi = torch.from_numpy(ids).cuda()
+    loss, stats, dz = torch.empty(tokens, device="cuda"), torch.empty(tokens, 2, device="cuda"), torch.empty_like(logits)
+    ops.distill(logits, hi, teacher, loss, stats, temperature=tau)
+    dloss = torch.full((tokens,), up, device="cuda")
+    ops.distill_backward(logits, hi, teacher, stats, dz, dloss=dloss, scale=0.75, temperature=tau)
+    got, hz, hs = host(dz), host(logits), host(stats)
+    want = ref.distill_backward(hz, ids, host(teacher), tau, hs, np.full(tokens, up * 0.75))
+    assert (got[:, [11, 599]] == 0).all() and (got[3] == 0).all() and not np.isnan(got).any()
+    with np.errstate(all="ignore"):
+        arg = np.where(np.isinf(hz), 0.0, (hz - hs[:, :1]) / tau)
+        err = np.where(np.isinf(hz), 0.0, np.exp(arg) / hs[:, 1:]) * (error(arg) + 4)
+    q, logq, ok = ref.choices(ids, host(teacher), vocab, tau)
+    r = error(np.where(q > 0, logq, 0.0))
+    for row in range(tokens):
+        np.add.at(err[row], ids[row][ok[row]], (q * (r + (q * r).sum(axis=1, keepdims=True) + 5))[row][ok[row]])
+    # exp(-88) is below 2^-126 and taken as 0 (the head of this file): off by the whole of such a share, p < 2^-126,
+    # times the factor, 2^-126 * 2^139.6 = 1.2e4 where the other terms are 0.1
+    err = (U * err + 2.0 ** -126) * abs(up) * 0.75 / tau + (U + HALF[dtype]) * np.abs(want)
+    largest = float(torch.finfo(getattr(torch, dtype)).max)
+    inside = np.abs(want) + err < largest
+    assert inside[:, 20:].any()
+    assert (np.abs(got - want)[inside] <= err[inside]).all()
+    over = np.abs(want) - err > largest
+    assert np.isinf(got[over]).all() and (np.sign(got[over]) == np.sign(want[over])).all()
