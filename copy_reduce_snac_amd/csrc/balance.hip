@@ -13,8 +13,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504f;
 
-// 1 / x for a normal binary64 x, off by a few of its last bits: the hardware's
-// estimate (2^-24 or better) and one step of Newton's iteration.
+// 1 / x for a normal binary64 x: the hardware's estimate (2^-24 or better) and one step
+// of Newton's iteration, which leaves its square, 2^-48.
 __device__ __forceinline__ double reciprocal(double x) {
   const double r = __builtin_amdgcn_rcp(x);
   return r * __builtin_fma(-x, r, 2.0);

@@ -148,8 +148,8 @@ __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(con
     u32x4 next[kUnits] = {};
     auto load = [&](uint32_t p) {
       const char* at = row + (uint64_t)p * kPiece * T::kSize;
-      if (lines) ld_held<T, kUnits, true, true>(at, a.width - p * kPiece, a.width, next);
-      else ld_held<T, kUnits, false, true>(at, a.width - p * kPiece, a.width, next);
+      if (lines) ld_held<T, kUnits, true>(at, a.width - p * kPiece, a.width, next);
+      else ld_held<T, kUnits, false>(at, a.width - p * kPiece, a.width, next);
     };
     if (w < pieces) load(w);
     Choices<C> k;
@@ -285,8 +285,8 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
     u32x4 next[kBackUnits];
     auto load = [&](uint32_t p) {
       const char* at = row + (uint64_t)p * kPiece * T::kSize;
-      if (lines) ld_held<T, kBackUnits, true, true>(at, a.width - p * kPiece, a.width, next);
-      else ld_held<T, kBackUnits, false, true>(at, a.width - p * kPiece, a.width, next);
+      if (lines) ld_held<T, kBackUnits, true>(at, a.width - p * kPiece, a.width, next);
+      else ld_held<T, kBackUnits, false>(at, a.width - p * kPiece, a.width, next);
     };
     if (p0 + w < p1) load(p0 + w);
     const float top = a.stats[2 * t], total = a.stats[2 * t + 1];
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
           v[j] = pack<T>(g);
         }
       }
-      st_held<T, kBackUnits, true, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
+      st_held<T, kBackUnits, true>(out + (uint64_t)p * kPiece * T::kSize, left, v);
     }
     if (items - it > gridDim.x) __syncthreads();  // the choices are read
   }

@@ -111,8 +111,8 @@ __device__ __forceinline__ float row_sum(float a, float* lds) {
   return a;
 }
 
-// 1 / sqrt(v), off by a few of binary64's last bits: the hardware's estimate
-// (2^-23 or better) and one step of Newton's iteration.
+// 1 / sqrt(v) rounded to binary32: the hardware's estimate (2^-23 or better) and one
+// step of Newton's iteration, which leaves 1.5 times its square, 2^-45.
 __device__ __forceinline__ float inverse_root(double v) {
   const double r = __builtin_amdgcn_rsq(v);
   return (float)(v > 0.0 && v < HUGE_VAL ? r * __builtin_fma(-0.5 * v * r, r, 1.5) : r);

@@ -190,13 +190,12 @@ __device__ __forceinline__ void st_rest(char* p, u32x4 v, uint32_t n) {
 // the caches; of others two share a line, and each would fetch it.
 __device__ __forceinline__ bool whole_lines(const char* p, uint64_t ld) { return (((uint64_t)(uintptr_t)p | ld) & 127) == 0; }
 
-// Pieces that are often not whole (a row held in registers, every row's last
-// one), of rows of `width` elements; `left` is the same in all lanes.  REST: rows
-// may end in a part of a unit.  It is loaded with the others, as the 16 bytes that
-// end where the row does, and settle_held brings its elements to their places when
-// they are there: what waits for them before, waits for every load in flight
-// (layer norm's gradients of 8192 rows of 5003 bf16 92 us, 74 this way).
-template <typename T, int U, bool NT, bool REST>
+// Pieces of rows of `width` elements, of which the last may end in a part of a unit;
+// `left` is the same in all lanes.  The part is loaded with the others, as the 16
+// bytes that end where the row does, and settle_held brings its elements to their
+// places when they are unpacked: what waits for them before, waits for every load in
+// flight.
+template <typename T, int U, bool NT>
 __device__ __forceinline__ void ld_held(const char* piece, uint32_t left, uint32_t width, u32x4 (&v)[U]) {
   constexpr uint32_t N = kUnit<T>;
   const uint32_t lane = threadIdx.x & 63u;
@@ -205,7 +204,7 @@ __device__ __forceinline__ void ld_held(const char* piece, uint32_t left, uint32
     for (int j = 0; j < U; ++j) v[j] = ld_unit<NT>(piece + (j * 64u + lane) * 16u);
     return;
   }
-  const uint32_t units = left / N, rest = REST ? left % N : 0;
+  const uint32_t units = left / N, rest = left % N;
   if (rest == 0 || width < N) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
@@ -224,24 +223,8 @@ __device__ __forceinline__ void ld_held(const char* piece, uint32_t left, uint32
   }
 }
 
-// Elements first, first + 1 .. of a unit as its elements 0, 1 .., zeros after them;
-// `first` (1 .. its number of elements - 1) is the same in all lanes.
-template <typename T>
-__device__ __forceinline__ u32x4 later_elems(u32x4 v, uint32_t first) {
-  const uint32_t words = first * T::kSize / 4;
-  u32x4 r = v;
-#pragma unroll
-  for (uint32_t q = 1; q < 4; ++q)
-    if (words == q) {
-#pragma unroll
-      for (uint32_t c = 0; c < 4; ++c) r[c] = c + q < 4 ? v[(c + q) & 3] : 0u;
-    }
-  if (T::kSize == 2 && (first & 1)) {
-#pragma unroll
-    for (uint32_t c = 0; c < 4; ++c) r[c] = r[c] >> 16 | (c < 3 ? r[(c + 1) & 3] << 16 : 0u);
-  }
-  return r;
-}
+// Elements first, first + 1 .. of a unit as its elements 0, 1 .., zeros after them,
+// where `mine`; `first` (1 .. its number of elements - 1) is the same in all lanes.
 template <uint32_t N>
 __device__ __forceinline__ void later_elems(float (&f)[N], uint32_t first, bool mine) {
 #pragma unroll
@@ -252,19 +235,6 @@ __device__ __forceinline__ void later_elems(float (&f)[N], uint32_t first, bool 
   }
 }
 
-// Of the units as they were loaded, or as they are unpacked.
-template <typename T, int U>
-__device__ __forceinline__ void settle_held(uint32_t left, uint32_t width, u32x4 (&v)[U]) {
-  constexpr uint32_t N = kUnit<T>;
-  const uint32_t units = left / N, rest = left % N;
-  if (rest == 0 || units >= 64u * U || width < N) return;
-#pragma unroll
-  for (uint32_t j = 0; j < U; ++j) {
-    if (units / 64 != j) continue;
-    const u32x4 r = later_elems<T>(v[j], N - rest);
-    if ((threadIdx.x & 63u) == units % 64) v[j] = r;
-  }
-}
 template <typename T, int U>
 __device__ __forceinline__ void settle_held(uint32_t left, uint32_t width, float (&f)[U][kUnit<T>]) {
   constexpr uint32_t N = kUnit<T>;
@@ -275,7 +245,7 @@ __device__ __forceinline__ void settle_held(uint32_t left, uint32_t width, float
     if (units / 64 == j) later_elems<N>(f[j], N - rest, (threadIdx.x & 63u) == units % 64);
 }
 
-template <typename T, int U, bool NT, bool REST>
+template <typename T, int U, bool NT>
 __device__ __forceinline__ void st_held(char* row, uint32_t left, const u32x4 (&v)[U]) {
   const uint32_t lane = threadIdx.x & 63u;
   if (whole_piece<T, U>(left)) {
@@ -283,7 +253,7 @@ __device__ __forceinline__ void st_held(char* row, uint32_t left, const u32x4 (&
     for (int j = 0; j < U; ++j) st_unit<NT>(row + (j * 64u + lane) * 16u, v[j]);
     return;
   }
-  const uint32_t units = left / kUnit<T>, rest = REST ? left % kUnit<T> : 0;
+  const uint32_t units = left / kUnit<T>, rest = left % kUnit<T>;
 #pragma unroll
   for (int j = 0; j < U; ++j)
     if (j * 64u + lane < units) st_unit<NT>(row + (j * 64u + lane) * 16u, v[j]);
