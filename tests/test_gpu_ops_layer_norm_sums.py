@@ -132,3 +132,45 @@ def test_a_rows_sums_over_its_waves(torch, ops, handle, dtype, width):
     g = dout.double()
     want = (g - g.mean(dim=1, keepdim=True)).float().to(dout.dtype)
     assert torch.equal(dx, want), (dx.float()[:, 100], want.float()[:, 100])
+
+
+def test_several_launches_in_a_graph(torch, ops, handle):
+    """Two launches and their joins, captured and replayed with other inputs, eager calls of the same scratch between."""
+    tokens, width = 8300, 16384
+    g = torch.Generator(device="cuda")
+    x, dout = (torch.empty(tokens, width, dtype=torch.bfloat16, device="cuda") for _ in "xd")
+    stats = torch.tensor([0.0, 1.0], device="cuda").repeat(tokens, 1)
+    dx, dw, db = torch.empty_like(x), torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+
+    def fill(seed):
+        g.manual_seed(seed)
+        x.normal_(generator=g)
+        dout.normal_(generator=g)
+
+    def run():
+        ops.layer_norm_backward(dout, x, None, stats, dx, dw, db, handle)
+
+    wants = {}
+    for seed in (1, 2, 3):
+        fill(seed)
+        run()
+        torch.cuda.synchronize()
+        wants[seed] = [t.clone() for t in (dx, dw, db)]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (1, 2, 3, 2):
+        small = torch.empty(width, device="cuda")  # another call of the scratch, a sum of few rows
+        ops.layer_norm_backward(dout[:700], x[:700], None, stats[:700], dx[:700], small, None, handle)
+        fill(seed)
+        for t in (dx, dw, db):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want, name in zip((dx, dw, db), wants[seed], ("dx", "dw", "db")):
+            assert torch.equal(got, want), (seed, name)
