@@ -164,9 +164,12 @@ constexpr int kLoadWaves = kLoadThreads / 64;
 //
 // 32768 x 256 f32 sigmoid 11.2 us of kernel for 35 MB, of which the launch and the
 // first row's load take 5 and two turns of 4 tokens a wave the rest; longer ones are
-// bound by instructions, two transcendental ones a logit (131072 x 256: 29 us, 4.6
-// TB/s).  256 workgroups of 16 waves, so that the join has no more than 256 sums an
-// expert; a turn's logits are fetched during the turn before.
+// bound by instructions, of which a sigmoid's logit takes two transcendental ones and
+// four of binary64: two conversions, an addition to the row's sum and a fused product
+// to the expert's (131072 x 256: 29 us, 4.6 TB/s; 16384 x 1000 softmax, one
+// transcendental and those four, 18 us, 3.7).  256 workgroups of 16 waves, so that the
+// join has no more than 256 sums an expert; a turn's logits are fetched during the
+// turn before.
 template <typename T, int L, int V, bool UNITS>
 __global__ __launch_bounds__(kLoadThreads) void balance_load_kernel(const BalanceArgs a) {
   constexpr uint32_t TPW = 64 / L, kRows = kLoadWaves * TPW;

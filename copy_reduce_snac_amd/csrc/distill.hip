@@ -126,12 +126,13 @@ constexpr int kUnits = 4;  // of a lane at a time
 // wave, which has the fewest pieces, sees to the choices before it begins and
 // makes the loss of them in the end.
 //
-// Bound by HBM: 4096 x 131072 bf16 163 us, 6.6 TB/s read; 2048 x 131072 f32 157, 6.8;
-// 4096 x 50258 bf16, rows that begin off the 16 bytes, 77, 5.3, and of 50257, off the
-// 4 bytes, 89.  A unit's exponentials
-// are summed in binary32 and units in binary64; the maximum so far moves for a whole
-// wave at a time, which it seldom does.  7 x 32768 f32 takes 6.4 us, one workgroup of 16
-// waves a row.
+// Bound by HBM: 4096 x 131072 bf16 163 us, 6.6 TB/s read; 2048 x 131072 f32 157, 6.8.
+// Units are counted from a row's first element, so rows that begin off the 16 bytes
+// straddle with every access, and the lines that two accesses share are not read past
+// the caches: 4096 x 50258 bf16 77 us, 5.3, and of 50257, off the 4 bytes, 89.  A unit's
+// exponentials are summed in binary32 and units in binary64; the maximum so far moves
+// for a whole wave at a time, which it seldom does.  7 x 32768 f32 takes 6.5 us, one
+// workgroup of 16 waves a row.
 template <typename T, int W, int C>
 __global__ __launch_bounds__(W == 1 ? kThreads : 64 * W) void distill_kernel(const DistillArgs a) {
   constexpr uint32_t N = kUnit<T>, kPiece = 64u * kUnits * N;

@@ -260,11 +260,14 @@ constexpr int kNormWaves = 4;  // of a workgroup whose rows take up to 4 waves
 // go over a unit in binary32 and on in binary64.
 //
 // Bound by HBM: each element is read and written once.  A workgroup takes `per` rows
-// one after another, so that its parameters are loaded once for them.  TB/s read and
-// written: 32768 x 4096 bf16 84 us, 6.4; 16384 x 4096 f32 84 us, 6.4; 65536 x 1024
-// bf16 43 us, 6.3; 262144 x 128 bf16 (16 lanes a row; with 64, 3 of 4 of them idle)
+// one after another, so that its parameters are loaded once for them.  Calls in a row
+// (one kernel alone has its ramp and drain, 88 us of the first), TB/s read and
+// written: 32768 x 4096 bf16 83 us, 6.4; 16384 x 4096 f32 84 us, 6.4; 65536 x 1024
+// bf16 43 us, 6.2; 262144 x 128 bf16 (16 lanes a row; with 64, 3 of 4 of them idle)
 // 23 us, 5.9; 8192 x 16384 f32 194 us, 5.5: one workgroup a CU there, whose waves load
-// and store at the same times.  One row of 8192 takes 3.2 us, two joins of four
+// and store at the same times.  Rows that fill a part of a shape hold its waves and
+// registers all the same, with lanes idle: 20000 x 5999 bf16 (12 of 16 KiB) 98 to 101,
+// 4.8.  One row of 8192 takes 3.2 us, two joins of four
 // waves' sums through LDS after its load.
 template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * (W > kNormWaves ? W : kNormWaves)) void layer_norm_kernel(const LayerNormArgs a,
@@ -471,11 +474,14 @@ __device__ __forceinline__ void put_grad(void* grad, bool bf16, bool accumulate,
 // kGradPartial bytes of partial sums serve take several launches, each with a join
 // into the call's sums.
 //
-// Bound by HBM: two streams read, one written, 16384 x 4096 bf16 63 us, 6.5 TB/s
+// Bound by HBM: two streams read, one written, 16384 x 4096 bf16 65 us, 6.4 TB/s
 // (8192 x 8192 66), the join 4.  One workgroup of 16 waves a CU leaves the fewest
 // partial sums (8.4 MB there), and its waves' registers are what one CU has: the row
-// after this one is on its way meanwhile.  131072 x 128 bf16 21 us, 4.7 TB/s; 2049 x
-// 1030 f32 10.7 and the join 3.9, launches and ramps.
+// after this one is on its way while this one is worked on, but not before this one's
+// mean and rstd, loaded at the head of its turn, are there.  That wait in each turn,
+// and that turns are dealt out evenly (171 of 256 CUs have the 3 of 2049 rows), is
+// what few or short rows spend besides launch and ramp: 2049 x 1030 f32 11 us for 27
+// MB and the join 3.9; 131072 x 128 bf16 21 us, 4.7 TB/s.
 template <typename T, typename P, int L, int W, int U, bool REST>
 __global__ __launch_bounds__(64 * kGradWaves) void layer_norm_backward_kernel(
     const LayerNormBackwardArgs a, const uint32_t per) {
