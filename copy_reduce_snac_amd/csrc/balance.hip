@@ -340,8 +340,9 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Balanc
   const double scale = c == 0.0 || s == 0.0 ? 0.0
                                             : (a.dloss ? (double)a.dloss[0] : 1.0) * (double)a.coefficient * (double)r.E / (c * s);
   // A scale that binary32 holds not at all, or with few bits, is taken by a power of two
-  // that the products get back.
-  const int power = scale != 0.0 && isfinite(scale) && !(fabs(scale) > 0x1p-60 && fabs(scale) < 0x1p60) ? ilogb(scale) : 0;
+  // that the products get back; 2^60 of it stays, for the smallest shares to be normal
+  // numbers with it.
+  const int power = scale != 0.0 && isfinite(scale) && !(fabs(scale) > 0x1p-60 && fabs(scale) < 0x1p60) ? ilogb(scale) - 60 : 0;
   const double scale_f = ldexp(scale, -power);
   for (uint64_t t0 = t - sub; t0 < a.tokens; t0 += step, t += step) {
     float x[V], far[V];

@@ -292,8 +292,9 @@ __global__ __launch_bounds__(64 * kBackWaves) void distill_backward_kernel(const
     if (p0 + w < p1) load(p0 + w);
     const float top = a.stats[2 * t], total = a.stats[2 * t + 1];
     const double whole = (double)a.scale / (double)a.teacher.temperature * (a.dloss ? (double)a.dloss[t] : 1.0);
-    // beyond binary32 by a power of two that the differences get back
-    const int power = (int)uniform(fabs(whole) >= 0x1p126 && isfinite(whole) ? (uint32_t)ilogb(whole) : 0u);
+    // beyond binary32 by a power of two that the differences get back; 2^100 of it stays,
+    // for the smallest shares to be normal numbers with it
+    const int power = (int)uniform(fabs(whole) >= 0x1p126 && isfinite(whole) ? (uint32_t)(ilogb(whole) - 100) : 0u);
     const float factor = (float)ldexp(whole, -power);
     const float f0 = (float)((double)factor / (double)total);
     if (w == 0) {

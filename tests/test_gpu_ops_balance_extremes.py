@@ -83,3 +83,22 @@ def test_far_factors(torch, ops, experts, score, size, dloss, accumulate):
     assert np.isinf(got[over]).all() and (np.sign(got[over]) == np.sign(want[over])).all()
     if size > 2:
         assert np.abs(want).max() > 1e-39 and inside.all()  # of the reference: 10^6 units of the smallest number
+
+
+def test_small_shares_with_a_large_factor(torch, ops):
+    """Shares of 2^-130 to 2^-136, whose scores are normal numbers, and a factor of 2^130: gradients to a few roundings."""
+    experts = 1000
+    x = np.zeros((5, experts), np.float32)
+    x[:, 3] = -np.arange(83, 88, dtype=np.float32)
+    load = np.ones((2, experts), np.float32)
+    load[0] = 1 + np.arange(experts) % 5
+    ids, dx = torch.zeros(5, 1, dtype=torch.int32, device="cuda"), torch.empty(5, experts, device="cuda")
+    dloss = np.float32(3e38)
+    ops.balance_backward(torch.from_numpy(x).cuda(), ids, torch.from_numpy(load).cuda(), dx, score="softmax", coefficient=1e4,
+                         dloss=torch.full((1,), float(dloss), device="cuda"))
+    want = ref.balance_backward(x, np.zeros((5, 1), np.int64), load, "softmax", float(np.float32(1e4)), float(dloss))[:, 3]
+    # the share's (2 + 2.5 |x|) u and 2 u of the row's sum; the mean of the differences, up to 4, 16 u of it, of a slope of
+    # 1 after it; 5 roundings
+    err = U * np.abs(want) * (2 + 2.5 * np.abs(x[:, 3]) + 2 + 16 * 4 + 5)
+    got = host(dx)[:, 3]
+    assert (want != 0).all() and (np.abs(got - want) <= err).all(), (got, want)

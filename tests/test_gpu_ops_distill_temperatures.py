@@ -169,3 +169,18 @@ def test_factors_beyond_binary32(torch, ops, up, tau, dtype):
     assert (np.abs(got - want)[inside] <= err[inside]).all()
     over = np.abs(want) - err > largest
     assert np.isinf(got[over]).all() and (np.sign(got[over]) == np.sign(want[over])).all()
+
+
+def test_small_shares_with_a_large_factor(torch, ops):
+    """Shares of 2^-120 to 2^-142, whose exponentials are normal numbers, and a factor of 2^140: each gradient to its
+    relative bound."""
+    vocab, n = 131072, 16
+    z = torch.zeros(3, vocab, device="cuda")
+    z[:, :n] = -torch.arange(72.0, 72.0 + n, device="cuda")
+    ids, t = torch.full((3, 1), vocab - 1, device="cuda"), torch.zeros(3, 1, device="cuda")
+    loss, stats, dz = torch.empty(3, device="cuda"), torch.empty(3, 2, device="cuda"), torch.empty_like(z)
+    ops.distill(z, ids, t, loss, stats)
+    ops.distill_backward(z, ids, t, stats, dz, dloss=torch.full((3,), 2.0 ** 100, device="cuda"), scale=2.0 ** 40)
+    hz, hs = host(z)[:, :n], host(stats)
+    want = np.exp(hz - hs[:, :1]) / hs[:, 1:] * 2.0 ** 140
+    assert (np.abs(host(dz)[:, :n] - want) <= U * (error(hz) + 4) * want).all()
